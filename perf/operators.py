@@ -189,8 +189,6 @@ def prepare(case, seed):
         st["kept"] = torch.empty(R, dtype=torch.int32, device=_DEV)
         if own:
             import speculative_decoding_medusa_b200 as M
-            st["ws"] = M.workspace(M.medusa_sample_tokens_workspace_size(
-                R, V, M.MEDUSA_BF16 if dt == torch.bfloat16 else M.MEDUSA_F32))
             st["status"] = M.new_status()
         return st
 
@@ -386,7 +384,7 @@ def run(state):
         M.medusa_sample_tokens(st["logits"], st["u"], st["tokens"],
                                temperature=st["temperature"], top_k=st["top_k"],
                                top_p=st["top_p"], min_p=st["min_p"], kept=st["kept"],
-                               ws=st["ws"], dev_status=st["status"])
+                               dev_status=st["status"])
         return st["tokens"], st["kept"]
     if op == "rope":
         return (_rotate(case, st["q"], st["positions"], case["inverse"]),
