@@ -21,7 +21,9 @@
  * (the sparse tree of the most accurate combinations, host only), the
  * vocabulary-sharding calls (medusa_topk_merge, medusa_verify_records,
  * medusa_verify_from_records), medusa_verify_accept_noalloc and
- * medusa_wait_flag (a check of the bounded device waits).
+ * medusa_wait_flag (a check of the bounded device waits).  Before them, the
+ * prompt side: medusa_rope, medusa_rope_append, medusa_chunk_attention and
+ * medusa_sample_tokens (with medusa_rope_freqs on the host).
  *
  * Sources (page title, then section):
  *   "Medusa Heads" glossary - "Comment les têtes prédisent les tokens
@@ -574,6 +576,219 @@ MEDUSA_API medusa_status_t medusa_tree_from_accuracies(const float* acc, int n_h
                                                        int32_t* parent, int32_t* depth,
                                                        int32_t* rank,
                                                        double* expected_accept_len);
+
+/* ------------------------------------------------------------------------
+ * Prompt side of the step: rotary positions, a paged key/value cache, the
+ * attention of a chunk of new tokens over it, and tokens sampled from
+ * filtered logits.
+ *
+ * No counterpart on the pages.  The decode step takes q and k "as already
+ * positioned", a cache that holds the prompt, and a root token; these calls
+ * produce them: a chunk of the prompt is rotated and written into the cache
+ * (medusa_rope_append), attends to everything before it
+ * (medusa_chunk_attention), and the logits of its last token give the first
+ * root (medusa_sample_tokens).  medusa_rope positions the tree's q and k_new
+ * at the pos_ids of medusa_tree_build.
+ *
+ * Row strides ("*_stride") count elements between consecutive tokens; the
+ * heads and elements of one token are dense.  They let q, k and v be slices
+ * of one packed projection.
+ * ---------------------------------------------------------------------- */
+
+typedef enum {
+  MEDUSA_ROPE_NONE = 0,   /* f_i = theta^(-2i / rot)                              */
+  MEDUSA_ROPE_LINEAR = 1, /* f_i / factor (positions divided by factor)           */
+  MEDUSA_ROPE_LLAMA3 = 2, /* f_i divided by factor below low_turns turns over the */
+                          /* original length, kept above high_turns, a linear     */
+                          /* blend in the number of turns between                 */
+  MEDUSA_ROPE_YARN = 3    /* the same two ends, blended linearly in the index i   */
+                          /* between the indices of high_turns and low_turns      */
+                          /* (rounded outwards); rotated elements gain the factor */
+                          /* 0.1 ln(factor) + 1                                   */
+} medusa_rope_scaling_t;
+
+/*
+ * A rotation.  The first rot elements of each head are rotated in rot / 2
+ * pairs, the rest pass through: pair i is (i, i + rot/2), or (2i, 2i + 1)
+ * when interleaved.  turns[i] (DEVICE array of rot/2) is the pair's frequency
+ * in full turns per position, as a fraction of 2^64; the angle of position p
+ * is the wrapping 64-bit product p * turns[i], so it keeps its precision at
+ * any position (also negative ones).  Rotated elements are multiplied by
+ * scale.
+ */
+typedef struct medusa_rope {
+  int32_t rot;
+  int32_t interleaved;
+  float scale;
+  const uint64_t* turns;
+} medusa_rope_t;
+
+/*
+ * A paged cache.  Slot s of sequence b is row s % page_size of page
+ * table[b * max_pages + s / page_size] (DEVICE array, int32); K and V are
+ * pools [n_pages, Hkv, page_size, dh].  The dense cache [B, Hkv, cap, dh] of
+ * the other calls is the pool with n_pages = B, page_size = cap, max_pages = 1
+ * and table[b] = b.  Table entries past a sequence's last page are not read.
+ */
+typedef struct medusa_pages {
+  void* K;
+  void* V;
+  const int32_t* table;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t max_pages;
+} medusa_pages_t;
+
+/* medusa_rope_freqs (host only): the turns array (host, [rot/2]) and scale of
+ * a medusa_rope_t.  f_i = theta^(-2i / rot) for i = 0..rot/2-1 in extended
+ * precision, then the scaling; turns[i] = round(f_i / (2 pi) * 2^64).
+ * low_turns, high_turns and original_max_position are read by LLAMA3 and YARN
+ * only, factor by all but NONE.
+ * Errors: MEDUSA_ERR_SHAPE for rot odd or outside [2, 512];
+ *   MEDUSA_ERR_INVALID_ARG unless theta > 1, factor >= 1,
+ *   0 < low_turns < high_turns and original_max_position > 0 (where read). */
+MEDUSA_API medusa_status_t medusa_rope_freqs(int rot, double theta,
+                                             medusa_rope_scaling_t scaling, double factor,
+                                             double low_turns, double high_turns,
+                                             double original_max_position, uint64_t* turns,
+                                             float* scale);
+
+/* ------------------------------------------------------------------------
+ * medusa_rope
+ *
+ *   y0 = scale * (x0 cos a - x1 sin a),  y1 = scale * (x0 sin a + x1 cos a)
+ *   for every pair (x0, x1) of the first rot elements of a head, with
+ *   a = 2 pi * positions[t] * turns[i] / 2^64 (inverse = 0) or its negative
+ *   (inverse = 1: the transpose, i.e. the gradient of the forward call).
+ *
+ * Inputs (device, dtype dt): q [T, Hq, dh] and k [T, Hkv, dh], tokens
+ *   q_stride / k_stride elements apart (k NULL: q alone, Hkv ignored);
+ *   positions [T] int32, any value.
+ * Outputs (device, dtype dt): q_out, k_out, tokens q_out_stride /
+ *   k_out_stride apart.  An output may be its input (in place, same stride);
+ *   otherwise outputs overlap no input.
+ * Precision: angles to 2^-33 turns, products in fp32, one rounding.
+ * Limits: T >= 0 (nothing is launched for 0); rot <= dh <= 1024;
+ *   Hq, Hkv >= 1; strides >= heads * dh.  No alignment beyond the type's own.
+ * ---------------------------------------------------------------------- */
+MEDUSA_API medusa_status_t medusa_rope(const medusa_rope_t* rope, const void* q,
+                                       long long q_stride, const void* k, long long k_stride,
+                                       medusa_dtype_t dt, const int32_t* positions, int T, int Hq,
+                                       int Hkv, int dh, int inverse, void* q_out,
+                                       long long q_out_stride, void* k_out,
+                                       long long k_out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * medusa_rope_append
+ *
+ * The new tokens of B sequences, rotated and written into the cache in one
+ * launch.  Sequence b's rows are cu_q[b] .. cu_q[b+1]-1; its i-th row goes to
+ * slot kv_len[b] - (cu_q[b+1] - cu_q[b]) + i, so kv_len counts the new tokens
+ * already.  k is rotated by its position, v copied, q rotated into q_out.
+ *
+ * Inputs (device): q, k, v (dtype dt) as in medusa_rope; positions [T] int32,
+ *   or NULL for the slots; cu_q [B + 1] int32, non-decreasing from 0;
+ *   kv_len [B] int32.  rope NULL: no rotation, and q and q_out must be NULL.
+ *   q may be NULL (then q_out too): only k and v.
+ * In/out: the pools of pages (dtype dt).
+ * T is the number of rows the caller holds; rows from cu_q[B] on (a padded
+ *   batch) are left as they are, in q_out too.  A row whose slot is negative
+ *   (kv_len shorter than the chunk) is rotated but not written.
+ * Device checks: a slot past max_pages pages, a page outside [0, n_pages)
+ *   (that row is not written).
+ * Limits: B >= 1, T >= 0, page_size, n_pages, max_pages >= 1; the rest as
+ *   medusa_rope.
+ * ---------------------------------------------------------------------- */
+MEDUSA_API medusa_status_t medusa_rope_append(
+    const medusa_rope_t* rope, const void* q, long long q_stride, const void* k,
+    long long k_stride, const void* v, long long v_stride, medusa_dtype_t dt,
+    const int32_t* positions, const int32_t* cu_q, const int32_t* kv_len, int B, int T, int Hq,
+    int Hkv, int dh, void* q_out, long long q_out_stride, const medusa_pages_t* pages,
+    int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * medusa_chunk_attention
+ *
+ * The new tokens of B sequences attend to the cache, their own keys (already
+ * written, e.g. by medusa_rope_append) included.  Row i of sequence b sits at
+ * slot p = kv_len[b] - (cu_q[b+1] - cu_q[b]) + i and attends with weights
+ * softmax(scale * q.k) to slots 0..p; with p < 0 it sees nothing and its
+ * output is zero.  Query head hq reads kv head hq / (Hq / Hkv).  Chunks of
+ * one token (decoding), of whole prompts and of anything between can be
+ * mixed in a call; sequences may have no new token.
+ *
+ * Inputs (device): q [T, Hq, dh] of dtype dt, tokens q_stride elements apart;
+ *   pages (dtype dt); cu_q [B + 1], kv_len [B] int32 as above.
+ * Output (device): out [T, Hq, dh] of dtype dt, dense; rows from cu_q[B] on
+ *   are left as they are.
+ * Workspace: medusa_chunk_attention_workspace_size(...) bytes, 256-byte
+ *   aligned; the size depends on the current device's multiprocessor count
+ *   and on none of the lengths.
+ * Precision: bf16: scores and softmax statistics fp32, the softmax weights
+ *   rounded to bf16 for the value product, which accumulates in fp32.
+ *   MEDUSA_F32: fp32 throughout (CUDA cores).
+ * Cache slots from kv_len[b] on are never used, whatever they hold; below it
+ *   K and V must be finite.
+ * Device checks: a page outside [0, n_pages), kv_len[b] outside
+ *   [0, max_pages * page_size], cu_q decreasing, negative or above T, a
+ *   non-finite output.
+ * Limits: B in [1, 1024], T >= 0, Hq % Hkv == 0, Hq / Hkv <= 128, Hkv <= 1024,
+ *   scale > 0; pools 16-byte aligned; bf16: dh in {64, 128}, q_stride % 8 == 0,
+ *   q and out 16-byte aligned; f32: dh % 32 == 0, dh <= 256.  Any page_size;
+ *   in bf16, sizes of 128 or more and multiples of 8 fill the 128-key tiles
+ *   best.
+ * ---------------------------------------------------------------------- */
+MEDUSA_API size_t medusa_chunk_attention_workspace_size(int Hq, int Hkv, int dh,
+                                                        medusa_dtype_t dt);
+MEDUSA_API medusa_status_t medusa_chunk_attention(const void* q, long long q_stride,
+                                                  const medusa_pages_t* pages, medusa_dtype_t dt,
+                                                  const int32_t* cu_q, const int32_t* kv_len,
+                                                  int B, int T, int Hq, int Hkv, int dh,
+                                                  float scale, void* out, void* ws,
+                                                  size_t ws_bytes, int32_t* dev_status,
+                                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * medusa_sample_tokens
+ *
+ * One token per row of logits, drawn with the caller's random numbers after
+ * the row's filters.  With the row's tokens in the order of descending logit
+ * (equal logits: ascending id) and w_v = exp((z_v - max z) / temperature):
+ *
+ *   top_k  > 0: the first top_k tokens of the order stay (0 or less: all);
+ *   top_p  < 1: of these, a token stays when the mass before it in the order
+ *               is below top_p times their mass (the first always stays);
+ *   min_p  > 0: a token stays when w_v >= min_p;
+ *   token = the lowest id among the tokens that stay whose cumulative mass in
+ *           id order exceeds u times their mass.
+ *   temperature = 0: the first token of the order (kept = 1).
+ *
+ * Inputs (device): logits [n_rows, V] of dtype dt, rows row_stride elements
+ *   apart; row_idx [R] int32, the logits row of each drawn token (NULL: row
+ *   r), e.g. b * N + the kept node for a bonus token; u [R] fp32 in [0, 1);
+ *   temperature, top_p, min_p [R] fp32 and top_k [R] int32, each NULL for 1,
+ *   1, 0 and 0.
+ * Outputs (device): tokens [R] int32; kept [R] int32, the number of tokens
+ *   that stay (NULL to skip).
+ * Logits of -inf are never drawn and stay out of kept.
+ * Precision: weights are 64-bit fixed point in units of 2^-42 of the largest
+ *   one, from fp64 exponents; sums are exact, so results do not depend on
+ *   the order of summation.  A weight below 2^-43 of the largest counts as
+ *   zero (it still counts in kept, and can be drawn when u = 0).
+ * Limits: 1 <= V <= 393216 (fp32) or 786432 (bf16); R >= 0, R, n_rows <= 65535;
+ *   row_stride >= V.
+ * Device checks: a NaN or +inf logit, a row without a finite logit, u outside
+ *   [0, 1), a NaN or negative parameter, min_p above 1, row_idx outside
+ *   [0, n_rows); that row's token is -1 and kept 0.
+ * ---------------------------------------------------------------------- */
+MEDUSA_API medusa_status_t medusa_sample_tokens(const void* logits, medusa_dtype_t dt,
+                                                long long row_stride, int n_rows,
+                                                const int32_t* row_idx, int R, int V,
+                                                const float* u, const float* temperature,
+                                                const int32_t* top_k, const float* top_p,
+                                                const float* min_p, int32_t* tokens,
+                                                int32_t* kept, int32_t* dev_status,
+                                                void* stream);
 
 /* ------------------------------------------------------------------------
  * medusa_wait_flag

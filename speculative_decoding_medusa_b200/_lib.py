@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libmedusa_b200.so")
 
 MEDUSA_BF16 = 0
 MEDUSA_F32 = 1
+MEDUSA_ROPE_SCALINGS = {"none": 0, "linear": 1, "llama3": 2, "yarn": 3}
 MEDUSA_ACCEPT_GREEDY = 0
 MEDUSA_ACCEPT_TYPICAL = 1
 MAX_NODES = 256
@@ -40,6 +41,8 @@ EXPORTS = (
     "medusa_lmhead_verify_workspace_size", "medusa_lmhead_verify", "medusa_next_step",
     "medusa_tree_from_accuracies", "medusa_sample_bonus", "medusa_topk_merge",
     "medusa_verify_records_workspace_size", "medusa_verify_records", "medusa_verify_from_records",
+    "medusa_rope_freqs", "medusa_rope", "medusa_rope_append",
+    "medusa_chunk_attention_workspace_size", "medusa_chunk_attention", "medusa_sample_tokens",
     "medusa_wait_flag",
 )
 
@@ -54,6 +57,17 @@ class medusa_tree_t(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_int32), ("max_depth", ctypes.c_int32),
                 ("n_leaves", ctypes.c_int32), ("parent", ctypes.c_void_p),
                 ("depth", ctypes.c_void_p), ("rank", ctypes.c_void_p)]
+
+
+class medusa_rope_t(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("turns", ctypes.c_void_p)]
+
+
+class medusa_pages_t(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -124,6 +138,23 @@ def lib() -> ctypes.CDLL:
     L.medusa_tree_from_accuracies.argtypes = [_V, _I, _I, _I, _I, _V, _V, _V, _V]
     L.medusa_next_step.restype = _I
     L.medusa_next_step.argtypes = [_V, _I, _V, _V, _V, _I, _I, _I, _I, _V, _V, _V, _V]
+    _D = ctypes.c_double
+    L.medusa_rope_freqs.restype = _I
+    L.medusa_rope_freqs.argtypes = [_I, _D, _I, _D, _D, _D, _D, _V, _V]
+    L.medusa_rope.restype = _I
+    L.medusa_rope.argtypes = [_V, _V, _LL, _V, _LL, _I, _V, _I, _I, _I, _I, _I, _V, _LL, _V, _LL,
+                              _V]
+    L.medusa_rope_append.restype = _I
+    L.medusa_rope_append.argtypes = [_V, _V, _LL, _V, _LL, _V, _LL, _I, _V, _V, _V, _I, _I, _I,
+                                     _I, _I, _V, _LL, _V, _V, _V]
+    L.medusa_chunk_attention_workspace_size.restype = _Z
+    L.medusa_chunk_attention_workspace_size.argtypes = [_I] * 4
+    L.medusa_chunk_attention.restype = _I
+    L.medusa_chunk_attention.argtypes = [_V, _LL, _V, _I, _V, _V, _I, _I, _I, _I, _I, _F, _V, _V,
+                                         _Z, _V, _V]
+    L.medusa_sample_tokens.restype = _I
+    L.medusa_sample_tokens.argtypes = [_V, _I, _LL, _I, _V, _I, _I, _V, _V, _V, _V, _V, _V, _V,
+                                       _V, _V]
     L.medusa_wait_flag.restype = _I
     L.medusa_wait_flag.argtypes = [_V, ctypes.c_int32, ctypes.c_longlong, _V, _V]
     L.medusa_lmhead_verify.restype = _I
@@ -460,6 +491,196 @@ def medusa_verify_from_records(records, cand_logit, cand_ids, tree: Tree, V: int
                                             float(eps), float(delta), _p(accept_len),
                                             _p(accepted_nodes), _p(accepted_tokens), _p(bonus),
                                             _p(dev_status), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# prompt side: rotary positions, paged cache, chunk attention, sampling
+# ---------------------------------------------------------------------------
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None, shape=None):
+    """(address, token stride) of a [T, H, dh] CUDA tensor whose heads and
+    elements are dense (a slice of a packed projection is allowed)."""
+    st, sh = t.stride(), t.shape
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a [T, H, dh] CUDA tensor")
+    if (sh[2] > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != sh[2]):
+        raise ValueError(f"{name}: the heads and elements of a token must be dense")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, as its partner tensors are")
+    if shape is not None and tuple(sh) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return t.data_ptr(), (st[0] if sh[0] > 1 else sh[1] * sh[2])
+
+
+def _vec(t: Optional[torch.Tensor], name: str, dtype, n: int):
+    """Address of a dense CUDA tensor of n elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _here(*tensors) -> None:
+    """Every tensor must be on the current device, where the call launches."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensors must be on the current device (cuda:{cur})")
+
+
+class Rope:
+    """A rotation of the first ``rot`` elements of each head: the frequencies
+    theta^(-2i/rot) under a long-context scaling ("none", "linear", "llama3",
+    "yarn"), in pairs (i, i + rot/2), or (2i, 2i + 1) when interleaved.
+
+    ``low_freq_factor`` and ``high_freq_factor`` are full turns over
+    ``original_max_position`` (llama3: 1 and 4, yarn: 1 and 32 by default)."""
+
+    def __init__(self, rot: int, *, theta: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0,
+                 low_freq_factor: Optional[float] = None,
+                 high_freq_factor: Optional[float] = None, original_max_position: int = 8192,
+                 device=None):
+        import numpy as np
+        if scaling not in MEDUSA_ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(MEDUSA_ROPE_SCALINGS)}")
+        low = 1.0 if low_freq_factor is None else low_freq_factor
+        high = (32.0 if scaling == "yarn" else 4.0) if high_freq_factor is None \
+            else high_freq_factor
+        turns = np.zeros(max(int(rot) // 2, 1), dtype=np.uint64)
+        scale = ctypes.c_float(1.0)
+        _check(lib().medusa_rope_freqs(rot, theta, MEDUSA_ROPE_SCALINGS[scaling], factor, low, high,
+                                       original_max_position, turns.ctypes.data,
+                                       ctypes.byref(scale)))
+        self.rot, self.interleaved, self.scale = int(rot), bool(interleaved), scale.value
+        # full turns per position, in units of 2^-64 (the bits of a uint64)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device or "cuda")
+        self._c = medusa_rope_t(self.rot, int(self.interleaved), self.scale,
+                                self.turns.data_ptr())
+        self._ref = ctypes.addressof(self._c)
+
+
+class PagedCache:
+    """K and V pools [n_pages, Hkv, page_size, dh] and the page table
+    [B, max_pages] int32 of the sequences that use them."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor):
+        _req(K, "K")
+        _req(V, "V")
+        _req(table, "table")
+        if K.dim() != 4 or V.shape != K.shape or V.dtype is not K.dtype:
+            raise ValueError("K and V must be [n_pages, Hkv, page_size, dh] of one dtype")
+        if table.dim() != 2 or table.dtype is not torch.int32:
+            raise ValueError("table must be [B, max_pages] int32")
+        self.K, self.V, self.table = K, V, table
+        self.dt = _dt(K)
+        self.B = table.shape[0]
+        self.n_pages, self.Hkv, self.page_size, self.dh = K.shape
+        self._c = medusa_pages_t(K.data_ptr(), V.data_ptr(), table.data_ptr(), self.n_pages,
+                                 self.page_size, table.shape[1])
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def dense(cls, Kc: torch.Tensor, Vc: torch.Tensor) -> "PagedCache":
+        """The step's dense cache [B, Hkv, cap, dh]: one page of cap slots a sequence."""
+        t = torch.arange(Kc.shape[0], dtype=torch.int32, device=Kc.device)
+        return cls(Kc, Vc, t.view(-1, 1))
+
+
+def medusa_rope(rope: Rope, q, k, positions, q_out, k_out, inverse: bool = False,
+                stream=None) -> None:
+    """q [T,Hq,dh], k [T,Hkv,dh] (or None) rotated at positions [T] int32 into
+    q_out, k_out (which may be q and k themselves).  inverse: by the negative
+    angle (the gradient of the forward call)."""
+    T, Hq, dh = q.shape
+    qp, qs = _rows(q, "q")
+    op, os_ = _rows(q_out, "q_out", q.dtype, q.shape)
+    kp = ks = kop = kos = None
+    Hkv = 0
+    if k is not None:
+        Hkv = k.shape[1]
+        kp, ks = _rows(k, "k", q.dtype, (T, Hkv, dh))
+        kop, kos = _rows(k_out, "k_out", q.dtype, k.shape)
+    pp = _vec(positions, "positions", torch.int32, T)
+    _here(q, k, q_out, k_out, positions, rope.turns)
+    _check(lib().medusa_rope(rope._ref, qp, qs, kp, ks or 0, _dt(q), pp, T, Hq, Hkv, dh,
+                             1 if inverse else 0, op, os_, kop, kos or 0, _stream(stream)))
+
+
+def medusa_rope_append(rope: Optional[Rope], q, k, v, cu_q, kv_len, q_out, cache: PagedCache,
+                       positions=None, dev_status=None, stream=None) -> None:
+    """The new tokens q [T,Hq,dh] (or None), k, v [T,Hkv,dh] of cache.B
+    sequences: q rotated into q_out, k rotated and v copied into the cache at
+    slots kv_len[b] - (cu_q[b+1] - cu_q[b]) .. kv_len[b] - 1."""
+    T, Hkv, dh = k.shape
+    if Hkv != cache.Hkv or dh != cache.dh or k.dtype is not cache.K.dtype:
+        raise ValueError("k must have the cache's heads, head size and dtype")
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v", k.dtype, k.shape)
+    qp = qs = op = os_ = None
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _rows(q, "q", k.dtype, (T, Hq, dh))
+        op, os_ = _rows(q_out, "q_out", k.dtype, q.shape)
+    cup = _vec(cu_q, "cu_q", torch.int32, cache.B + 1)
+    kvp = _vec(kv_len, "kv_len", torch.int32, cache.B)
+    pp = _vec(positions, "positions", torch.int32, T)
+    _here(q, k, v, q_out, cu_q, kv_len, positions, cache.K)
+    _check(lib().medusa_rope_append(rope._ref if rope is not None else None, qp, qs or 0, kp, ks,
+                                    vp, vs, cache.dt, pp, cup, kvp, cache.B, T, Hq, Hkv, dh, op,
+                                    os_ or 0, cache._ref, _p(dev_status), _stream(stream)))
+
+
+def medusa_chunk_attention_workspace_size(Hq: int, Hkv: int, dh: int, dt: int) -> int:
+    return int(lib().medusa_chunk_attention_workspace_size(Hq, Hkv, dh, dt))
+
+
+def medusa_chunk_attention(q, cache: PagedCache, cu_q, kv_len, out,
+                           scale: Optional[float] = None, ws=None, dev_status=None,
+                           stream=None) -> None:
+    """q [T,Hq,dh] of cache.B sequences' new tokens (their k and v already in
+    the cache) -> out [T,Hq,dh], each token over its sequence's slots up to its
+    own."""
+    T, Hq, dh = q.shape
+    qp, qs = _rows(q, "q", cache.K.dtype)
+    if dh != cache.dh:
+        raise ValueError("q must have the cache's head size")
+    _req(out, "out")
+    if out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    cup = _vec(cu_q, "cu_q", torch.int32, cache.B + 1)
+    kvp = _vec(kv_len, "kv_len", torch.int32, cache.B)
+    _here(q, cache.K, cu_q, kv_len, out)
+    if scale is None:
+        scale = dh ** -0.5
+    if ws is None:
+        ws = workspace(medusa_chunk_attention_workspace_size(Hq, cache.Hkv, dh, cache.dt), q.device)
+    _check(lib().medusa_chunk_attention(qp, qs, cache._ref, cache.dt, cup, kvp, cache.B, T, Hq,
+                                        cache.Hkv, dh, scale, out.data_ptr(), ws.data_ptr(),
+                                        ws.numel(), _p(dev_status), _stream(stream)))
+
+
+def medusa_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
+                         row_idx=None, kept=None, dev_status=None, stream=None) -> None:
+    """tokens [R] int32 drawn from logits [n_rows,V] (rows may be strided) with
+    uniform numbers u [R]; temperature, top_p, min_p [R] fp32 and top_k [R]
+    int32 are off when None; row_idx [R] picks each draw's row."""
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be an [n_rows, V] CUDA tensor with dense rows")
+    n, V = logits.shape
+    R = u.numel()
+    f32, i32 = torch.float32, torch.int32
+    _here(logits, u, tokens, temperature, top_k, top_p, min_p, row_idx, kept)
+    _check(lib().medusa_sample_tokens(
+        logits.data_ptr(), _dt(logits), logits.stride(0) if n > 1 else V, n,
+        _vec(row_idx, "row_idx", i32, R), R, V, _vec(u, "u", f32, R),
+        _vec(temperature, "temperature", f32, R), _vec(top_k, "top_k", i32, R),
+        _vec(top_p, "top_p", f32, R), _vec(min_p, "min_p", f32, R),
+        _vec(tokens, "tokens", i32, R), _vec(kept, "kept", i32, R), _p(dev_status),
+        _stream(stream)))
 
 
 def medusa_wait_flag(flag, value: int, budget_cycles: int, dev_status, stream=None) -> None:

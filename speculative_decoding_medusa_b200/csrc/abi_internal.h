@@ -140,4 +140,30 @@ medusa_status_t kv_compact(void* Kc, void* Vc, medusa_dtype_t dt, int32_t* prefi
                            int Hkv, int dh, int cap, int max_depth, int32_t* compact_src,
                            int32_t* status, cudaStream_t stream);
 
+medusa_status_t rope_freqs(int rot, double theta, medusa_rope_scaling_t scaling, double factor,
+                           double low_turns, double high_turns, double original_max_position,
+                           uint64_t* turns, float* scale);
+medusa_status_t rope(const medusa_rope_t& r, const void* q, long long q_stride, const void* k,
+                     long long k_stride, medusa_dtype_t dt, const int32_t* positions, int T,
+                     int Hq, int Hkv, int dh, int inverse, void* q_out, long long q_out_stride,
+                     void* k_out, long long k_out_stride, cudaStream_t stream);
+medusa_status_t rope_append(const medusa_rope_t* r, const void* q, long long q_stride,
+                            const void* k, long long k_stride, const void* v, long long v_stride,
+                            medusa_dtype_t dt, const int32_t* positions, const int32_t* cu_q,
+                            const int32_t* kv_len, int B, int T, int Hq, int Hkv, int dh,
+                            void* q_out, long long q_out_stride, const medusa_pages_t& pages,
+                            int32_t* status, cudaStream_t stream);
+
+size_t chunk_attention_workspace_size(int Hq, int Hkv, int dh, medusa_dtype_t dt);
+medusa_status_t chunk_attention(const void* q, long long q_stride, const medusa_pages_t& pages,
+                                medusa_dtype_t dt, const int32_t* cu_q, const int32_t* kv_len,
+                                int B, int T, int Hq, int Hkv, int dh, float scale, void* out,
+                                void* ws, int32_t* status, cudaStream_t stream);
+
+medusa_status_t sample_tokens(const void* logits, medusa_dtype_t dt, long long row_stride,
+                              int n_rows, const int32_t* row_idx, int R, int V, const float* u,
+                              const float* temperature, const int32_t* top_k, const float* top_p,
+                              const float* min_p, int32_t* tokens, int32_t* kept, int32_t* status,
+                              cudaStream_t stream);
+
 }  // namespace medusa

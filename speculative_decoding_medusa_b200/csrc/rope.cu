@@ -1,0 +1,362 @@
+// Rotary positions: pairs of head elements rotated by an angle proportional
+// to the token's position, alone or with the write of K and V into the cache.
+//
+//   y0 = s (x0 cos a - x1 sin a),  y1 = s (x0 sin a + x1 cos a),  a = p f_i
+//
+// The frequency of a pair is kept in full turns per position as a 64-bit
+// fraction, so the angle modulo one turn is the low 64 bits of an integer
+// product: no range reduction, and the same precision at position 1e6 as at 1
+// (a fp32 product p * f would be off by 0.06 rad there).  The top 32 bits,
+// taken as a quadrant and a remainder of at most 1/8 turn, go through
+// sinpi / cospi in fp32 (angle error below 2^-28 turns).
+//
+// A block takes TB tokens: their rot / 2 sine/cosine pairs are computed once
+// into shared memory and serve every head (and, in the append, q and k).  A
+// thread then owns one unit of two 16-byte vectors per token (the two halves
+// of VEC pairs) and moves all TB tokens' units with their loads in flight
+// together.  Bound by HBM: every byte is read once and written once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "abi_internal.h"
+#include "common.cuh"
+
+namespace medusa {
+
+namespace {
+
+struct RopeParams {
+  const void *q, *k, *v;
+  void *q_out, *k_out;  // k_out unused in the append
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  const int32_t* positions;
+  const uint64_t* turns;
+  float scale;
+  int rot, interleaved, inverse;
+  int T, Hq, Hkv, dh;
+  int units, v_units;  // units of two vectors per q or k head, per v head
+  // append
+  const int32_t *cu_q, *kv_len, *table;
+  void *K, *V;
+  int B, n_pages, page_size, max_pages;
+  int32_t* status;
+};
+
+// cosine and sine (times scale) of p * turns / 2^64 turns
+__device__ __forceinline__ float2 turn_cos_sin(uint64_t turns, int p, float scale, float sign) {
+  const uint64_t t = turns * static_cast<uint64_t>(static_cast<int64_t>(p));
+  const uint32_t hi = static_cast<uint32_t>((t + 0x80000000ull) >> 32);  // 2^-32 turns
+  const uint32_t quad = (hi + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(hi - (quad << 30))) * 4.656612873077393e-10f;
+  const float c = cospif(x), s = sinpif(x);  // x half turns, |x| <= 1/4
+  float cc = (quad & 1u) ? -s : c, ss = (quad & 1u) ? c : s;
+  if (quad & 2u) {
+    cc = -cc;
+    ss = -ss;
+  }
+  return make_float2(cc * scale, ss * scale * sign);
+}
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Vec {
+  T e[VEC];
+};
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f(float& d, float x) { d = x; }
+
+template <typename T, int VEC, int TB, bool kAppend>
+__global__ void __launch_bounds__(512) rope_kernel(RopeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  using V = Vec<T, VEC>;
+  extern __shared__ float2 cs[];  // [TB][rot / 2]
+  __shared__ int s_pos[TB];       // position of the token
+  __shared__ int s_state[TB];     // bit 0: the row exists, bit 1: it has a cache slot
+  __shared__ long long s_dst[TB];  // row of kv head 0 in the pools
+  const int t0 = blockIdx.x * TB;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int half = p.rot >> 1;
+  if (kAppend) {
+    for (int j = tid >> 5; j < TB; j += blockDim.x >> 5) {
+      const int t = t0 + j;
+      // the sequence of row t: how many sequences end at or before it
+      int n = 0;
+      for (int b = lane; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) {
+        int state = 0, pos = 0;
+        long long dst = 0;
+        if (t < p.T && n < p.B) {
+          state = 1;
+          const int first = p.cu_q[n];
+          const int slot = p.kv_len[n] - (p.cu_q[n + 1] - first) + (t - first);
+          pos = p.positions != nullptr ? p.positions[t] : slot;
+          if (slot >= 0) {
+            const int pg = slot / p.page_size;
+            const int id = pg < p.max_pages ? p.table[(size_t)n * p.max_pages + pg] : -1;
+            if (id >= 0 && id < p.n_pages) {
+              state = 3;
+              dst = (long long)id * p.Hkv * p.page_size + (slot - pg * p.page_size);
+            } else {
+              report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+            }
+          }
+        }
+        s_state[j] = state;
+        s_pos[j] = pos;
+        s_dst[j] = dst;
+      }
+    }
+  } else if (tid < TB) {
+    s_state[tid] = t0 + tid < p.T ? 1 : 0;
+    s_pos[tid] = t0 + tid < p.T ? p.positions[t0 + tid] : 0;
+  }
+  __syncthreads();
+  const float sign = p.inverse ? -1.f : 1.f;
+  for (int e = tid; e < TB * half; e += blockDim.x) {
+    const int j = e / half, i = e - j * half;
+    cs[e] = turn_cos_sin(p.turns[i], s_pos[j], p.scale, sign);
+  }
+  __syncthreads();
+
+  const int rot_units = half / VEC;
+  const int nq = p.q != nullptr ? p.Hq * p.units : 0;
+  const int nk = p.k != nullptr ? p.Hkv * p.units : 0;
+  const int nv = kAppend ? p.Hkv * p.v_units : 0;
+  for (int w = tid; w < nq + nk + nv; w += blockDim.x) {
+    // which tensor, head and unit (the same for all TB tokens)
+    const bool is_q = w < nq, is_v = w >= nq + nk;
+    const int x = is_q ? w : is_v ? w - nq - nk : w - nq;
+    const int per = is_v ? p.v_units : p.units;
+    const int h = x / per, un = x - h * per;
+    const bool turns = !is_v && un < rot_units;
+    int o0, o1;  // element offsets of the unit's two vectors (o1 < 0: only one)
+    if (turns) {
+      o0 = p.interleaved ? un * 2 * VEC : un * VEC;
+      o1 = p.interleaved ? o0 + VEC : o0 + half;
+    } else {
+      o0 = (is_v ? un : un - rot_units) * 2 * VEC + (is_v ? 0 : p.rot);
+      o1 = o0 + VEC < p.dh ? o0 + VEC : -1;
+    }
+    const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) + (size_t)h * p.dh;
+    const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+    V a[TB], b[TB];
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      if (s_state[j] != 0) {
+        const T* s = src + (t0 + j) * stride;
+        a[j] = *reinterpret_cast<const V*>(s + o0);
+        if (o1 >= 0) b[j] = *reinterpret_cast<const V*>(s + o1);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      if (s_state[j] == 0) continue;
+      T* dst;
+      if (is_q) {
+        dst = static_cast<T*>(p.q_out) + (t0 + j) * p.q_out_stride + (size_t)h * p.dh;
+      } else if (kAppend) {
+        if (s_state[j] != 3) continue;
+        dst = static_cast<T*>(is_v ? p.V : p.K) + (s_dst[j] + (long long)h * p.page_size) * p.dh;
+      } else {
+        dst = static_cast<T*>(p.k_out) + (t0 + j) * p.k_out_stride + (size_t)h * p.dh;
+      }
+      if (turns) {
+        const float2* f = cs + j * half + un * VEC;
+        if (p.interleaved) {
+          T z[2 * VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            z[e] = a[j].e[e];
+            z[VEC + e] = b[j].e[e];
+          }
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float x0 = to_f(z[2 * e]), x1 = to_f(z[2 * e + 1]);
+            from_f(z[2 * e], x0 * f[e].x - x1 * f[e].y);
+            from_f(z[2 * e + 1], x0 * f[e].y + x1 * f[e].x);
+          }
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            a[j].e[e] = z[e];
+            b[j].e[e] = z[VEC + e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float x0 = to_f(a[j].e[e]), x1 = to_f(b[j].e[e]);
+            from_f(a[j].e[e], x0 * f[e].x - x1 * f[e].y);
+            from_f(b[j].e[e], x0 * f[e].y + x1 * f[e].x);
+          }
+        }
+      }
+      *reinterpret_cast<V*>(dst + o0) = a[j];
+      if (o1 >= 0) *reinterpret_cast<V*>(dst + o1) = b[j];
+    }
+  }
+}
+
+// the widest vector every access allows: VEC elements must divide the pairs,
+// the head, every stride and (in bytes) every base address
+int vector_width(const RopeParams& p, int eb) {
+  uintptr_t addr = 0;
+  long long step = p.rot / 2;
+  auto take = [&](const void* ptr, long long stride) {
+    if (ptr == nullptr) return;
+    addr |= reinterpret_cast<uintptr_t>(ptr);
+    step |= stride;
+  };
+  step |= p.dh;
+  take(p.q, p.q_stride);
+  take(p.q_out, p.q_out_stride);
+  take(p.k, p.k_stride);
+  take(p.k_out, p.k_out_stride);
+  take(p.v, p.v_stride);
+  take(p.K, 0);
+  take(p.V, 0);
+  int vec = 16 / eb;
+  while (vec > 1 && (step % vec != 0 || addr % (vec * eb) != 0)) vec >>= 1;
+  return vec;
+}
+
+template <typename T, int VEC, bool kAppend>
+medusa_status_t launch_vec(RopeParams& p, cudaStream_t stream) {
+  p.units = p.rot / (2 * VEC) + (p.dh - p.rot + 2 * VEC - 1) / (2 * VEC);
+  p.v_units = (p.dh + 2 * VEC - 1) / (2 * VEC);
+  const int work = (p.q ? p.Hq * p.units : 0) + (p.k ? p.Hkv * p.units : 0) +
+                   (kAppend ? p.Hkv * p.v_units : 0);
+  const int rounds = (work + 511) / 512;
+  const int threads = ((work + rounds - 1) / rounds + 31) / 32 * 32;
+  // four tokens a block once that still leaves several blocks per SM
+  if (p.T >= 4 * 4 * device_sm_count())
+    launch(rope_kernel<T, VEC, 4, kAppend>, (p.T + 3) / 4, threads, 4 * (p.rot / 2) * sizeof(float2),
+           stream, p);
+  else
+    launch(rope_kernel<T, VEC, 1, kAppend>, p.T, threads, (p.rot / 2) * sizeof(float2), stream, p);
+  return check_launch(kAppend ? "rope_append" : "rope");
+}
+
+template <bool kAppend>
+medusa_status_t dispatch(RopeParams& p, medusa_dtype_t dt, cudaStream_t stream) {
+  if (dt == MEDUSA_BF16) {
+    switch (vector_width(p, 2)) {
+      case 8: return launch_vec<__nv_bfloat16, 8, kAppend>(p, stream);
+      case 4: return launch_vec<__nv_bfloat16, 4, kAppend>(p, stream);
+      case 2: return launch_vec<__nv_bfloat16, 2, kAppend>(p, stream);
+      default: return launch_vec<__nv_bfloat16, 1, kAppend>(p, stream);
+    }
+  }
+  switch (vector_width(p, 4)) {
+    case 4: return launch_vec<float, 4, kAppend>(p, stream);
+    case 2: return launch_vec<float, 2, kAppend>(p, stream);
+    default: return launch_vec<float, 1, kAppend>(p, stream);
+  }
+}
+
+}  // namespace
+
+medusa_status_t rope_freqs(int rot, double theta, medusa_rope_scaling_t scaling, double factor,
+                           double low_turns, double high_turns, double original_max_position,
+                           uint64_t* turns, float* scale) {
+  const long double two_pi = 6.283185307179586476925286766559L;
+  const long double lt = logl((long double)theta);
+  long double lo = 0.0L, hi = 0.0L;
+  *scale = 1.f;
+  if (scaling == MEDUSA_ROPE_YARN) {
+    // the indices whose pairs make high_turns and low_turns full turns over
+    // the original length
+    const long double lo_len = logl(two_pi * high_turns), hi_len = logl(two_pi * low_turns);
+    const long double len = logl((long double)original_max_position);
+    lo = fmaxl(floorl(rot * (len - lo_len) / (2.0L * lt)), 0.0L);
+    hi = fminl(ceill(rot * (len - hi_len) / (2.0L * lt)), (long double)(rot - 1));
+    *scale = (float)(0.1 * log(factor) + 1.0);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    long double f = expl(-2.0L * i / rot * lt);
+    long double keep = 1.0L;  // share of the unscaled frequency
+    if (scaling == MEDUSA_ROPE_LINEAR) {
+      keep = 0.0L;
+    } else if (scaling == MEDUSA_ROPE_LLAMA3) {
+      const long double n = f * original_max_position / two_pi;
+      keep = fminl(fmaxl((n - low_turns) / (high_turns - low_turns), 0.0L), 1.0L);
+    } else if (scaling == MEDUSA_ROPE_YARN) {
+      keep = 1.0L - fminl(fmaxl((i - lo) / fmaxl(hi - lo, 1e-3L), 0.0L), 1.0L);
+    }
+    f = f * keep + f / factor * (1.0L - keep);
+    turns[i] = (uint64_t)(f / two_pi * 18446744073709551616.0L + 0.5L);
+  }
+  return MEDUSA_OK;
+}
+
+medusa_status_t rope(const medusa_rope_t& r, const void* q, long long q_stride, const void* k,
+                     long long k_stride, medusa_dtype_t dt, const int32_t* positions, int T,
+                     int Hq, int Hkv, int dh, int inverse, void* q_out, long long q_out_stride,
+                     void* k_out, long long k_out_stride, cudaStream_t stream) {
+  RopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.positions = positions;
+  p.turns = r.turns;
+  p.scale = r.scale;
+  p.rot = r.rot;
+  p.interleaved = r.interleaved;
+  p.inverse = inverse;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.dh = dh;
+  return dispatch<false>(p, dt, stream);
+}
+
+medusa_status_t rope_append(const medusa_rope_t* r, const void* q, long long q_stride,
+                            const void* k, long long k_stride, const void* v, long long v_stride,
+                            medusa_dtype_t dt, const int32_t* positions, const int32_t* cu_q,
+                            const int32_t* kv_len, int B, int T, int Hq, int Hkv, int dh,
+                            void* q_out, long long q_out_stride, const medusa_pages_t& pages,
+                            int32_t* status, cudaStream_t stream) {
+  RopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.positions = positions;
+  p.scale = 1.f;
+  if (r != nullptr) {
+    p.turns = r->turns;
+    p.scale = r->scale;
+    p.rot = r->rot;
+    p.interleaved = r->interleaved;
+  }
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.dh = dh;
+  p.cu_q = cu_q;
+  p.kv_len = kv_len;
+  p.B = B;
+  p.table = pages.table;
+  p.K = pages.K;
+  p.V = pages.V;
+  p.n_pages = pages.n_pages;
+  p.page_size = pages.page_size;
+  p.max_pages = pages.max_pages;
+  p.status = status;
+  return dispatch<true>(p, dt, stream);
+}
+
+}  // namespace medusa
