@@ -42,6 +42,7 @@
 #include <stdint.h>
 
 #include "abi_internal.h"
+#include "attn_common.cuh"
 #include "common.cuh"
 
 namespace medusa {
@@ -57,25 +58,6 @@ constexpr float kRescaleLog2 = 8.f;  // lazy rescale threshold, log2 units
 constexpr uint32_t kAttnTmemCols = 512;
 constexpr int kAttnMaxB = 256;       // sequences per call (schedule table in shared memory)
 constexpr int kAttnMinTiles = 4;     // smallest tile range a CTA takes
-
-// 2^x with the SFU instruction (ex2.approx; relative error about 2^-22, -inf -> 0)
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Register budget of a warpgroup (all four warps execute it together).  The
-// shares must add up to no more than the registers the CTA was launched with
-// (threads x registers per thread), or the increase waits for ever.
-template <int N>
-__device__ __forceinline__ void warpgroup_regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void warpgroup_regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 // 5-D tiled load (no multicast), c0 innermost
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -106,33 +88,6 @@ __device__ __forceinline__ void bulk_wait_read_all() {
 // every committed store has been performed
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-// max of three (one instruction on sm_100)
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// paired fp32 arithmetic (two lanes in one 64-bit register, sm_100)
-__device__ __forceinline__ uint64_t f32x2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f32x2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 struct AttnParams {

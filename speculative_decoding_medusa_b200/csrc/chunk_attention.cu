@@ -10,23 +10,12 @@
 #include <stdint.h>
 
 #include "abi_internal.h"
+#include "chunk_attention.cuh"
 #include "common.cuh"
 
 namespace medusa {
 
 namespace {
-
-struct ChunkParams {
-  const void* q;
-  long long q_stride;
-  const void *K, *V;
-  const int32_t *table, *cu_q, *kv_len;
-  int n_pages, page_size, max_pages;
-  int B, T, Hq, Hkv, G;
-  float scale;
-  void* out;
-  int32_t* status;
-};
 
 __device__ __forceinline__ float ld(const __nv_bfloat16* x) { return __bfloat162float(*x); }
 __device__ __forceinline__ float ld(const float* x) { return *x; }
@@ -147,19 +136,16 @@ medusa_status_t launch_rows(const ChunkParams& p, int dh, cudaStream_t stream) {
 size_t chunk_attention_workspace_size(int Hq, int Hkv, int dh, medusa_dtype_t dt) {
   (void)Hq;
   (void)Hkv;
-  (void)dh;
-  (void)dt;
-  return 0;
+  return dt == MEDUSA_BF16 ? chunk_attention_tc_workspace(dh) : 0;
 }
 
 medusa_status_t chunk_attention(const void* q, long long q_stride, const medusa_pages_t& pages,
                                 medusa_dtype_t dt, const int32_t* cu_q, const int32_t* kv_len,
                                 int B, int T, int Hq, int Hkv, int dh, float scale, void* out,
                                 void* ws, int32_t* status, cudaStream_t stream) {
-  (void)ws;
   ChunkParams p{q, q_stride, pages.K, pages.V, pages.table, cu_q, kv_len, pages.n_pages,
                 pages.page_size, pages.max_pages, B, T, Hq, Hkv, Hq / Hkv, scale, out, status};
-  if (dt == MEDUSA_BF16) return launch_rows<__nv_bfloat16>(p, dh, stream);
+  if (dt == MEDUSA_BF16) return chunk_attention_tc(p, dh, ws, stream);
   return launch_rows<float>(p, dh, stream);
 }
 

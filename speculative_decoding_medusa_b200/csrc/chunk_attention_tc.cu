@@ -1,0 +1,884 @@
+// Attention of a chunk of new tokens over a paged cache, bf16, on the tensor
+// cores (tcgen05).
+//
+//   out[t, h] = sum_j softmax_j(scale q.k_j) v_j  over slots j <= p(t)
+//
+// One online-softmax pass over the keys.  A segment is one (sequence, kv head,
+// group of query tokens): two M tiles of 128 rows, each floor(128 / G) tokens
+// times their G query heads, against the key tiles its last token can see.
+// All segments are laid end to end and every CTA takes an equal contiguous
+// range of their tiles, so prompts, single tokens and anything between fill
+// the machine alike; where a range cuts a segment, its pieces are merged by
+// log-sum-exp weights inside the kernel by the last piece to arrive.  A range
+// has at most two such pieces (its first and its last), so the workspace
+// depends on the number of CTAs alone.
+//
+// Roles (384 threads):
+//   warp 0      TMA producer.  Key tiles are 128 slots: part of a page of 128
+//               or more, or as many whole smaller pages as fit (their boxes
+//               land one after another in the tile; page sizes are multiples
+//               of the 8-row swizzle atom, any other size takes one page per
+//               tile).  Lanes fetch the page table entries and issue one
+//               box each.  K and V share one ring of 32 KB slots (dh = 128:
+//               5), K's freed after its scores, V's after its product.
+//   warp 1      MMA issuer: S = Q K^T into TMEM, then O += P V with P as bf16
+//               in TMEM over the scores' columns.
+//   warps 4-11  two softmax warpgroups, one query row per thread.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "abi_internal.h"
+#include "attn_common.cuh"
+#include "chunk_attention.cuh"
+#include "common.cuh"
+
+namespace medusa {
+
+namespace {
+
+constexpr int kBN = 128;       // keys per tile
+constexpr int kMT = 128;       // rows per M tile
+constexpr int kRows = 256;     // rows per segment
+constexpr int kThreads = 384;
+constexpr int kRegsLow = 96;   // registers a thread: producer and MMA warpgroup
+constexpr int kRegsHigh = 200;  // softmax warpgroups
+constexpr float kLazy = 8.f;   // rescale O only when the maximum grows by 2^8
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMinTiles = 4;   // smallest tile range a CTA takes
+constexpr int kMaxB = 1024;
+
+struct TcParams {
+  const int32_t *table, *cu_q, *kv_len;
+  int n_pages, page, max_pages;
+  int ppt;  // pages per tile (0: pages of 128 or more, tpp tiles each)
+  int tpp, kt;  // kt: slots of a full tile
+  int B, T, Hq, Hkv, G, tpt;  // tpt: tokens per M tile
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* o_part;             // [2 * grid][dh / 4][256] groups of 4 floats
+  float* lse_part;           // [2 * grid][256]
+  unsigned int* piece_count;  // [grid][8] pieces written, per warp of the segment that
+                              // starts in the CTA and leaves it (zeroed per call)
+  int32_t* status;
+};
+
+template <int DH>
+struct Smem {
+  static constexpr int kPanels = DH / 64;
+  static constexpr int kQBytes = kMT * DH * 2;
+  static constexpr int kItem = kBN * DH * 2;  // one K or V tile
+  static constexpr int kPanel = kBN * 128;
+  static constexpr int kRing = 5 * 128 / DH;  // K and V slots
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = 2 * kQBytes;
+  static constexpr int kBarOff = kRingOff + kRing * kItem;
+  // full[ring], empty[ring], q_full[2], s_full[2], p_full[2], pv_done[2], drain, exit
+  static constexpr int kNumBars = 2 * kRing + 10;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // holder, abort, ok, info[ring]
+  static constexpr int kStartOff = kMiscOff + 16 + kRing * 4;
+  static constexpr int kBytes = kStartOff + 32;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+  static_assert((kMaxB + 1) * 8 + 16 * 8 <= kRing * kItem, "schedule fits in the ring");
+};
+
+// key tiles that cover `vis` slots (at least one, so an empty row is written)
+__device__ __forceinline__ int tiles_of(int vis, const TcParams& p) {
+  if (p.ppt > 0) return max(1, (vis + p.kt - 1) / p.kt);
+  const int fp = vis / p.page;
+  return max(1, fp * p.tpp + (vis - fp * p.page + kBN - 1) / kBN);
+}
+
+// slots the last token of query group qg sees
+__device__ __forceinline__ int group_vis(int qlen, int kv, int qg, const TcParams& p) {
+  return max(0, kv - qlen + min(qlen, (qg + 1) * 2 * p.tpt));
+}
+
+struct Cursor {
+  int t, t0, t1;
+  int b, kvh, qg, n_qg, q0, qlen, kv;
+  int lt, ntiles, vis, n_mt;
+  bool first, last;
+
+  __device__ __forceinline__ void sequence(const TcParams& p) {
+    q0 = p.cu_q[b];
+    qlen = p.cu_q[b + 1] - q0;
+    kv = p.kv_len[b];
+    n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
+  }
+  __device__ __forceinline__ void group(const TcParams& p) {
+    vis = group_vis(qlen, kv, qg, p);
+    ntiles = tiles_of(vis, p);
+    n_mt = qlen - qg * 2 * p.tpt > p.tpt ? 2 : 1;
+  }
+  __device__ __forceinline__ void flags() {
+    first = t == t0 || lt == 0;
+    last = t == t1 - 1 || lt == ntiles - 1;
+  }
+  // s: {b, kvh, qg, lt} of tile t0
+  __device__ __forceinline__ void init(const int* s, int t0_, int t1_, const TcParams& p) {
+    t = t0 = t0_;
+    t1 = t1_;
+    b = s[0];
+    kvh = s[1];
+    qg = s[2];
+    lt = s[3];
+    sequence(p);
+    group(p);
+    flags();
+  }
+  __device__ __forceinline__ void advance(const TcParams& p) {
+    ++t;
+    if (t >= t1) return;
+    if (++lt == ntiles) {
+      lt = 0;
+      if (++qg == n_qg) {
+        qg = 0;
+        if (++kvh == p.Hkv) {
+          kvh = 0;
+          do {  // a later sequence with new tokens exists: t < t1 <= total
+            ++b;
+            sequence(p);
+          } while (qlen == 0);
+        }
+      }
+      group(p);
+    }
+    flags();
+  }
+  // first slot of the tile and how many of its slots the segment sees
+  __device__ __forceinline__ void span(const TcParams& p, int& key0, int& nv, int& pg, int& r0) const {
+    if (p.ppt > 0) {
+      pg = lt * p.ppt;
+      r0 = 0;
+      key0 = lt * p.kt;
+      nv = min(p.kt, vis - key0);
+    } else {
+      pg = lt / p.tpp;
+      r0 = (lt - pg * p.tpp) * kBN;
+      key0 = pg * p.page + r0;
+      nv = min(min(kBN, p.page - r0), vis - key0);
+    }
+    nv = max(nv, 0);
+  }
+  // slots of the tile that the copy fills with real rows or zeros, whatever
+  // the segment sees (rows nv .. there hold other slots)
+  __device__ __forceinline__ int filled(const TcParams& p, int r0) const {
+    return p.ppt > 0 ? p.kt : min(kBN, p.page - r0);
+  }
+};
+
+template <int DH>
+__device__ __forceinline__ bool store_row32(__nv_bfloat16* o, const float (&v)[32]) {
+  bool finite = true;
+  uint4* dst = reinterpret_cast<uint4*>(o);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float a = v[8 * c + 2 * x], b = v[8 * c + 2 * x + 1];
+      finite = finite && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[x] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return finite;
+}
+
+__global__ void chunk_zero_kernel(unsigned int* __restrict__ cnt, int n) {
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) cnt[i] = 0u;
+}
+
+// slot of the workspace that holds the piece of a segment (first tile s0,
+// global) in CTA c
+__device__ __forceinline__ int piece_slot(int c, int per, int s0) {
+  return 2 * c + (c * per >= s0 ? 0 : 1);
+}
+
+// The merge of a row's pieces (CTAs c0 .. c0 + n - 1) by the last to arrive.
+template <int DH>
+__device__ __noinline__ bool merge_row(const TcParams& p, __nv_bfloat16* out, int c0, int n, int per,
+                                       int s0, int row) {
+  float M = -INFINITY;
+  for (int k = 0; k < n; ++k)
+    M = fmaxf(M, __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row));
+  float wsum = 0.f;
+  for (int k = 0; k < n; ++k) {
+    const float lse = __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row);
+    wsum += lse == -INFINITY ? 0.f : exp2f(lse - M);
+  }
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  bool finite = true;
+#pragma unroll 1
+  for (int ch = 0; ch < DH / 32; ++ch) {
+    float acc[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+    for (int k = 0; k < n; ++k) {
+      const size_t slot = piece_slot(c0 + k, per, s0);
+      const float lse = __ldcg(p.lse_part + slot * kRows + row);
+      const float w = lse == -INFINITY ? 0.f : exp2f(lse - M) * inv;
+      const float4* src = reinterpret_cast<const float4*>(p.o_part) +
+                          (slot * (DH / 4) + ch * 8) * kRows + row;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 v = __ldcg(src + c * kRows);
+        acc[4 * c] += w * v.x;
+        acc[4 * c + 1] += w * v.y;
+        acc[4 * c + 2] += w * v.z;
+        acc[4 * c + 3] += w * v.w;
+      }
+    }
+    finite = store_row32<DH>(out + ch * 32, acc) && finite;
+  }
+  return finite;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, TcParams p) {
+  // The launch before this one is always chunk_zero_kernel, which waited for
+  // every earlier grid: the inputs are final already.  Only the piece
+  // counters it zeroes (and the writes that must follow it) need its
+  // completion, so griddepcontrol.wait comes right before those.
+  grid_dep_launch();
+  using L = Smem<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + L::kRing;
+  uint64_t* q_full = bars + 2 * L::kRing;
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* drain = pv_done + 2;
+  uint64_t* exit_bar = drain + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  volatile int* sched_bad = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
+  int* info = reinterpret_cast<int*>(smem + L::kMiscOff + 16);  // per ring slot, with each K
+  int* start = reinterpret_cast<int*>(smem + L::kStartOff);     // {b, kvh, qg, lt}
+
+  // ---- schedule: cum[b] = tiles of the sequences before b (in the ring) ----
+  long long* cum = reinterpret_cast<long long*>(smem + L::kRingOff);
+  long long* wsum = cum + kMaxB + 1;
+  if (tid == 0) *sched_bad = 0;
+  __syncthreads();
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int a0 = p.cu_q[b], a1 = p.cu_q[b + 1], kv = p.kv_len[b];
+    if (a0 < 0 || a1 < a0 || a1 > p.T || kv < 0 || kv > (long long)p.max_pages * p.page) {
+      *sched_bad = 1;
+      cum[b + 1] = 0;
+      continue;
+    }
+    const int n_qg = (a1 - a0 + 2 * p.tpt - 1) / (2 * p.tpt);
+    if (n_qg > 4) {
+      cum[b + 1] = -1;  // left to a warp
+      continue;
+    }
+    long long n = 0;
+    for (int g = 0; g < n_qg; ++g) n += tiles_of(group_vis(a1 - a0, kv, g, p), p);
+    cum[b + 1] = n * p.Hkv;
+  }
+  __syncthreads();
+  if (*sched_bad) {
+    if (tid == 0 && blockIdx.x == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    return;
+  }
+  for (int b = warp; b < p.B; b += kThreads / 32) {
+    if (cum[b + 1] >= 0) continue;
+    const int qlen = p.cu_q[b + 1] - p.cu_q[b], kv = p.kv_len[b];
+    const int n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
+    long long n = 0;
+    for (int g = lane; g < n_qg; g += 32) n += tiles_of(group_vis(qlen, kv, g, p), p);
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    __syncwarp();
+    if (lane == 0) cum[b + 1] = n * p.Hkv;
+  }
+  __syncthreads();
+  {  // inclusive scan over the sequences
+    const int each = (p.B + kThreads - 1) / kThreads;
+    long long n = 0;
+    for (int i = tid * each; i < min(p.B, (tid + 1) * each); ++i) n += cum[i + 1];
+    long long s = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long a = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += a;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    s -= n;
+    for (int w = 0; w < warp; ++w) s += wsum[w];
+    for (int i = tid * each; i < min(p.B, (tid + 1) * each); ++i) {
+      s += cum[i + 1];
+      cum[i + 1] = s;
+    }
+    if (tid == 0) cum[0] = 0;
+  }
+  __syncthreads();
+  if (cum[p.B] > 0x7fffffffLL) {
+    if (tid == 0 && blockIdx.x == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    return;
+  }
+  const int total = static_cast<int>(cum[p.B]);
+  const int per = max(kMinTiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const long long t0l = (long long)blockIdx.x * per;
+  if (t0l >= total) return;
+  const int t0 = static_cast<int>(t0l);
+  const int t1 = min(total, t0 + per);
+  const int n_tiles = t1 - t0;
+  if (warp == 2) {
+    // the segment of tile t0
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= t0) lo = mid;
+      else hi = mid;
+    }
+    const int per_head = static_cast<int>((cum[lo + 1] - cum[lo]) / p.Hkv);
+    int rem = t0 - static_cast<int>(cum[lo]);
+    const int kvh = rem / per_head;
+    rem -= kvh * per_head;
+    const int qlen = p.cu_q[lo + 1] - p.cu_q[lo], kv = p.kv_len[lo];
+    int g0 = 0;
+    for (;;) {
+      const int n = tiles_of(group_vis(qlen, kv, g0 + lane, p), p);
+      int s = n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += a;
+      }
+      const unsigned int over = __ballot_sync(0xffffffffu, s > rem);
+      if (over != 0u) {
+        const int at = __ffs(over) - 1;
+        if (lane == at) {
+          start[0] = lo;
+          start[1] = kvh;
+          start[2] = g0 + at;
+          start[3] = rem - (s - n);
+        }
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, s, 31);
+      g0 += 32;
+    }
+  }
+  if (tid == 0) {
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&q_full[m], 1);
+      mbar_init(&s_full[m], 1);
+      mbar_init(&p_full[m], 128);
+      mbar_init(&pv_done[m], 1);
+    }
+    mbar_init(drain, 1);
+    mbar_init(exit_bar, kThreads);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();  // the schedule in the ring has been read
+  // Rows that no copy ever writes are cleared once: of the Q tiles past their
+  // tokens, of the key tiles past a full tile's slots (their weights are zero,
+  // but 0 * NaN is not).
+  {
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const int q_rows = p.G * p.tpt;
+    if (q_rows < kMT) {
+      for (int i = tid; i < 2 * L::kQBytes / 16; i += kThreads)
+        reinterpret_cast<uint4*>(smem + L::kQOff)[i] = z;
+    }
+    if (p.ppt > 0 && p.kt < kBN) {
+      for (int i = tid; i < L::kRing * L::kItem / 16; i += kThreads)
+        reinterpret_cast<uint4*>(smem + L::kRingOff)[i] = z;
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t tmem_o = tmem_base;           // O[m]: DH columns each
+  const uint32_t tmem_s = tmem_base + 2 * DH;  // S[m], then P[m]: 128 columns each
+
+  // 128 x kRegsLow + 256 x kRegsHigh stays within the launch's 384 x 168
+  static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168,
+                "register split exceeds the launch's allocation");
+  if (warp < 4) {
+    warpgroup_regs_dec<kRegsLow>();
+    if (warp == 0) {
+      // ---------------- TMA producer ----------------
+      const uint64_t pol = l2_policy_evict_last();
+      Cursor cur;
+      cur.init(start, t0, t1, p);
+      const int panel_rows = p.ppt > 0 ? p.page : kBN;
+      const uint32_t box_bytes = static_cast<uint32_t>(panel_rows) * 128u * L::kPanels;
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true, bad_page = false;
+      int issued = 0;  // ring items whose copies were started
+      for (int j = 0; ok && j < n_tiles; ++j, cur.advance(p)) {
+        int key0, nv, pg, r0;
+        cur.span(p, key0, nv, pg, r0);
+        // boxes of the tile: one per lane
+        const int boxes = p.ppt > 0 ? (nv + p.page - 1) / p.page : (nv > 0 ? 1 : 0);
+        int id = 0;
+        bool mine = lane < boxes;
+        if (mine) {
+          id = p.table[(size_t)cur.b * p.max_pages + pg + lane];
+          if (id < 0 || id >= p.n_pages) {
+            bad_page = true;
+            mine = false;
+          }
+        }
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
+#pragma unroll
+        for (int kvi = 0; kvi < 2; ++kvi) {
+          if (lane == 0) {
+            ok = mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag, p.status);
+            if (ok) {
+              if (kvi == 0) info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0);
+              if (bytes > 0) mbar_arrive_expect_tx(&full[slot], bytes);
+              else mbar_arrive(&full[slot]);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          ++issued;
+          if (mine) {
+            uint8_t* dst = smem + L::kRingOff + slot * L::kItem + lane * panel_rows * 128;
+#pragma unroll
+            for (int pn = 0; pn < L::kPanels; ++pn)
+              tma_load_4d(dst + pn * L::kPanel, kvi == 0 ? &tmK : &tmV, &full[slot], pn * 64, r0,
+                          cur.kvh, id, pol);
+          }
+          if (++slot == L::kRing) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (bad_page) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      // every copy started has landed before the CTA may end
+      if (lane == 0) {
+        int no_abort = 0;
+        for (int x = max(0, issued - L::kRing); x < issued; ++x)
+          mbar_wait_bounded(&full[x % L::kRing], (x / L::kRing) & 1, &no_abort, p.status);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------- MMA issuer ----------------
+      // Order per tile j: PV(0,j), QK(0,j+1), PV(1,j), QK(1,j+1): while one
+      // warpgroup computes its softmax the tensor core works on the other M
+      // tile.
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = umma_idesc_bf16(kMT, kBN, 0);
+        constexpr uint32_t idesc_pv = umma_idesc_bf16(kMT, DH, 1);
+        const uint64_t dq0 = umma_desc_sw128(smem_u32(smem + L::kQOff));
+        const uint64_t dk0 = umma_desc_sw128(smem_u32(smem + L::kRingOff));
+        const uint64_t dv0 = umma_desc_sw128_lbo(smem_u32(smem + L::kRingOff), L::kPanel, 1024);
+        auto issue_qk = [&](int m, int st) {
+          const uint64_t dq = dq0 + (uint64_t)((m * L::kQBytes) >> 4);
+          const uint64_t dk = dk0 + (uint64_t)((st * L::kItem) >> 4);
+          const uint32_t d = tmem_s + m * kBN;
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            constexpr uint32_t qpanel = (kMT * 128) >> 4, kpanel = L::kPanel >> 4;
+            umma_bf16(d, dq + (kk >> 2) * qpanel + (kk & 3) * 2,
+                      dk + (kk >> 2) * kpanel + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[m]);
+        };
+        auto issue_pv = [&](int m, int st, uint32_t acc0) {
+          const uint64_t dv = dv0 + (uint64_t)((st * L::kItem) >> 4);
+          const uint32_t d = tmem_o + m * DH;
+          const uint32_t pcol = tmem_s + m * kBN;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            // 16 keys: 8 columns of packed P, two 8-row groups of V
+            umma_bf16_ts(d, pcol + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                         kk > 0 ? 1u : acc0);
+          umma_commit(&pv_done[m]);
+        };
+        uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // completed waits per barrier
+        int ks = 0;
+        uint32_t kph = 0;
+        bool ok = mbar_wait_bounded(&full[0], 0, abort_flag, p.status);
+        int cur = ok ? info[0] : 0;
+        if (ok) ok = mbar_wait_bounded(&q_full[0], nq0++ & 1, abort_flag, p.status);
+        if (ok) {
+          tc_fence_after();
+          issue_qk(0, 0);
+          if (cur & 2) {
+            ok = mbar_wait_bounded(&q_full[1], nq1++ & 1, abort_flag, p.status);
+            if (ok) {
+              tc_fence_after();
+              issue_qk(1, 0);
+            }
+          }
+          umma_commit(&empty[0]);
+        }
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          int vs = ks + 1;
+          uint32_t vph = kph;
+          if (vs == L::kRing) {
+            vs = 0;
+            vph ^= 1u;
+          }
+          ks = vs + 1;
+          kph = vph;
+          if (ks == L::kRing) {
+            ks = 0;
+            kph ^= 1u;
+          }
+          const bool has_next = j + 1 < n_tiles;
+          const bool two = (cur & 2) != 0;
+          const uint32_t acc0 = (cur & 1) ? 0u : 1u;
+          if (!mbar_wait_bounded(&full[vs], vph, abort_flag, p.status) ||
+              !mbar_wait_bounded(&p_full[0], np0++ & 1, abort_flag, p.status))
+            break;
+          tc_fence_after();
+          issue_pv(0, vs, acc0);
+          if (!two) umma_commit(&empty[vs]);
+          int nxt = 0;
+          if (has_next) {
+            if (!mbar_wait_bounded(&full[ks], kph, abort_flag, p.status)) break;
+            nxt = info[ks];
+            if ((nxt & 1) && !mbar_wait_bounded(&q_full[0], nq0++ & 1, abort_flag, p.status)) break;
+            tc_fence_after();
+            issue_qk(0, ks);
+            if (!(nxt & 2)) umma_commit(&empty[ks]);
+          }
+          if (two) {
+            if (!mbar_wait_bounded(&p_full[1], np1++ & 1, abort_flag, p.status)) break;
+            tc_fence_after();
+            issue_pv(1, vs, acc0);
+            umma_commit(&empty[vs]);
+          }
+          if (has_next && (nxt & 2)) {
+            if ((nxt & 1) && !mbar_wait_bounded(&q_full[1], nq1++ & 1, abort_flag, p.status)) break;
+            tc_fence_after();
+            issue_qk(1, ks);
+            umma_commit(&empty[ks]);
+          }
+          cur = nxt;
+        }
+        umma_commit(drain);
+        int no_abort = 0;
+        mbar_wait_bounded(drain, 0, &no_abort, p.status);
+      }
+    }
+  } else {
+    warpgroup_regs_inc<kRegsHigh>();
+    // ---------------- softmax warpgroups (M tile 0: warps 4-7, 1: 8-11) ----------------
+    const int m = (warp - 4) >> 2;
+    const int quad = warp & 3;
+    const int rl = quad * 32 + lane;  // row within the M tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t srow = tmem_s + lane_off + m * kBN;
+    const int tok_l = rl / p.G, g = rl - tok_l * p.G;  // token of the M tile, head of the group
+    uint8_t* qtile = smem + L::kQOff + m * L::kQBytes;
+    auto load_q = [&](const Cursor& x) {
+      if (rl == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(p.G * p.tpt) * 128u * L::kPanels;
+        mbar_arrive_expect_tx(&q_full[m], bytes);
+#pragma unroll
+        for (int pn = 0; pn < L::kPanels; ++pn)
+          tma_load_4d(qtile + pn * (kMT * 128), &tmQ, &q_full[m], pn * 64, 0, x.kvh,
+                      x.q0 + (x.qg * 2 + m) * p.tpt, l2_policy_evict_first());
+      }
+    };
+    uint32_t tcount = 0;
+    bool q_ready = false;
+    float m_used = -INFINITY, l_run = 0.f;
+    int jj = 0, piece_lt0 = 0;
+    bool finite = true;
+    Cursor cur;
+    cur.init(start, t0, t1, p);
+    for (int j = 0; j < n_tiles; ++j, cur.advance(p)) {
+      if (m >= cur.n_mt) continue;
+      const int tok = (cur.qg * 2 + m) * p.tpt + tok_l;
+      const bool valid = tok_l < p.tpt && tok < cur.qlen;
+      if (cur.first) {
+        if (!q_ready) load_q(cur);
+        q_ready = false;
+        m_used = -INFINITY;
+        l_run = 0.f;
+        jj = 0;
+        piece_lt0 = cur.lt;
+      }
+      int key0, nv, pg, r0;
+      cur.span(p, key0, nv, pg, r0);
+      // slots of the tile this row sees
+      const int limit = valid ? min(nv, cur.kv - cur.qlen + tok + 1 - key0) : 0;
+      if (!mbar_wait_bounded(&s_full[m], tcount & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      if (cur.last && j + 1 < n_tiles) {
+        // every QK of this piece is done: fetch the next piece's Q now
+        Cursor nx = cur;
+        nx.advance(p);
+        if (m < nx.n_mt) {
+          load_q(nx);
+          q_ready = true;
+        }
+      }
+      if (m == 0 && nv < cur.filled(p, r0)) {
+        // The tile's V rows from nv on belong to no slot of the segment and
+        // may hold anything: cleared once they have landed (PV of either M
+        // tile is issued after this warpgroup's arrival below).
+        const int item = 2 * j + 1, vs = item % L::kRing;
+        if (!mbar_wait_bounded(&full[vs], (item / L::kRing) & 1, abort_flag, p.status)) break;
+        uint8_t* vt = smem + L::kRingOff + vs * L::kItem;
+        for (int row = nv + quad; row < kBN; row += 4) {
+          if (lane < 8 * L::kPanels)
+            *reinterpret_cast<uint4*>(vt + (lane >> 3) * L::kPanel + row * 128 + (lane & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      // warps without a query row only keep the pipeline going
+      if (__any_sync(0xffffffffu, valid)) {
+        float sv[kBN];
+        {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32_raw(srow + q * 32, r[q]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_regs_after_wait(r[q]);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sv[q * 32 + c] = __uint_as_float(r[q][c]);
+          }
+        }
+        if (!__all_sync(0xffffffffu, limit >= kBN)) {
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if (c >= limit) sv[c] = -INFINITY;
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kBN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], sv[c], sv[c + 1]);
+        const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * p.scale_log2;
+        // The exponent base is a running maximum that only moves when a tile
+        // exceeds it by more than 2^8 (the stale base cancels in O / l).
+        const bool need = (m_used == -INFINITY) ? (mx != -INFINITY) : (mx > m_used + kLazy);
+        if (__any_sync(0xffffffffu, need)) {
+          const float new_m = need ? mx : m_used;
+          const float corr = (need && m_used != -INFINITY) ? ex2_approx(m_used - new_m) : 1.f;
+          if (jj > 0) {
+            // O holds earlier tiles (their PV precedes this tile's QK)
+#pragma unroll 1
+            for (int ch = 0; ch < DH / 32; ++ch) {
+              float o[32];
+              const uint32_t ta = tmem_o + lane_off + m * DH + ch * 32;
+              tmem_ld32(ta, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= corr;
+              tmem_st32(ta, o);
+            }
+          }
+          l_run *= corr;
+          m_used = new_m;
+        }
+        const float nbase = m_used == -INFINITY ? 0.f : -m_used;
+        const uint64_t scale2 = f32x2_pack(p.scale_log2, p.scale_log2);
+        const uint64_t nbase2 = f32x2_pack(nbase, nbase);
+        uint64_t part[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hq = 0; hq < 2; ++hq) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = hq * 64 + 2 * e;
+            float x0, x1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(sv[c], sv[c + 1]), scale2, nbase2), x0, x1);
+            const float a0 = ex2_approx(x0);
+            const float a1 = ex2_approx(x1);
+            part[e & 3] = f32x2_add(part[e & 3], f32x2_pack(a0, a1));
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a0, a1);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          tmem_st32_u(srow + hq * 32, pk);
+        }
+        float s0, s1;
+        f32x2_unpack(f32x2_add(f32x2_add(part[0], part[1]), f32x2_add(part[2], part[3])), s0, s1);
+        l_run += s0 + s1;
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(&p_full[m]);
+      if (cur.last) {
+        grid_dep_wait();
+        if (!mbar_wait_bounded(&pv_done[m], tcount & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        const bool any = __any_sync(0xffffffffu, valid);
+        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+        // a NaN sum is no empty row
+        const float norm = l_run == l_run ? inv : l_run;
+        __nv_bfloat16* out =
+            p.out + ((size_t)(cur.q0 + tok) * p.Hq + cur.kvh * p.G + g) * DH;
+        if (!any) {
+          // nothing to write
+        } else if (piece_lt0 == 0 && cur.lt == cur.ntiles - 1) {
+#pragma unroll 1
+          for (int ch = 0; ch < DH / 32; ++ch) {
+            float o[32];
+            tmem_ld32(tmem_o + lane_off + m * DH + ch * 32, o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = l_run == 0.f ? 0.f : o[c] * norm;
+            if (valid) finite = store_row32<DH>(out + ch * 32, o) && finite;
+          }
+        } else {
+          const int s0 = t0 + j - cur.lt;  // the segment's first tile
+          const int c0 = s0 / per;
+          const int n_pieces = (s0 + cur.ntiles - 1) / per - c0 + 1;
+          const size_t slot = piece_slot(blockIdx.x, per, s0);
+          const int row = m * kMT + rl;
+          float4* dst = reinterpret_cast<float4*>(p.o_part) + slot * (DH / 4) * kRows + row;
+#pragma unroll 1
+          for (int ch = 0; ch < DH / 32; ++ch) {
+            float o[32];
+            tmem_ld32(tmem_o + lane_off + m * DH + ch * 32, o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = l_run == 0.f ? 0.f : o[c] * norm;
+            if (valid) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                dst[(ch * 8 + c) * kRows] =
+                    make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            }
+          }
+          if (valid)
+            p.lse_part[slot * kRows + row] = l_run > 0.f ? m_used + log2f(l_run)
+                                             : l_run == 0.f ? -INFINITY : l_run;
+          // release this warp's rows, count them in; the last piece merges
+          __threadfence();
+          __syncwarp();
+          unsigned int before = 0u;
+          if (lane == 0)
+            before = atomicAdd(&p.piece_count[c0 * 8 + (warp - 4)], 1u);
+          before = __shfl_sync(0xffffffffu, before, 0);
+          if (before == static_cast<unsigned int>(n_pieces - 1)) {
+            __threadfence();
+            if (valid) finite = merge_row<DH>(p, out, c0, n_pieces, per, s0, row) && finite;
+          }
+        }
+        tc_fence_before();
+      }
+      ++tcount;
+      ++jj;
+    }
+    if (!finite) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+  }
+
+  // TMEM is released once every thread is past its last TMEM access
+  tc_fence_before();
+  mbar_arrive(exit_bar);
+  if (warp == 1) {
+    __syncwarp();
+    int no_abort = 0;
+    mbar_wait_bounded(exit_bar, 0, &no_abort, p.status);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+template <int DH>
+medusa_status_t launch_tc(const ChunkParams& c, void* ws, cudaStream_t stream) {
+  using L = Smem<DH>;
+  TcParams p{};
+  p.table = c.table;
+  p.cu_q = c.cu_q;
+  p.kv_len = c.kv_len;
+  p.n_pages = c.n_pages;
+  p.page = c.page_size;
+  p.max_pages = c.max_pages;
+  if (c.page_size >= kBN) {
+    p.ppt = 0;
+    p.tpp = (c.page_size + kBN - 1) / kBN;
+    p.kt = kBN;
+  } else {
+    // several pages in a tile need whole swizzle atoms of 8 rows
+    p.ppt = c.page_size % 8 == 0 ? kBN / c.page_size : 1;
+    p.tpp = 1;
+    p.kt = p.ppt * c.page_size;
+  }
+  p.B = c.B;
+  p.T = c.T;
+  p.Hq = c.Hq;
+  p.Hkv = c.Hkv;
+  p.G = c.G;
+  p.tpt = kMT / c.G;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(c.out);
+  p.status = c.status;
+  const int grid = device_sm_count();  // persistent: one CTA per SM
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  const size_t o_bytes = (size_t)2 * grid * kRows * DH * 4, l_bytes = (size_t)2 * grid * kRows * 4;
+  p.o_part = reinterpret_cast<float*>(w8);
+  p.lse_part = reinterpret_cast<float*>(w8 + o_bytes);
+  p.piece_count = reinterpret_cast<unsigned int*>(w8 + o_bytes + l_bytes);
+
+  CUtensorMap mQ, mK, mV;
+  // queries as [T][Hkv][G][DH]: boxes of 64 columns x G heads x tpt tokens
+  const uint64_t dq[4] = {DH, (uint64_t)c.G, (uint64_t)c.Hkv, (uint64_t)c.T};
+  const uint64_t sq[3] = {DH * 2, (uint64_t)c.G * DH * 2,
+                          (uint64_t)(c.T > 1 ? c.q_stride : (long long)c.Hq * DH) * 2};
+  const uint32_t bq[4] = {64, (uint32_t)c.G, 1, (uint32_t)p.tpt};
+  // pools [n_pages][Hkv][page][DH]: boxes of 64 columns x (a page or 128 rows)
+  const uint64_t dk[4] = {DH, (uint64_t)c.page_size, (uint64_t)c.Hkv, (uint64_t)c.n_pages};
+  const uint64_t sk[3] = {DH * 2, (uint64_t)c.page_size * DH * 2,
+                          (uint64_t)c.Hkv * c.page_size * DH * 2};
+  const uint32_t bk[4] = {64, (uint32_t)(c.page_size < kBN ? c.page_size : kBN), 1, 1};
+  if (!make_tmap_bf16(&mQ, c.q, 4, dq, sq, bq) || !make_tmap_bf16(&mK, c.K, 4, dk, sk, bk) ||
+      !make_tmap_bf16(&mV, c.V, 4, dk, sk, bk))
+    return fail(MEDUSA_ERR_CUDA, "chunk_attention: cuTensorMapEncodeTiled failed");
+  if (cudaFuncSetAttribute(chunk_attn_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           L::kAlloc) != cudaSuccess)
+    return fail(MEDUSA_ERR_CUDA, "cudaFuncSetAttribute(chunk_attention) failed");
+  // the register shares must fit in what the launch allocates, or the softmax
+  // warpgroups' increase would wait for ever
+  static const int regs = [] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, chunk_attn_tc_kernel<DH>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (128 * kRegsLow + 256 * kRegsHigh > kThreads * regs)
+    return fail(MEDUSA_ERR_UNSUPPORTED, "chunk_attention: register split exceeds the build's");
+  launch(chunk_zero_kernel, 1, 1024, 0, stream, p.piece_count, grid * 8);
+  const medusa_status_t st = check_launch("chunk_attention_counters");
+  if (st != MEDUSA_OK) return st;
+  launch(chunk_attn_tc_kernel<DH>, grid, kThreads, L::kAlloc, stream, mQ, mK, mV, p);
+  return check_launch("chunk_attention");
+}
+
+}  // namespace
+
+size_t chunk_attention_tc_workspace(int dh) {
+  const size_t grid = device_sm_count();
+  return align256(2 * grid * kRows * dh * 4 + 2 * grid * kRows * 4 + grid * 8 * 4);
+}
+
+medusa_status_t chunk_attention_tc(const ChunkParams& p, int dh, void* ws, cudaStream_t stream) {
+  if (dh == 128) return launch_tc<128>(p, ws, stream);
+  return launch_tc<64>(p, ws, stream);
+}
+
+}  // namespace medusa
