@@ -775,7 +775,7 @@ MEDUSA_API medusa_status_t medusa_chunk_attention(const void* q, long long q_str
  *   one, from fp64 exponents; sums are exact, so results do not depend on
  *   the order of summation.  A weight below 2^-43 of the largest counts as
  *   zero (it still counts in kept, and can be drawn when u = 0).
- * Limits: 1 <= V <= 393216 (fp32) or 786432 (bf16); R >= 0, R, n_rows <= 65535;
+ * Limits: 1 <= V <= 327680 (fp32) or 655360 (bf16); R >= 0, R, n_rows <= 65535;
  *   row_stride >= V.
  * Device checks: a NaN or +inf logit, a row without a finite logit, u outside
  *   [0, 1), a NaN or negative parameter, min_p above 1, row_idx outside

@@ -498,36 +498,54 @@ def medusa_verify_from_records(records, cand_logit, cand_ids, tree: Tree, V: int
 # ---------------------------------------------------------------------------
 
 
-def _rows(t: torch.Tensor, name: str, dtype=None, shape=None):
-    """(address, token stride) of a [T, H, dh] CUDA tensor whose heads and
-    elements are dense (a slice of a packed projection is allowed)."""
-    st, sh = t.stride(), t.shape
-    if t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a [T, H, dh] CUDA tensor")
-    if (sh[2] > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != sh[2]):
+# These calls are short enough for the marshalling to show, so an argument is
+# checked with as few tensor queries as possible: one test of the common case,
+# and the reasons only when it fails.
+
+
+def _dev() -> int:
+    """The current device, where a call launches and every tensor must be."""
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _bad_tensor(t, name: str, dev: int, what: str):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device (cuda:{dev})")
+    raise ValueError(f"{name} must be {what}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """(address, token stride) of a [T, H, dh] tensor whose heads and elements
+    are dense (a slice of a packed projection is allowed)."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _bad_tensor(t, name, dev, f"a {dtype} CUDA tensor of shape {tuple(shape)}")
+    _, H, dh = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * dh
+    st = t.stride()
+    if (dh > 1 and st[2] != 1) or (H > 1 and st[1] != dh):
         raise ValueError(f"{name}: the heads and elements of a token must be dense")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, as its partner tensors are")
-    if shape is not None and tuple(sh) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    return t.data_ptr(), (st[0] if sh[0] > 1 else sh[1] * sh[2])
+    return t.data_ptr(), (st[0] if shape[0] > 1 else H * dh)
 
 
-def _vec(t: Optional[torch.Tensor], name: str, dtype, n: int):
-    """Address of a dense CUDA tensor of n elements (None: NULL)."""
+def _vec(t: Optional[torch.Tensor], name: str, dtype, n: int, dev: int):
+    """Address of a dense tensor of n elements (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _bad_tensor(t, name, dev, f"a contiguous {dtype} CUDA tensor of {n} elements")
     return t.data_ptr()
 
 
-def _here(*tensors) -> None:
-    """Every tensor must be on the current device, where the call launches."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensors must be on the current device (cuda:{cur})")
+def _3d(t: torch.Tensor, name: str):
+    sh = t.shape
+    if len(sh) != 3:
+        raise ValueError(f"{name} must be a [T, H, dh] CUDA tensor")
+    return sh
 
 
 class Rope:
@@ -574,13 +592,20 @@ class PagedCache:
             raise ValueError("K and V must be [n_pages, Hkv, page_size, dh] of one dtype")
         if table.dim() != 2 or table.dtype is not torch.int32:
             raise ValueError("table must be [B, max_pages] int32")
+        if V.device != K.device or table.device != K.device:
+            raise ValueError("K, V and table must be on one device")
         self.K, self.V, self.table = K, V, table
+        self._device = K.get_device()
         self.dt = _dt(K)
         self.B = table.shape[0]
         self.n_pages, self.Hkv, self.page_size, self.dh = K.shape
         self._c = medusa_pages_t(K.data_ptr(), V.data_ptr(), table.data_ptr(), self.n_pages,
                                  self.page_size, table.shape[1])
         self._ref = ctypes.addressof(self._c)
+
+    def _on(self, dev: int) -> None:
+        if self._device != dev:
+            _bad_tensor(self.K, "cache", dev, "on a CUDA device")
 
     @classmethod
     def dense(cls, Kc: torch.Tensor, Vc: torch.Tensor) -> "PagedCache":
@@ -594,19 +619,27 @@ def medusa_rope(rope: Rope, q, k, positions, q_out, k_out, inverse: bool = False
     """q [T,Hq,dh], k [T,Hkv,dh] (or None) rotated at positions [T] int32 into
     q_out, k_out (which may be q and k themselves).  inverse: by the negative
     angle (the gradient of the forward call)."""
-    T, Hq, dh = q.shape
-    qp, qs = _rows(q, "q")
-    op, os_ = _rows(q_out, "q_out", q.dtype, q.shape)
-    kp = ks = kop = kos = None
-    Hkv = 0
+    dev = _dev()
+    qsh, dtype = _3d(q, "q"), q.dtype
+    T, Hq, dh = qsh
+    qp, qs = _rows(q, "q", dtype, qsh, dev)
+    op, os_ = _rows(q_out, "q_out", dtype, qsh, dev)
+    kp = kop = None
+    ks = kos = Hkv = 0
     if k is not None:
-        Hkv = k.shape[1]
-        kp, ks = _rows(k, "k", q.dtype, (T, Hkv, dh))
-        kop, kos = _rows(k_out, "k_out", q.dtype, k.shape)
-    pp = _vec(positions, "positions", torch.int32, T)
-    _here(q, k, q_out, k_out, positions, rope.turns)
-    _check(lib().medusa_rope(rope._ref, qp, qs, kp, ks or 0, _dt(q), pp, T, Hq, Hkv, dh,
-                             1 if inverse else 0, op, os_, kop, kos or 0, _stream(stream)))
+        ksh = _3d(k, "k")
+        Hkv = ksh[1]
+        if ksh[0] != T or ksh[2] != dh:
+            raise ValueError("k must have q's tokens and head size")
+        kp, ks = _rows(k, "k", dtype, ksh, dev)
+        kop, kos = _rows(k_out, "k_out", dtype, ksh, dev)
+    pp = _vec(positions, "positions", torch.int32, T, dev)
+    if rope.turns.get_device() != dev:
+        _bad_tensor(rope.turns, "rope", dev, "on a CUDA device")
+    st = lib().medusa_rope(rope._ref, qp, qs, kp, ks, _dt(q), pp, T, Hq, Hkv, dh,
+                           1 if inverse else 0, op, os_, kop, kos, _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def medusa_rope_append(rope: Optional[Rope], q, k, v, cu_q, kv_len, q_out, cache: PagedCache,
@@ -614,24 +647,37 @@ def medusa_rope_append(rope: Optional[Rope], q, k, v, cu_q, kv_len, q_out, cache
     """The new tokens q [T,Hq,dh] (or None), k, v [T,Hkv,dh] of cache.B
     sequences: q rotated into q_out, k rotated and v copied into the cache at
     slots kv_len[b] - (cu_q[b+1] - cu_q[b]) .. kv_len[b] - 1."""
-    T, Hkv, dh = k.shape
-    if Hkv != cache.Hkv or dh != cache.dh or k.dtype is not cache.K.dtype:
-        raise ValueError("k must have the cache's heads, head size and dtype")
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v", k.dtype, k.shape)
-    qp = qs = op = os_ = None
-    Hq = 0
+    dev = _dev()
+    ksh, dtype = _3d(k, "k"), cache.K.dtype
+    T, Hkv, dh = ksh
+    if Hkv != cache.Hkv or dh != cache.dh:
+        raise ValueError("k must have the cache's heads and head size")
+    kp, ks = _rows(k, "k", dtype, ksh, dev)
+    vp, vs = _rows(v, "v", dtype, ksh, dev)
+    qp = op = ref = None
+    qs = os_ = Hq = 0
     if q is not None:
-        Hq = q.shape[1]
-        qp, qs = _rows(q, "q", k.dtype, (T, Hq, dh))
-        op, os_ = _rows(q_out, "q_out", k.dtype, q.shape)
-    cup = _vec(cu_q, "cu_q", torch.int32, cache.B + 1)
-    kvp = _vec(kv_len, "kv_len", torch.int32, cache.B)
-    pp = _vec(positions, "positions", torch.int32, T)
-    _here(q, k, v, q_out, cu_q, kv_len, positions, cache.K)
-    _check(lib().medusa_rope_append(rope._ref if rope is not None else None, qp, qs or 0, kp, ks,
-                                    vp, vs, cache.dt, pp, cup, kvp, cache.B, T, Hq, Hkv, dh, op,
-                                    os_ or 0, cache._ref, _p(dev_status), _stream(stream)))
+        qsh = _3d(q, "q")
+        Hq = qsh[1]
+        if qsh[0] != T or qsh[2] != dh:
+            raise ValueError("q must have k's tokens and head size")
+        qp, qs = _rows(q, "q", dtype, qsh, dev)
+        op, os_ = _rows(q_out, "q_out", dtype, qsh, dev)
+    if rope is not None:
+        ref = rope._ref
+        if rope.turns.get_device() != dev:
+            _bad_tensor(rope.turns, "rope", dev, "on a CUDA device")
+    i32, B = torch.int32, cache.B
+    cup = _vec(cu_q, "cu_q", i32, B + 1, dev)
+    kvp = _vec(kv_len, "kv_len", i32, B, dev)
+    pp = _vec(positions, "positions", i32, T, dev)
+    cache._on(dev)
+    st = lib().medusa_rope_append(ref, qp, qs, kp, ks, vp, vs, cache.dt, pp, cup, kvp, B, T, Hq,
+                                  Hkv, dh, op, os_, cache._ref,
+                                  _vec(dev_status, "dev_status", i32, 1, dev),
+                                  _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def medusa_chunk_attention_workspace_size(Hq: int, Hkv: int, dh: int, dt: int) -> int:
@@ -644,23 +690,30 @@ def medusa_chunk_attention(q, cache: PagedCache, cu_q, kv_len, out,
     """q [T,Hq,dh] of cache.B sequences' new tokens (their k and v already in
     the cache) -> out [T,Hq,dh], each token over its sequence's slots up to its
     own."""
-    T, Hq, dh = q.shape
-    qp, qs = _rows(q, "q", cache.K.dtype)
+    dev = _dev()
+    qsh, dtype = _3d(q, "q"), cache.K.dtype
+    T, Hq, dh = qsh
     if dh != cache.dh:
         raise ValueError("q must have the cache's head size")
-    _req(out, "out")
-    if out.shape != q.shape or out.dtype is not q.dtype:
-        raise ValueError("out must have q's shape and dtype")
-    cup = _vec(cu_q, "cu_q", torch.int32, cache.B + 1)
-    kvp = _vec(kv_len, "kv_len", torch.int32, cache.B)
-    _here(q, cache.K, cu_q, kv_len, out)
-    if scale is None:
-        scale = dh ** -0.5
+    qp, qs = _rows(q, "q", dtype, qsh, dev)
+    op, os_ = _rows(out, "out", dtype, qsh, dev)
+    if os_ != Hq * dh:
+        raise ValueError("out must be dense")
+    i32, B = torch.int32, cache.B
+    cup = _vec(cu_q, "cu_q", i32, B + 1, dev)
+    kvp = _vec(kv_len, "kv_len", i32, B, dev)
+    cache._on(dev)
     if ws is None:
-        ws = workspace(medusa_chunk_attention_workspace_size(Hq, cache.Hkv, dh, cache.dt), q.device)
-    _check(lib().medusa_chunk_attention(qp, qs, cache._ref, cache.dt, cup, kvp, cache.B, T, Hq,
-                                        cache.Hkv, dh, scale, out.data_ptr(), ws.data_ptr(),
-                                        ws.numel(), _p(dev_status), _stream(stream)))
+        ws = workspace(medusa_chunk_attention_workspace_size(Hq, cache.Hkv, dh, cache.dt),
+                       cache.K.device)
+    nbytes = ws.numel()
+    st = lib().medusa_chunk_attention(qp, qs, cache._ref, cache.dt, cup, kvp, B, T, Hq, cache.Hkv,
+                                      dh, dh ** -0.5 if scale is None else scale, op,
+                                      _vec(ws, "ws", torch.uint8, nbytes, dev), nbytes,
+                                      _vec(dev_status, "dev_status", i32, 1, dev),
+                                      _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def medusa_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -668,19 +721,22 @@ def medusa_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=
     """tokens [R] int32 drawn from logits [n_rows,V] (rows may be strided) with
     uniform numbers u [R]; temperature, top_p, min_p [R] fp32 and top_k [R]
     int32 are off when None; row_idx [R] picks each draw's row."""
-    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be an [n_rows, V] CUDA tensor with dense rows")
-    n, V = logits.shape
+    dev = _dev()
+    sh = logits.shape
+    if len(sh) != 2 or logits.get_device() != dev or (sh[1] > 1 and logits.stride(1) != 1):
+        _bad_tensor(logits, "logits", dev, "an [n_rows, V] CUDA tensor with dense rows")
+    n, V = sh
     R = u.numel()
     f32, i32 = torch.float32, torch.int32
-    _here(logits, u, tokens, temperature, top_k, top_p, min_p, row_idx, kept)
-    _check(lib().medusa_sample_tokens(
+    st = lib().medusa_sample_tokens(
         logits.data_ptr(), _dt(logits), logits.stride(0) if n > 1 else V, n,
-        _vec(row_idx, "row_idx", i32, R), R, V, _vec(u, "u", f32, R),
-        _vec(temperature, "temperature", f32, R), _vec(top_k, "top_k", i32, R),
-        _vec(top_p, "top_p", f32, R), _vec(min_p, "min_p", f32, R),
-        _vec(tokens, "tokens", i32, R), _vec(kept, "kept", i32, R), _p(dev_status),
-        _stream(stream)))
+        _vec(row_idx, "row_idx", i32, R, dev), R, V, _vec(u, "u", f32, R, dev),
+        _vec(temperature, "temperature", f32, R, dev), _vec(top_k, "top_k", i32, R, dev),
+        _vec(top_p, "top_p", f32, R, dev), _vec(min_p, "min_p", f32, R, dev),
+        _vec(tokens, "tokens", i32, R, dev), _vec(kept, "kept", i32, R, dev),
+        _vec(dev_status, "dev_status", i32, 1, dev), _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def medusa_wait_flag(flag, value: int, budget_cycles: int, dev_status, stream=None) -> None:

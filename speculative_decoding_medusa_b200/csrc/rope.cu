@@ -27,6 +27,8 @@ namespace medusa {
 
 namespace {
 
+constexpr int kRopeThreads = 384;  // largest block: four of them fit on an SM
+
 struct RopeParams {
   const void *q, *k, *v;
   void *q_out, *k_out;  // k_out unused in the append
@@ -69,8 +71,35 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f(float& d, float x) { d = x; }
 
+// one thread's unit: two vectors of a q, k or v head
+struct Unit {
+  bool is_q, is_v, turns;
+  int h, un, o0, o1;  // head, unit of the head, element offsets (o1 < 0: one vector)
+};
+
+template <int VEC>
+__device__ __forceinline__ Unit unit_of(int w, int nq, int nk, const RopeParams& p) {
+  Unit u;
+  u.is_q = w < nq;
+  u.is_v = w >= nq + nk;
+  const int x = u.is_q ? w : u.is_v ? w - nq - nk : w - nq;
+  const int per = u.is_v ? p.v_units : p.units;
+  u.h = x / per;
+  u.un = x - u.h * per;
+  const int half = p.rot >> 1, rot_units = half / VEC;
+  u.turns = !u.is_v && u.un < rot_units;
+  if (u.turns) {
+    u.o0 = p.interleaved ? u.un * 2 * VEC : u.un * VEC;
+    u.o1 = p.interleaved ? u.o0 + VEC : u.o0 + half;
+  } else {
+    u.o0 = (u.is_v ? u.un : u.un - rot_units) * 2 * VEC + (u.is_v ? 0 : p.rot);
+    u.o1 = u.o0 + VEC < p.dh ? u.o0 + VEC : -1;
+  }
+  return u;
+}
+
 template <typename T, int VEC, int TB, bool kAppend>
-__global__ void __launch_bounds__(512) rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, TB == 1 ? 4 : 3) rope_kernel(RopeParams p) {
   grid_dep_wait();
   grid_dep_launch();
   using V = Vec<T, VEC>;
@@ -81,6 +110,32 @@ __global__ void __launch_bounds__(512) rope_kernel(RopeParams p) {
   const int t0 = blockIdx.x * TB;
   const int tid = threadIdx.x, lane = tid & 31;
   const int half = p.rot >> 1;
+  const int nq = p.q != nullptr ? p.Hq * p.units : 0;
+  const int nk = p.k != nullptr ? p.Hkv * p.units : 0;
+  const int total = nq + nk + (kAppend ? p.Hkv * p.v_units : 0);
+
+  // The first unit's loads go out before anything else: they depend on no
+  // metadata, and hide the chain sequence -> slot -> page -> angle behind them.
+  V a[TB], b[TB];
+  auto fetch = [&](const Unit& u) {
+    const T* src = static_cast<const T*>(u.is_q ? p.q : u.is_v ? p.v : p.k) + (size_t)u.h * p.dh;
+    const long long stride = u.is_q ? p.q_stride : u.is_v ? p.v_stride : p.k_stride;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      if (t0 + j < p.T) {
+        const T* s = src + (t0 + j) * stride;
+        a[j] = *reinterpret_cast<const V*>(s + u.o0);
+        if (u.o1 >= 0) b[j] = *reinterpret_cast<const V*>(s + u.o1);
+      }
+    }
+  };
+  int w = tid;
+  Unit u{};
+  if (w < total) {
+    u = unit_of<VEC>(w, nq, nk, p);
+    fetch(u);
+  }
+
   if (kAppend) {
     for (int j = tid >> 5; j < TB; j += blockDim.x >> 5) {
       const int t = t0 + j;
@@ -124,50 +179,19 @@ __global__ void __launch_bounds__(512) rope_kernel(RopeParams p) {
   }
   __syncthreads();
 
-  const int rot_units = half / VEC;
-  const int nq = p.q != nullptr ? p.Hq * p.units : 0;
-  const int nk = p.k != nullptr ? p.Hkv * p.units : 0;
-  const int nv = kAppend ? p.Hkv * p.v_units : 0;
-  for (int w = tid; w < nq + nk + nv; w += blockDim.x) {
-    // which tensor, head and unit (the same for all TB tokens)
-    const bool is_q = w < nq, is_v = w >= nq + nk;
-    const int x = is_q ? w : is_v ? w - nq - nk : w - nq;
-    const int per = is_v ? p.v_units : p.units;
-    const int h = x / per, un = x - h * per;
-    const bool turns = !is_v && un < rot_units;
-    int o0, o1;  // element offsets of the unit's two vectors (o1 < 0: only one)
-    if (turns) {
-      o0 = p.interleaved ? un * 2 * VEC : un * VEC;
-      o1 = p.interleaved ? o0 + VEC : o0 + half;
-    } else {
-      o0 = (is_v ? un : un - rot_units) * 2 * VEC + (is_v ? 0 : p.rot);
-      o1 = o0 + VEC < p.dh ? o0 + VEC : -1;
-    }
-    const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) + (size_t)h * p.dh;
-    const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
-    V a[TB], b[TB];
+  while (w < total) {
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
-      if (s_state[j] != 0) {
-        const T* s = src + (t0 + j) * stride;
-        a[j] = *reinterpret_cast<const V*>(s + o0);
-        if (o1 >= 0) b[j] = *reinterpret_cast<const V*>(s + o1);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      if (s_state[j] == 0) continue;
+      if (s_state[j] == 0 || (kAppend && !u.is_q && s_state[j] != 3)) continue;
       T* dst;
-      if (is_q) {
-        dst = static_cast<T*>(p.q_out) + (t0 + j) * p.q_out_stride + (size_t)h * p.dh;
-      } else if (kAppend) {
-        if (s_state[j] != 3) continue;
-        dst = static_cast<T*>(is_v ? p.V : p.K) + (s_dst[j] + (long long)h * p.page_size) * p.dh;
-      } else {
-        dst = static_cast<T*>(p.k_out) + (t0 + j) * p.k_out_stride + (size_t)h * p.dh;
-      }
-      if (turns) {
-        const float2* f = cs + j * half + un * VEC;
+      if (u.is_q)
+        dst = static_cast<T*>(p.q_out) + (t0 + j) * p.q_out_stride + (size_t)u.h * p.dh;
+      else if (kAppend)
+        dst = static_cast<T*>(u.is_v ? p.V : p.K) + (s_dst[j] + (long long)u.h * p.page_size) * p.dh;
+      else
+        dst = static_cast<T*>(p.k_out) + (t0 + j) * p.k_out_stride + (size_t)u.h * p.dh;
+      if (u.turns) {
+        const float2* f = cs + j * half + u.un * VEC;
         if (p.interleaved) {
           T z[2 * VEC];
 #pragma unroll
@@ -195,8 +219,13 @@ __global__ void __launch_bounds__(512) rope_kernel(RopeParams p) {
           }
         }
       }
-      *reinterpret_cast<V*>(dst + o0) = a[j];
-      if (o1 >= 0) *reinterpret_cast<V*>(dst + o1) = b[j];
+      *reinterpret_cast<V*>(dst + u.o0) = a[j];
+      if (u.o1 >= 0) *reinterpret_cast<V*>(dst + u.o1) = b[j];
+    }
+    w += blockDim.x;
+    if (w < total) {
+      u = unit_of<VEC>(w, nq, nk, p);
+      fetch(u);
     }
   }
 }
@@ -230,14 +259,14 @@ medusa_status_t launch_vec(RopeParams& p, cudaStream_t stream) {
   p.v_units = (p.dh + 2 * VEC - 1) / (2 * VEC);
   const int work = (p.q ? p.Hq * p.units : 0) + (p.k ? p.Hkv * p.units : 0) +
                    (kAppend ? p.Hkv * p.v_units : 0);
-  const int rounds = (work + 511) / 512;
+  const int rounds = (work + kRopeThreads - 1) / kRopeThreads;
   const int threads = ((work + rounds - 1) / rounds + 31) / 32 * 32;
-  // four tokens a block once that still leaves several blocks per SM
-  if (p.T >= 4 * 4 * device_sm_count())
-    launch(rope_kernel<T, VEC, 4, kAppend>, (p.T + 3) / 4, threads, 4 * (p.rot / 2) * sizeof(float2),
-           stream, p);
+  const size_t table = (p.rot / 2) * sizeof(float2);
+  // two tokens a block once one a block fills the machine twice over
+  if (p.T >= 2 * 4 * device_sm_count())
+    launch(rope_kernel<T, VEC, 2, kAppend>, (p.T + 1) / 2, threads, 2 * table, stream, p);
   else
-    launch(rope_kernel<T, VEC, 1, kAppend>, p.T, threads, (p.rot / 2) * sizeof(float2), stream, p);
+    launch(rope_kernel<T, VEC, 1, kAppend>, p.T, threads, table, stream, p);
   return check_launch(kAppend ? "rope_append" : "rope");
 }
 

@@ -2,26 +2,30 @@
 // the caller's uniform numbers.
 //
 // Every filter keeps a prefix of the row's tokens in the order (logit
-// descending, id ascending), so the kept set is a cut: a key and how many of
-// the tokens with exactly that key (lowest ids) stay.  The cut is found by
-// selection, never by sorting the row:
-//   - a histogram of the row over kBins bins of falling logit, with token
-//     counts and (for top-p) their mass;
+// descending, id ascending), so the kept set is a cut: a key (the logit as an
+// ordered integer) and the last id that stays among the tokens with exactly
+// that key.  The cut is found by selection, never by sorting the row:
+//   - a histogram of the row over kBins bins of falling logit: token counts
+//     for top-k, mass for top-p;
 //   - the bin where the count reaches top_k, or the mass before it reaches
 //     top_p of the total;
-//   - inside that bin the exact key: a short list of its keys ranked against
-//     one another, or, when the bin holds too many, histograms over its own
-//     key range until it is short or a single key is left.
-// min-p is a bound on the exponent and needs no selection.
+//   - inside that bin the exact cut: its tokens go on a short list and are
+//     ranked against one another; a bin that holds too many is split by
+//     histograms over its own key range until it is short or one key is left.
+// min-p is a bound on the logit and needs no selection.
 //
 // Masses are exact: w = exp((z - max) / T) is rounded once to 64-bit fixed
 // point (units of 2^-42 of the largest weight, which is 1), and integers add
 // up the same in any order, so a draw is the same however the row is split
-// and a token is decided as in a 64-bit sum up to 2^-43 per token.  A fp32 sum
+// and a token is decided as in a 64-bit sum up to 2^-42 per token.  A fp32 sum
 // over a vocabulary of 128256 decides one draw in about a hundred differently.
 //
 // A row belongs to a cluster of thread blocks that hold it in shared memory:
-// it is read from HBM once, and every later pass runs on the copy.
+// it is read from HBM once, and every later pass runs on the copy.  What the
+// blocks tell one another they push into every block's shared memory before a
+// cluster barrier and then evaluate redundantly, so a step costs one barrier
+// and no broadcast: extremes; group sums of the histogram; the short list;
+// kept masses.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,9 +44,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kShort = 512;       // keys a bin may hold to be ranked directly
+constexpr int kGroups = kBins / 32;
+constexpr int kShort = 128;  // tokens a block may put on the short list
 constexpr int kMaxCluster = 8;
-constexpr double kUnit = 4398046511104.0;  // 2^42: weight 1 in fixed point
+constexpr int kExpTable = 256;
+constexpr uint32_t kLowestKey = 0x00800000u;  // key of the lowest finite float
 
 struct SampleParams {
   const void* logits;
@@ -54,13 +60,21 @@ struct SampleParams {
   int32_t *tokens, *kept, *status;
 };
 
-// order-preserving integer of a finite float or -inf; -0 counts as +0
+// order-preserving integer of a float; -0 counts as +0
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// A finite float as a double by its bits; zero and subnormals become values
+// of that size (below 2^-126), which no logit difference notices.
+__device__ __forceinline__ double widen(float z) {
+  const uint32_t b = __float_as_uint(z);
+  const uint32_t hi = ((b >> 3) & 0x0fffffffu) + 0x38000000u;
+  return __hiloint2double(static_cast<int>(hi | (b & 0x80000000u)), static_cast<int>(b << 29));
 }
 
 template <typename T>
@@ -90,43 +104,80 @@ struct Elem<__nv_bfloat16> {
   static constexpr uint32_t kNegInf = 0xff80ff80u;
 };
 
+// The weight exp((z - max) / T) in units of 2^-42: 2^y with y = (z - max) *
+// log2(e) / T split as y = n + j / 256 + r / 256, |r| <= 1/2: a table of
+// 2^(j / 256) and the Taylor polynomial of 2^(r / 256) to the third power
+// (the fourth term is below 2^-42).  Ten fp64 operations and a table read;
+// the rounding to an integer is the addition of 1.5 * 2^10, whose last bit
+// is 2^-42.
+struct Weight {
+  const double* table;
+  double zmax, c;  // c: 256 * log2(e) / T
+
+  __device__ __forceinline__ unsigned long long operator()(float z) const {
+    constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52
+    constexpr double kRound = 1536.0;              // 1.5 * 2^10
+    constexpr double kL = 2.7076061740622863e-3;   // ln 2 / 256
+    const double dz = widen(z) - zmax;
+    const double kd = fma(dz, c, kMagic);
+    const int k = __double2loint(kd);
+    const double kf = kd - kMagic;
+    const double r = fma(dz, c, -kf);
+    const double t = table[k & (kExpTable - 1)];
+    const double q = fma(fma(kL * kL * kL / 6.0, r, kL * kL / 2.0), r, kL);
+    double v = fma(t * r, q, t);
+    v = __hiloint2double(__double2hiint(v) + (k >> 8) * (1 << 20), __double2loint(v));
+    const unsigned long long w = static_cast<unsigned long long>(
+        __double_as_longlong(v + kRound) - __double_as_longlong(kRound));
+    // below 2^-44 of the largest: nothing
+    return kf < -44.0 * kExpTable ? 0ull : w;
+  }
+};
+
 // what a block tells the others of its cluster
 struct Extremes {
   float hi, lo;  // largest logit, smallest finite logit
   int arg;       // lowest id of the largest
   int bad;       // a NaN or +inf
 };
-struct Totals {
+struct Sums {
   unsigned long long mass;
   unsigned int count;
-  int first;  // lowest kept id
+  int first;  // draw: lowest kept id
 };
-struct Found {
-  unsigned long long mass;  // before the bin (or key)
+struct Bin {
+  unsigned long long mass;  // before it
+  unsigned long long limit;
   unsigned int count;
-  unsigned int n;  // tokens in the bin (or with the key)
-  uint32_t bin;    // bin, or cut key
-  uint32_t m;      // tokens of the cut key that stay
+  uint32_t bin;
+};
+struct Cut {
+  unsigned long long mass;  // of the tokens that stay
+  uint32_t key;             // of the last of them
+  int id;
 };
 
 struct Shared {
   Extremes ext[kMaxCluster];
-  Totals chunk[kMaxCluster];   // histogram chunk totals
-  Totals part[kMaxCluster];    // draw: kept mass of each block
-  unsigned int ties[kMaxCluster];
+  Sums group[kMaxCluster][kGroups];
+  Sums part[kMaxCluster];
+  unsigned long long mine[kShort];  // short list: key and complemented id
+  unsigned long long list[kMaxCluster][kShort];
+  unsigned long long sorted[kMaxCluster * kShort];
+  unsigned int list_n[kMaxCluster];
   uint32_t kmin[kMaxCluster], kmax[kMaxCluster];
-  Found found;
-  unsigned int n_list;
-  uint32_t list[kShort];
-  unsigned long long list_w[kShort];
+  double table[kExpTable];
+  Bin bin;
+  Cut cut;
+  unsigned int n_local;
+  int cut_id;
   unsigned long long red64[kWarps];
   unsigned int red32[kWarps], red32b[kWarps];
   float redf[kWarps], redg[kWarps];
-  uint32_t best_key;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams p) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int VE = Elem<T>::kVec;
@@ -143,10 +194,6 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
   uint32_t* h_cnt = reinterpret_cast<uint32_t*>(dyn + (size_t)n_vec * 16);
   uint32_t* h_lo = h_cnt + kBins;
   uint32_t* h_hi = h_lo + kBins;
-  const int per = kBins / C;  // bins of a chunk
-  // the cluster's sums over the chunk of bins this block owns
-  unsigned long long* c_mass = reinterpret_cast<unsigned long long*>(h_hi + kBins);
-  uint32_t* c_cnt = reinterpret_cast<uint32_t*>(c_mass + per);
   __shared__ Shared sh;
 
   const float temp = p.temperature != nullptr ? p.temperature[r] : 1.f;
@@ -156,8 +203,7 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
   const float min_p = p.min_p != nullptr ? p.min_p[r] : 0.f;
   const int src_row = p.row_idx != nullptr ? p.row_idx[r] : r;
   bool bad = !(u >= 0.f && u < 1.f) || !(temp >= 0.f) || !(top_p >= 0.f) ||
-             !(min_p >= 0.f && min_p <= 1.f) ||
-             src_row < 0 || src_row >= p.n_rows || isinf(temp);
+             !(min_p >= 0.f && min_p <= 1.f) || src_row < 0 || src_row >= p.n_rows || isinf(temp);
 
   // ---- the slice into shared memory; extremes ----
   // Blocks split the row at 16-byte boundaries of its address: element i of
@@ -170,31 +216,56 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
     const T* row = static_cast<const T*>(p.logits) + (size_t)src_row * p.row_stride;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % VE);
     base = rank * p.slice - off;  // token id of the slice's first element
-    for (int v = tid; v < n_vec; v += kThreads) {
-      const int id = base + v * VE;
-      uint4 raw;
-      if (id >= 0 && id + VE <= p.V) {
-        raw = __ldg(reinterpret_cast<const uint4*>(row + id));
-      } else {
-        raw = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
-        T* e = reinterpret_cast<T*>(&raw);
-        for (int i = 0; i < VE; ++i)
-          if (id + i >= 0 && id + i < p.V) e[i] = row[id + i];
-      }
-      slice[v] = raw;
-      float z[VE];
-      Elem<T>::unpack(raw, z);
+    constexpr int kFetch = 4;     // vectors a thread has in flight
+    for (int v0 = tid; v0 < n_vec; v0 += kFetch * kThreads) {
+      uint4 raw[kFetch];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        if (!(z[i] < INFINITY)) nan = true;
-        if (z[i] > hi) {
-          hi = z[i];
-          arg = id + i;
+      for (int f = 0; f < kFetch; ++f) {
+        const int v = v0 + f * kThreads, id = base + v * VE;
+        raw[f] = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
+        if (v < n_vec) {
+          if (id >= 0 && id + VE <= p.V) {
+            raw[f] = __ldg(reinterpret_cast<const uint4*>(row + id));
+          } else {
+            uint32_t w[4] = {raw[f].x, raw[f].y, raw[f].z, raw[f].w};
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+              if (id + i >= 0 && id + i < p.V) {
+                if (sizeof(T) == 4) {
+                  w[i % 4] = reinterpret_cast<const uint32_t*>(row)[id + i];
+                } else {
+                  const uint32_t x = reinterpret_cast<const uint16_t*>(row)[id + i];
+                  w[(i / 2) % 4] = (i & 1) ? (w[(i / 2) % 4] & 0xffffu) | (x << 16)
+                                           : (w[(i / 2) % 4] & 0xffff0000u) | x;
+                }
+              }
+            }
+            raw[f] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        if (z[i] > -INFINITY) lo = fminf(lo, z[i]);
+      }
+      // the table of powers, while the first loads are under way
+      if (v0 < kExpTable) sh.table[v0] = exp2((double)v0 / kExpTable);
+#pragma unroll
+      for (int f = 0; f < kFetch; ++f) {
+        const int v = v0 + f * kThreads;
+        if (v >= n_vec) break;
+        slice[v] = raw[f];
+        float z[VE];
+        Elem<T>::unpack(raw[f], z);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          if (!(z[i] < INFINITY)) nan = true;
+          if (z[i] > hi) {
+            hi = z[i];
+            arg = base + v * VE + i;
+          }
+          if (z[i] > -INFINITY) lo = fminf(lo, z[i]);
+        }
       }
     }
   }
+  if (tid >= n_vec && tid < kExpTable) sh.table[tid] = exp2((double)tid / kExpTable);
   for (int o = 16; o > 0; o >>= 1) {
     const float oh = __shfl_xor_sync(0xffffffffu, hi, o);
     const int oa = __shfl_xor_sync(0xffffffffu, arg, o);
@@ -248,13 +319,9 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
     return;  // the whole cluster takes this branch, after its last exchange
   }
 
-  const double zmax = hi;
   const double c_log2 = 1.4426950408889634074 / (double)temp;  // log2(e) / T
-  auto exponent = [&](float z) { return ((double)z - zmax) * c_log2; };
-  auto weight = [&](float z) -> unsigned long long {
-    const double y = exponent(z);
-    return y < -43.5 ? 0ull : __double2ull_rn(exp2(y) * kUnit);
-  };
+  const double zmax = widen(hi);
+  const Weight weight{sh.table, zmax, c_log2 * kExpTable};
   // bins of level 0: linear in the logit, over the range that can carry mass
   // or, if that is smaller, the row's own
   const float range = fminf(hi - zlo, 32.f * temp);
@@ -265,10 +332,11 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
   const bool by_k = top_k > 0 && top_k < p.V;
   const bool by_p = top_p < 1.f;
 
-  // one histogram over the cluster: `pick(z, key, bin)` says whether a token
-  // counts and in which bin.  Leaves the chunk sums in c_cnt / c_mass and every
-  // chunk's totals in sh.chunk.
-  auto histogram = [&](auto pick) {
+  // One histogram over the cluster: `pick(z, bin)` says whether a finite
+  // logit counts and in which bin.  Afterwards every block holds every
+  // block's sums of each group of 32 bins, and the blocks' own bins stay in
+  // place for find().
+  auto histogram = [&](bool counts, bool masses, auto pick) {
     for (int i = tid; i < kBins; i += kThreads) {
       h_cnt[i] = 0u;
       h_lo[i] = 0u;
@@ -278,208 +346,295 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
     for (int v = tid; v < n_vec; v += kThreads) {
       float z[VE];
       Elem<T>::unpack(slice[v], z);
+      // four independent weights at a time, then their additions
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        uint32_t bin;
-        if (z[i] > -INFINITY && pick(z[i], bin)) {
-          atomicAdd(&h_cnt[bin], 1u);
-          if (by_p) {
-            const unsigned long long w = weight(z[i]);
-            const uint32_t wl = static_cast<uint32_t>(w);
-            uint32_t wh = static_cast<uint32_t>(w >> 32);
-            if (wl != 0u && atomicAdd(&h_lo[bin], wl) + wl < wl) ++wh;
-            if (wh != 0u) atomicAdd(&h_hi[bin], wh);
+      for (int i0 = 0; i0 < VE; i0 += 4) {
+        uint32_t bin[4];
+        bool in[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) in[i] = z[i0 + i] > -INFINITY && pick(z[i0 + i], bin[i]);
+        if (masses) {
+          unsigned long long w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
+          // two 32-bit words with a carry (64-bit shared-memory additions
+          // measured 1.5 times slower)
+          uint32_t old[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            old[i] = in[i] && w[i] != 0ull ? atomicAdd(&h_lo[bin[i]], static_cast<uint32_t>(w[i])) : 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t wh = static_cast<uint32_t>(w[i] >> 32) +
+                                (old[i] + static_cast<uint32_t>(w[i]) < old[i] ? 1u : 0u);
+            if (in[i] && wh != 0u) atomicAdd(&h_hi[bin[i]], wh);
           }
         }
+        if (counts) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (in[i]) atomicAdd(&h_cnt[bin[i]], 1u);
+        }
       }
-    }
-    cluster.sync();
-    // sum of this block's chunk over the cluster
-    unsigned long long mass = 0ull;
-    unsigned int count = 0u;
-    for (int i = tid; i < per; i += kThreads) {
-      const int bin = rank * per + i;
-      unsigned int n = 0u;
-      unsigned long long m = 0ull;
-      for (int c = 0; c < C; ++c) {
-        n += cluster.map_shared_rank(h_cnt, c)[bin];
-        if (by_p)
-          m += (static_cast<unsigned long long>(cluster.map_shared_rank(h_hi, c)[bin]) << 32) +
-               cluster.map_shared_rank(h_lo, c)[bin];
-      }
-      c_cnt[i] = n;
-      c_mass[i] = m;
-      count += n;
-      mass += m;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-      mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    }
-    if (lane == 0) {
-      sh.red32[warp] = count;
-      sh.red64[warp] = mass;
     }
     __syncthreads();
-    if (tid < C) {
-      Totals t{0ull, 0u, 0};
-      for (int w = 0; w < kWarps; ++w) {
-        t.count += sh.red32[w];
-        t.mass += sh.red64[w];
-      }
-      *cluster.map_shared_rank(&sh.chunk[rank], tid) = t;
+    for (int g = warp; g < kGroups; g += kWarps) {
+      const int bin = g * 32 + lane;
+      const unsigned int n = __reduce_add_sync(0xffffffffu, h_cnt[bin]);
+      unsigned long long m = (static_cast<unsigned long long>(h_hi[bin]) << 32) + h_lo[bin];
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane < C) *cluster.map_shared_rank(&sh.group[rank][g], lane) = Sums{m, n, 0};
     }
     cluster.sync();
   };
 
-  // the last bin with tokens before which the count (or the mass) is below
-  // `limit`, given what lies before the histogram's range; told to every block
-  auto find_bin = [&](bool mass_mode, unsigned long long limit, unsigned int count0,
-                      unsigned long long mass0) -> Found {
-    unsigned int cb = count0, mine_c = 0u;
-    unsigned long long mb = mass0, mine_m = 0ull;
-    int owner = -1;
-    for (int c = 0; c < C; ++c) {
-      const Totals t = sh.chunk[c];
-      if (t.count > 0u && (mass_mode ? mb : (unsigned long long)cb) < limit) {
-        owner = c;
-        mine_c = cb;
-        mine_m = mb;
+  // The last bin with tokens before which the count (or the mass) is below
+  // `limit`, given what lies before the histogram's range.  In mass mode
+  // limit 0 stands for top_p of the histogram's own total.
+  auto p_limit = [&](unsigned long long total) {
+    // kept while the mass before is below top_p * total: an integer limit
+    return max(1ull, static_cast<unsigned long long>(ceil((double)top_p * (double)total)));
+  };
+  auto find = [&](bool by_mass, unsigned long long limit, unsigned int count0,
+                  unsigned long long mass0) -> Bin {
+    static_assert(kGroups == 64, "two groups per lane");
+    if (warp == 0) {
+      Sums s[2];
+      for (int x = 0; x < 2; ++x) {
+        s[x] = Sums{0ull, 0u, 0};
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          if (c >= C) break;
+          const Sums t = sh.group[c][2 * lane + x];
+          s[x].mass += t.mass;
+          s[x].count += t.count;
+        }
       }
-      cb += t.count;
-      mb += t.mass;
-    }
-    if (rank == owner) {
-      // thread t scans bins t * each .. of the chunk
-      const int each = (per + kThreads - 1) / kThreads;
-      unsigned int n = 0u;
-      unsigned long long m = 0ull;
-      for (int i = tid * each; i < min(per, (tid + 1) * each); ++i) {
-        n += c_cnt[i];
-        m += c_mass[i];
-      }
-      unsigned int sn = n;
-      unsigned long long sm = m;
+      // exclusive prefix over the lanes
+      unsigned long long m = s[0].mass + s[1].mass;
+      unsigned int n = s[0].count + s[1].count;
+      const unsigned long long own_m = m;
+      const unsigned int own_n = n;
       for (int o = 1; o < 32; o <<= 1) {
-        const unsigned int a = __shfl_up_sync(0xffffffffu, sn, o);
-        const unsigned long long b = __shfl_up_sync(0xffffffffu, sm, o);
+        const unsigned long long a = __shfl_up_sync(0xffffffffu, m, o);
+        const unsigned int b = __shfl_up_sync(0xffffffffu, n, o);
         if (lane >= o) {
-          sn += a;
-          sm += b;
+          m += a;
+          n += b;
         }
       }
-      if (lane == 31) {
-        sh.red32[warp] = sn;
-        sh.red64[warp] = sm;
-      }
-      if (tid == 0) sh.best_key = 0u;
-      __syncthreads();
-      unsigned int before_n = mine_c + sn - n;
-      unsigned long long before_m = mine_m + sm - m;
-      for (int w = 0; w < warp; ++w) {
-        before_n += sh.red32[w];
-        before_m += sh.red64[w];
-      }
-      int best = -1;
-      Found f{};
-      for (int i = tid * each; i < min(per, (tid + 1) * each); ++i) {
-        if (c_cnt[i] > 0u && (mass_mode ? before_m : (unsigned long long)before_n) < limit) {
-          best = i;
-          f = Found{before_m, before_n, c_cnt[i], static_cast<uint32_t>(rank * per + i), 0u};
+      if (limit == 0ull) limit = p_limit(__shfl_sync(0xffffffffu, m, 31));
+      m += mass0 - own_m;
+      n += count0 - own_n;
+      // this lane's later qualifying group, if any
+      int g = -1;
+      unsigned long long gm = 0ull;
+      unsigned int gn = 0u;
+      for (int x = 0; x < 2; ++x) {
+        const bool some = by_mass ? s[x].mass > 0ull : s[x].count > 0u;
+        if (some && (by_mass ? m : (unsigned long long)n) < limit) {
+          g = 2 * lane + x;
+          gm = m;
+          gn = n;
         }
-        before_n += c_cnt[i];
-        before_m += c_mass[i];
+        m += s[x].mass;
+        n += s[x].count;
       }
-      if (best >= 0) atomicMax(&sh.best_key, static_cast<uint32_t>(best + 1));
-      __syncthreads();
-      if (best >= 0 && sh.best_key == static_cast<uint32_t>(best + 1))
-        for (int c = 0; c < C; ++c) *cluster.map_shared_rank(&sh.found, c) = f;
+      const unsigned int votes = __ballot_sync(0xffffffffu, g >= 0);
+      const int from = 31 - __clz(votes);  // the first bin of all always qualifies
+      g = __shfl_sync(0xffffffffu, g, from);
+      gm = __shfl_sync(0xffffffffu, gm, from);
+      gn = __shfl_sync(0xffffffffu, gn, from);
+      // its 32 bins over the cluster
+      const int bin = g * 32 + lane;
+      uint32_t rn[kMaxCluster], rl[kMaxCluster], rh[kMaxCluster];  // all reads in flight
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        rn[c] = c < C ? cluster.map_shared_rank(h_cnt, c)[bin] : 0u;
+        rl[c] = c < C ? cluster.map_shared_rank(h_lo, c)[bin] : 0u;
+        rh[c] = c < C ? cluster.map_shared_rank(h_hi, c)[bin] : 0u;
+      }
+      m = 0ull;
+      n = 0u;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        m += (static_cast<unsigned long long>(rh[c]) << 32) + rl[c];
+        n += rn[c];
+      }
+      const bool some = by_mass ? m > 0ull : n > 0u;
+      const unsigned long long bm = m;
+      const unsigned int bn = n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xffffffffu, m, o);
+        const unsigned int b = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) {
+          m += a;
+          n += b;
+        }
+      }
+      m += gm - bm;
+      n += gn - bn;
+      const bool in = some && (by_mass ? m : (unsigned long long)n) < limit;
+      const unsigned int bins = __ballot_sync(0xffffffffu, in);
+      if (lane == 31 - __clz(bins)) sh.bin = Bin{m, limit, n, static_cast<uint32_t>(bin)};
     }
-    cluster.sync();
-    const Found f = sh.found;
-    cluster.sync();
-    return f;
+    __syncthreads();
+    const Bin b = sh.bin;
+    __syncthreads();
+    return b;
   };
 
-  // tokens of equal key and weight w that stay when `before` lies ahead of them
-  auto ties_kept = [&](bool mass_mode, unsigned long long limit, unsigned int count,
+  // tokens of one key, n of them with weight w each, that stay
+  auto ties_kept = [&](bool by_mass, unsigned long long limit, unsigned int count,
                        unsigned long long mass, unsigned int n, unsigned long long w) {
-    if (!mass_mode) return static_cast<uint32_t>(min((unsigned long long)n, limit - count));
+    if (!by_mass) return static_cast<unsigned int>(min((unsigned long long)n, limit - count));
     if (w == 0ull) return n;
-    return static_cast<uint32_t>(min((unsigned long long)n, (limit - mass + w - 1) / w));
+    return static_cast<unsigned int>(min((unsigned long long)n, (limit - mass + w - 1) / w));
   };
 
-  // The exact cut inside bin f of the current histogram; pred(z, key) tells
-  // the bin's tokens.  Returns {mass, count before the key, n with the key,
-  // key, m kept}.
-  auto resolve = [&](bool mass_mode, unsigned long long limit, Found f) -> Found {
+  // The exact cut inside bin b of the current histogram.
+  bool crowded = false;  // a crowded bin has used the histogram
+  auto resolve = [&](bool by_mass, Bin b, bool again) -> Cut {
+    const unsigned long long limit = b.limit;
     bool level0 = true;
     uint32_t plo = 0u, phi = 0xffffffffu;  // key interval of the bin (levels >= 1)
     for (;;) {
       auto in_bin = [&](float z) {
-        if (level0) return bin0(z) == f.bin;
+        if (!(z > -INFINITY)) return false;
+        if (level0) return bin0(z) == b.bin;
         const uint32_t k = key_of(z);
         return k >= plo && k <= phi;
       };
-      if (f.n <= kShort) {
-        if (tid == 0) sh.n_list = 0u;
-        cluster.sync();
-        unsigned int* n_list = cluster.map_shared_rank(&sh.n_list, 0);
-        uint32_t* list = cluster.map_shared_rank(sh.list, 0);
-        for (int v = tid; v < n_vec; v += kThreads) {
-          float z[VE];
-          Elem<T>::unpack(slice[v], z);
+      // the bin's tokens onto the list of every block
+      if (tid == 0) sh.n_local = 0u;
+      __syncthreads();
+      for (int v = tid; v < n_vec; v += kThreads) {
+        float z[VE];
+        Elem<T>::unpack(slice[v], z);
 #pragma unroll
-          for (int i = 0; i < VE; ++i)
-            if (z[i] > -INFINITY && in_bin(z[i])) {
-              const unsigned int at = atomicAdd(n_list, 1u);
-              if (at < kShort) list[at] = key_of(z[i]);
-            }
+        for (int i = 0; i < VE; ++i)
+          if (in_bin(z[i])) {
+            const unsigned int at = atomicAdd(&sh.n_local, 1u);
+            if (at < (unsigned int)kShort)
+              sh.mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
+                            (0xffffffffu - static_cast<uint32_t>(base + v * VE + i));
+          }
+      }
+      __syncthreads();
+      if (tid < C) *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local;
+      {
+        const int n = static_cast<int>(min(sh.n_local, (unsigned int)kShort));
+        for (int e = tid; e < n * C; e += kThreads) {
+          const int c = e / n, i = e - c * n;
+          *cluster.map_shared_rank(&sh.list[rank][i], c) = sh.mine[i];
         }
-        cluster.sync();
-        if (rank == 0) {
-          const int n = static_cast<int>(min(sh.n_list, (unsigned int)kShort));
-          for (int i = tid; i < n; i += kThreads) sh.list_w[i] = weight(value_of(sh.list[i]));
-          if (tid == 0) sh.best_key = 0xffffffffu;
-          __syncthreads();
-          Found g{};
-          bool ok = false;
-          if (tid < n) {  // kShort == kThreads: one key per thread
-            const uint32_t k = sh.list[tid];
-            unsigned int ahead = 0u, same = 0u;
-            unsigned long long ahead_m = 0ull;
-            for (int j = 0; j < n; ++j) {
-              const uint32_t kj = sh.list[j];
-              if (kj > k) {
-                ++ahead;
-                ahead_m += sh.list_w[j];
-              }
-              same += kj == k ? 1u : 0u;
-            }
-            g = Found{f.mass + ahead_m, f.count + ahead, same, k, 0u};
-            ok = (mass_mode ? g.mass : (unsigned long long)g.count) < limit;
-            if (ok) {
-              g.m = ties_kept(mass_mode, limit, g.count, g.mass, same, sh.list_w[tid]);
-              atomicMin(&sh.best_key, k);
+      }
+      cluster.sync();
+      bool fits = true;
+      unsigned int n = 0u;
+      for (int c = 0; c < C; ++c) {
+        fits = fits && sh.list_n[c] <= (unsigned int)kShort;
+        n += sh.list_n[c];
+      }
+      if (fits) {
+        // All of the bin, sorted into the order of the tokens: words of key
+        // and complemented id, largest first.  Thread t holds word t (and
+        // t + kThreads when there are more); a bitonic network exchanges them
+        // by shuffles, and through shared memory for distances of a warp or
+        // more.
+        int size = 32;
+        while (size < (int)n) size <<= 1;
+        {
+          unsigned int at = 0u;
+          for (int c = 0; c < C; ++c) {
+            for (int i = tid; i < (int)sh.list_n[c]; i += kThreads) sh.sorted[at + i] = sh.list[c][i];
+            at += sh.list_n[c];
+          }
+          for (int i = n + tid; i < size; i += kThreads) sh.sorted[i] = 0ull;
+        }
+        __syncthreads();
+        const bool wide = size > kThreads;
+        const bool act = warp * 32 < size;
+        unsigned long long e0 = act ? sh.sorted[tid] : 0ull;
+        unsigned long long e1 = wide ? sh.sorted[tid + kThreads] : 0ull;
+        auto keep = [&](unsigned long long mine, unsigned long long other, int x, int k, int j) {
+          const bool larger = ((x & j) == 0) == ((x & k) == 0);
+          return (mine > other) == larger ? mine : other;
+        };
+        for (int k = 2; k <= size; k <<= 1) {
+          for (int j = k >> 1; j > 0; j >>= 1) {
+            if (j == kThreads) {  // the thread's own two words
+              const unsigned long long a = keep(e0, e1, tid, k, j);
+              e1 = keep(e1, e0, tid + kThreads, k, j);
+              e0 = a;
+            } else if (j >= 32) {
+              __syncthreads();
+              if (act) sh.sorted[tid] = e0;
+              if (wide) sh.sorted[tid + kThreads] = e1;
+              __syncthreads();
+              if (act) e0 = keep(e0, sh.sorted[tid ^ j], tid, k, j);
+              if (wide) e1 = keep(e1, sh.sorted[(tid + kThreads) ^ j], tid + kThreads, k, j);
+            } else if (act) {
+              e0 = keep(e0, __shfl_xor_sync(0xffffffffu, e0, j), tid, k, j);
+              if (wide) e1 = keep(e1, __shfl_xor_sync(0xffffffffu, e1, j), tid + kThreads, k, j);
             }
           }
-          __syncthreads();
-          if (ok && sh.best_key == g.bin)  // several threads may hold equal copies
-            for (int c = 0; c < C; ++c) *cluster.map_shared_rank(&sh.found, c) = g;
         }
-        cluster.sync();
-        const Found g = sh.found;
-        cluster.sync();
-        return g;
+        __syncthreads();
+        if (act) sh.sorted[tid] = e0;
+        if (wide) sh.sorted[tid + kThreads] = e1;
+        __syncthreads();
+        // mass before each token: two tokens a thread
+        unsigned long long w[2] = {0ull, 0ull};
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (by_p && 2 * tid + x < (int)n)
+            w[x] = weight(value_of(static_cast<uint32_t>(sh.sorted[2 * tid + x] >> 32)));
+        unsigned long long m = w[0] + w[1];
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, m, o);
+          if (lane >= o) m += y;
+        }
+        if (lane == 31) sh.red64[warp] = m;
+        __syncthreads();
+        m += b.mass - w[0] - w[1];
+        for (int x = 0; x < warp; ++x) m += sh.red64[x];
+        // the last token that stays: one thread holds it
+        int last = -1;
+        unsigned long long mass = 0ull;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int i = 2 * tid + x;
+          if (i < (int)n && (by_mass ? m : (unsigned long long)b.count + i) < limit) {
+            last = i;
+            mass = m + w[x];
+          }
+          m += w[x];
+        }
+        const unsigned int votes = __ballot_sync(0xffffffffu, last >= 0);
+        if (votes != 0u && lane == 31 - __clz(votes)) sh.red32[warp] = last + 1;
+        if (votes == 0u && lane == 0) sh.red32[warp] = 0u;
+        __syncthreads();
+        unsigned int best = 0u;
+        for (int x = 0; x < kWarps; ++x) best = max(best, sh.red32[x]);
+        if (last >= 0 && (unsigned int)last + 1u == best) {
+          const unsigned long long e = sh.sorted[last];
+          sh.cut = Cut{mass, static_cast<uint32_t>(e >> 32),
+                       static_cast<int>(0xffffffffu - static_cast<uint32_t>(e))};
+        }
+        __syncthreads();
+        const Cut cut = sh.cut;
+        if (again) cluster.sync();  // the lists will be written again
+        return cut;
       }
-      // a crowded bin: its key range, then a histogram over that range
+      // a crowded bin: its key range
       uint32_t kmin = 0xffffffffu, kmax = 0u;
       for (int v = tid; v < n_vec; v += kThreads) {
         float z[VE];
         Elem<T>::unpack(slice[v], z);
 #pragma unroll
         for (int i = 0; i < VE; ++i)
-          if (z[i] > -INFINITY && in_bin(z[i])) {
+          if (in_bin(z[i])) {
             const uint32_t k = key_of(z[i]);
             kmin = min(kmin, k);
             kmax = max(kmax, k);
@@ -508,220 +663,223 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(SampleParams p)
         kmax = max(kmax, sh.kmax[c]);
       }
       if (kmin == kmax) {
-        f.bin = kmin;
-        f.m = ties_kept(mass_mode, limit, f.count, f.mass, f.n, weight(value_of(kmin)));
-        return f;
+        // one key: the id of the last of its tokens that stay, by counting
+        const unsigned long long w = weight(value_of(kmin));
+        const unsigned int m = ties_kept(by_mass, limit, b.count, b.mass, n, w);
+        unsigned int before = 0u;
+        int owner = 0;
+        for (int c = 0; c < C; ++c) {
+          if (before + sh.list_n[c] >= m) break;
+          before += sh.list_n[c];
+          ++owner;
+        }
+        if (rank == owner) {
+          // ids rise with the vector index: warps take contiguous runs of it
+          const int seg = (n_vec + kWarps * 32 - 1) / (kWarps * 32) * 32;
+          const int v0 = warp * seg, v1 = min(n_vec, v0 + seg);
+          auto count = [&](int v, float (&z)[VE]) {
+            unsigned int c = 0u;
+            if (v < v1) {
+              Elem<T>::unpack(slice[v], z);
+#pragma unroll
+              for (int i = 0; i < VE; ++i)
+                c += z[i] > -INFINITY && key_of(z[i]) == kmin ? 1u : 0u;
+            }
+            return c;
+          };
+          float z[VE];
+          unsigned int c = 0u;
+          for (int v = v0 + lane; v < v1; v += 32) c += count(v, z);
+          c = __reduce_add_sync(0xffffffffu, c);
+          if (lane == 0) sh.red32[warp] = c;
+          __syncthreads();
+          for (int w = 0; w < warp; ++w) before += sh.red32[w];
+          if (before < m && before + c >= m) {
+            for (int vv = v0; vv < v1; vv += 32) {
+              const unsigned int x = count(vv + lane, z);
+              unsigned int s = x;
+              for (int o = 1; o < 32; o <<= 1) {
+                const unsigned int a = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += a;
+              }
+              unsigned int at = before + s - x;
+              if (at < m && at + x >= m) {
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                  if (z[i] > -INFINITY && key_of(z[i]) == kmin && ++at == m)
+                    for (int c2 = 0; c2 < C; ++c2)
+                      *cluster.map_shared_rank(&sh.cut_id, c2) = base + (vv + lane) * VE + i;
+              }
+              before += __shfl_sync(0xffffffffu, s, 31);
+            }
+          }
+        }
+        cluster.sync();
+        return Cut{b.mass + m * w, kmin, sh.cut_id};
       }
+      crowded = true;
       int shift = 0;
       while (((kmax - kmin) >> shift) >= (uint32_t)kBins) ++shift;
-      histogram([&](float z, uint32_t& bin) {
+      histogram(true, by_p, [&](float z, uint32_t& bin) {
         const uint32_t k = key_of(z);
         if (k < kmin || k > kmax) return false;
         bin = (kmax - k) >> shift;
         return true;
       });
-      f = find_bin(mass_mode, limit, f.count, f.mass);
+      b = find(by_mass, limit, b.count, b.mass);  // the same limit
       level0 = false;
-      phi = kmax - (f.bin << shift);
+      phi = kmax - (b.bin << shift);
       const uint32_t width = (1u << shift) - 1u;
       plo = phi - kmin > width ? phi - width : kmin;
     }
   };
 
-  // ---- the cut ----
-  uint32_t cut = 0u;            // tokens with a larger key stay
-  uint32_t cut_m = 0xffffffffu;  // and the first cut_m with this one
-  bool ranked = false;          // some tokens with the cut's key do not stay
+  // ---- the cut: larger keys stay, and ids up to cut_id of this one ----
+  uint32_t cut_key = kLowestKey;
+  int cut_id = 0x7fffffff;
   if (by_k || by_p) {
-    histogram([&](float z, uint32_t& bin) {
+    auto all = [&](float z, uint32_t& bin) {
       bin = bin0(z);
       return true;
-    });
-    unsigned long long total = 0ull;
-    unsigned int count = 0u;
-    for (int c = 0; c < C; ++c) {
-      total += sh.chunk[c].mass;
-      count += sh.chunk[c].count;
+    };
+    histogram(by_k, by_p, all);
+    unsigned long long limit = 0ull;  // top_p of the whole row
+    bool k_cut = false;
+    if (by_k) {
+      unsigned int count = 0u;
+      for (int i = lane; i < C * kGroups; i += 32) count += sh.group[i / kGroups][i % kGroups].count;
+      k_cut = (unsigned int)top_k < __reduce_add_sync(0xffffffffu, count);
     }
-    Found fp{};
-    bool p_cut = false;
-    if (by_k && (unsigned int)top_k < count) {
-      // find both bins on the level-0 histogram before a crowded bin reuses it
-      Found fk = find_bin(false, (unsigned long long)top_k, 0u, 0ull);
-      fk = resolve(false, (unsigned long long)top_k, fk);
-      cut = fk.bin;
-      cut_m = fk.m;
-      ranked = fk.m < fk.n;
+    if (k_cut) {
+      const Bin b = find(false, (unsigned long long)top_k, 0u, 0ull);
+      const Cut cut = resolve(false, b, by_p);
+      cut_key = cut.key;
+      cut_id = cut.id;
       if (by_p) {
-        total = fk.mass + fk.m * weight(value_of(fk.bin));
-        histogram([&](float z, uint32_t& bin) {
-          bin = bin0(z);
-          return true;
-        });
+        limit = p_limit(cut.mass);
+        if (crowded) histogram(true, true, all);
       }
     }
     if (by_p) {
-      // kept while the mass before is below top_p * total: an integer limit
-      const unsigned long long limit =
-          max(1ull, static_cast<unsigned long long>(ceil((double)top_p * (double)total)));
-      fp = find_bin(true, limit, 0u, 0ull);
-      fp = resolve(true, limit, fp);
-      p_cut = fp.bin > cut || (fp.bin == cut && fp.m < cut_m);
+      const Bin b = find(true, limit, 0u, 0ull);
+      const Cut cut = resolve(true, b, false);
+      if (cut.key > cut_key || (cut.key == cut_key && cut.id < cut_id)) {
+        cut_key = cut.key;
+        cut_id = cut.id;
+      }
     }
-    if (p_cut) {
-      cut = fp.bin;
-      cut_m = fp.m;
-      ranked = fp.m < fp.n;
+  }
+  if (min_p > 0.f) {
+    // w >= min_p: a bound on the logit, rounded up to a float
+    const float z_min = __double2float_ru((double)hi + log2((double)min_p) / c_log2);
+    if (z_min > -INFINITY && key_of(z_min) > cut_key) {
+      cut_key = key_of(z_min);
+      cut_id = 0x7fffffff;
     }
   }
 
   // ---- the draw: kept mass in id order ----
   // warp w takes the vectors [w * seg, (w + 1) * seg) of the slice, 32 at a time
-  const double y_min = min_p > 0.f ? log2((double)min_p) : -INFINITY;
   const int seg = (n_vec + kWarps * 32 - 1) / (kWarps * 32) * 32;
   const int v_begin = warp * seg, v_end = min(n_vec, v_begin + seg);
-  unsigned int tie_base = 0u;  // tokens with the cut's key before this warp's
-  if (ranked) {
-    unsigned int n = 0u;
-    for (int v = v_begin + lane; v < v_end; v += 32) {
-      float z[VE];
-      Elem<T>::unpack(slice[v], z);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) n += key_of(z[i]) == cut ? 1u : 0u;
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) sh.red32[warp] = n;
-    __syncthreads();
-    if (tid < C) {
-      unsigned int t = 0u;
-      for (int w = 0; w < kWarps; ++w) t += sh.red32[w];
-      *cluster.map_shared_rank(&sh.ties[rank], tid) = t;
-    }
-    cluster.sync();
-    for (int c = 0; c < rank; ++c) tie_base += sh.ties[c];
-    for (int w = 0; w < warp; ++w) tie_base += sh.red32[w];
-    __syncthreads();
-  }
-  // one vector's kept weights; `tie` counts the cut's key before this warp step
-  auto kept_weights = [&](int v, unsigned int& tie, unsigned long long (&w)[VE],
-                          bool (&stay)[VE]) {
-    float z[VE];
-    if (v < v_end) {
-      Elem<T>::unpack(slice[v], z);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) z[i] = -INFINITY;
-    }
-    unsigned int before = 0u;
-    if (ranked) {
-      unsigned int n = 0u;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) n += key_of(z[i]) == cut ? 1u : 0u;
-      unsigned int s = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned int a = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += a;
-      }
-      before = tie + s - n;
-      tie += __shfl_sync(0xffffffffu, s, 31);
-    }
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const uint32_t k = key_of(z[i]);
-      bool keep = z[i] > -INFINITY && k >= cut;
-      if (ranked && k == cut) keep = before++ < cut_m;
-      w[i] = 0ull;
-      if (keep) {
-        const double y = exponent(z[i]);
-        keep = y >= y_min;
-        if (keep) w[i] = y < -43.5 ? 0ull : __double2ull_rn(exp2(y) * kUnit);
-      }
-      stay[i] = keep;
-    }
+  auto stays = [&](float z, int id) {
+    const uint32_t k = key_of(z);
+    return k > cut_key || (k == cut_key && id <= cut_id);
   };
   unsigned long long mass = 0ull;
   unsigned int count = 0u;
   int first = 0x7fffffff;
-  {
-    unsigned int tie = tie_base;
-    for (int v0 = v_begin; v0 < v_end; v0 += 32) {
-      unsigned long long w[VE];
-      bool stay[VE];
-      kept_weights(v0 + lane, tie, w, stay);
+  for (int v = v_begin + lane; v < v_end; v += 32) {
+    float z[VE];
+    Elem<T>::unpack(slice[v], z);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        mass += w[i];
-        if (stay[i]) {
-          ++count;
-          first = min(first, base + (v0 + lane) * VE + i);
+    for (int i0 = 0; i0 < VE; i0 += 4) {
+      bool in[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[i] = stays(z[i0 + i], base + v * VE + i0 + i);
+      if (in[0] || in[1] || in[2] || in[3]) {
+        // four independent weights, then the ones that stay
+        unsigned long long w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (in[i]) {
+            mass += w[i];
+            ++count;
+            first = min(first, base + v * VE + i0 + i);
+          }
         }
       }
     }
-    for (int o = 16; o > 0; o >>= 1) {
-      mass += __shfl_xor_sync(0xffffffffu, mass, o);
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-    }
-    if (lane == 0) {
-      sh.red64[warp] = mass;
-      sh.red32[warp] = count;
-      sh.red32b[warp] = static_cast<unsigned int>(first);
-    }
-    __syncthreads();
-    if (tid < C) {
-      Totals t{0ull, 0u, 0x7fffffff};
-      for (int w = 0; w < kWarps; ++w) {
-        t.mass += sh.red64[w];
-        t.count += sh.red32[w];
-        t.first = min(t.first, static_cast<int>(sh.red32b[w]));
-      }
-      *cluster.map_shared_rank(&sh.part[rank], tid) = t;
-    }
-    cluster.sync();
   }
-  unsigned long long total = 0ull, my_base = 0ull;
-  unsigned int all = 0u;
+  for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  count = __reduce_add_sync(0xffffffffu, count);
+  first = __reduce_min_sync(0xffffffffu, first);
+  if (lane == 0) {
+    sh.red64[warp] = mass;
+    sh.red32[warp] = count;
+    sh.red32b[warp] = static_cast<unsigned int>(first);
+  }
+  __syncthreads();
+  if (tid < C) {
+    Sums t{0ull, 0u, 0x7fffffff};
+    for (int w = 0; w < kWarps; ++w) {
+      t.mass += sh.red64[w];
+      t.count += sh.red32[w];
+      t.first = min(t.first, static_cast<int>(sh.red32b[w]));
+    }
+    *cluster.map_shared_rank(&sh.part[rank], tid) = t;
+  }
+  cluster.sync();
+  unsigned long long total = 0ull, before = 0ull;
+  unsigned int kept = 0u;
   first = 0x7fffffff;
   for (int c = 0; c < C; ++c) {
-    if (c == rank) my_base = total;
+    if (c == rank) before = total;
     total += sh.part[c].mass;
-    all += sh.part[c].count;
+    kept += sh.part[c].count;
     first = min(first, sh.part[c].first);
   }
-  if (rank == 0 && tid == 0 && p.kept != nullptr) p.kept[r] = static_cast<int>(all);
-  if (u == 0.f) {
+  if (rank == 0 && tid == 0 && p.kept != nullptr) p.kept[r] = static_cast<int>(kept);
+  if (u == 0.f) {  // the first token that stays, however small its weight
     if (rank == 0 && tid == 0) p.tokens[r] = first;
     return;
   }
   const unsigned long long target =
       min(static_cast<unsigned long long>((double)u * (double)total), total - 1);
-  for (int w = 0; w < warp; ++w) my_base += sh.red64[w];
-  if (target < my_base || target >= my_base + mass) return;
+  for (int w = 0; w < warp; ++w) before += sh.red64[w];
+  if (target < before || target >= before + mass) return;
   // this warp holds the drawn token
-  unsigned int tie = tie_base;
   for (int v0 = v_begin; v0 < v_end; v0 += 32) {
-    unsigned long long w[VE];
-    bool stay[VE];
-    kept_weights(v0 + lane, tie, w, stay);
-    unsigned long long n = 0ull;
+    const int v = v0 + lane;
+    unsigned long long w[VE], n = 0ull;
+    if (v < v_end) {
+      float z[VE];
+      Elem<T>::unpack(slice[v], z);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) n += w[i];
+      for (int i = 0; i < VE; ++i) {
+        w[i] = stays(z[i], base + v * VE + i) ? weight(z[i]) : 0ull;
+        n += w[i];
+      }
+    }
     unsigned long long s = n;
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long a = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += a;
     }
-    unsigned long long at = my_base + s - n;
+    unsigned long long at = before + s - n;
     if (target >= at && target < at + n) {
       int id = -1;
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        if (id < 0 && target < at + w[i]) id = base + (v0 + lane) * VE + i;
+        if (id < 0 && target < at + w[i]) id = base + v * VE + i;
         at += w[i];
       }
       p.tokens[r] = id;
     }
-    my_base += __shfl_sync(0xffffffffu, s, 31);
+    before += __shfl_sync(0xffffffffu, s, 31);
+    if (target < before) break;
   }
 }
 
@@ -734,8 +892,7 @@ medusa_status_t launch_sample(SampleParams& p, cudaStream_t stream) {
   while (C < kMaxCluster && p.V > 4096 * C) C *= 2;
   const int span = p.V + VE - 1;  // the row and its offset in a 16-byte word
   p.slice = ((span + C - 1) / C + 32 * VE - 1) / (32 * VE) * (32 * VE);
-  const size_t smem = (size_t)p.slice * sizeof(T) + 3 * kBins * sizeof(uint32_t) +
-                      (size_t)(kBins / C) * 12;
+  const size_t smem = (size_t)p.slice * sizeof(T) + 3 * kBins * sizeof(uint32_t);
   if (cudaFuncSetAttribute(sample_tokens_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return fail(MEDUSA_ERR_CUDA, "cudaFuncSetAttribute(sample_tokens) failed");

@@ -111,8 +111,8 @@ def test_sample_tokens_refusals(L):
 
     assert call(R=0) == 0 and call(R=0, n=0, lg=None, u=None, tok=None) == 0
     assert call(dt=5) == 1
-    assert call(V=0) == 2 and call(V=786433, stride=786433) == 2
-    assert call(dt=1, V=393217, stride=393217) == 2
+    assert call(V=0) == 2 and call(V=655361, stride=655361) == 2
+    assert call(dt=1, V=327681, stride=327681) == 2
     assert call(R=-1) == 2 and call(R=70000, n=70000) == 2
     assert call(stride=99) == 2
     assert call(R=3) == 2                         # more draws than rows without row_idx
@@ -120,10 +120,13 @@ def test_sample_tokens_refusals(L):
     assert call(lg=4097) == 8
 
 
-def test_binding_refuses_wrong_tensors():
+def test_binding_refuses_wrong_tensors(monkeypatch):
+    monkeypatch.setattr(_lib, "_dev", lambda: 0)
     q = torch.zeros(4, 2, 64)
     with pytest.raises(ValueError, match="CUDA"):
         M.medusa_rope(M.Rope(64, device="cpu"), q, None, torch.zeros(4, dtype=torch.int32), q, None)
+    with pytest.raises(ValueError, match="T, H, dh"):
+        M.medusa_rope(M.Rope(64, device="cpu"), q[0], None, None, q, None)
     with pytest.raises(ValueError, match="contiguous CUDA"):
         M.PagedCache(torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 16, 64),
                      torch.zeros(2, 1, dtype=torch.int32))
