@@ -23,9 +23,15 @@
 //               5), K's freed after its scores, V's after its product.
 //   warp 1      MMA issuer: S = Q K^T into TMEM, then O += P V with P as bf16
 //               in TMEM over the scores' columns.
-//   warps 4-11  two softmax warpgroups, one query row per thread.
+//   warps 4-11  two softmax warpgroups, one query row per thread, each with a
+//               score buffer and an O of its own.  A segment of two M tiles
+//               gives one to each.  A segment of one M tile (single tokens,
+//               short chunks) gives its key tiles to them in turn, two
+//               independent chains instead of one; the first warpgroup adds
+//               the second's O to its own where the piece ends.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -64,6 +70,15 @@ struct TcParams {
   int32_t* status;
 };
 
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 template <int DH>
 struct Smem {
   static constexpr int kPanels = DH / 64;
@@ -74,11 +89,13 @@ struct Smem {
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = 2 * kQBytes;
   static constexpr int kBarOff = kRingOff + kRing * kItem;
-  // full[ring], empty[ring], q_full[2], s_full[2], p_full[2], pv_done[2], drain, exit
-  static constexpr int kNumBars = 2 * kRing + 10;
+  // full[ring], empty[ring], q_full[2], s_full[2], p_full[2], pv_done[2], q_empty, half_ready,
+  // half_free, drain, exit
+  static constexpr int kNumBars = 2 * kRing + 13;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // holder, abort, ok, info[ring]
   static constexpr int kStartOff = kMiscOff + 16 + kRing * 4;
-  static constexpr int kBytes = kStartOff + 32;
+  static constexpr int kHalfOff = (kStartOff + 16 + 7) & ~7;  // float2 {base, sum}[128] of the second half
+  static constexpr int kBytes = kHalfOff + kMT * 8;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
   static_assert((kMaxB + 1) * 8 + 16 * 8 <= kRing * kItem, "schedule fits in the ring");
@@ -261,13 +278,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
-  uint64_t* drain = pv_done + 2;
+  uint64_t* q_empty = pv_done + 2;
+  uint64_t* half_ready = q_empty + 1;
+  uint64_t* half_free = half_ready + 1;
+  uint64_t* drain = half_free + 1;
   uint64_t* exit_bar = drain + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   volatile int* sched_bad = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
   int* info = reinterpret_cast<int*>(smem + L::kMiscOff + 16);  // per ring slot, with each K
   int* start = reinterpret_cast<int*>(smem + L::kStartOff);     // {b, kvh, qg, lt}
+  float2* half_ml = reinterpret_cast<float2*>(smem + L::kHalfOff);
 
   // ---- schedule: cum[b] = tiles of the sequences before b (in the ring) ----
   long long* cum = reinterpret_cast<long long*>(smem + L::kRingOff);
@@ -384,6 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[m], 128);
       mbar_init(&pv_done[m], 1);
     }
+    mbar_init(q_empty, 1);
+    mbar_init(half_ready, 128);
+    mbar_init(half_free, 128);
     mbar_init(drain, 1);
     mbar_init(exit_bar, kThreads);
     *abort_flag = 0;
@@ -424,36 +448,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     warpgroup_regs_dec<kRegsLow>();
     if (warp == 0) {
       // ---------------- TMA producer ----------------
-      const uint64_t pol = l2_policy_evict_last();
+      // K/V that several query groups read stays in L2, the rest passes by
+      const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
       Cursor cur;
       cur.init(start, t0, t1, p);
+      // A tile's page ids (one per lane) are fetched a tile ahead: the read
+      // would otherwise hold up the copies of every tile.
+      auto page_id = [&](const Cursor& x) {
+        int key0, nv, pg, r0;
+        x.span(p, key0, nv, pg, r0);
+        const int boxes = p.ppt > 0 ? (nv + p.page - 1) / p.page : (nv > 0 ? 1 : 0);
+        return lane < boxes ? p.table[(size_t)x.b * p.max_pages + pg + lane] : INT_MIN;
+      };
+      int next_id = page_id(cur);
       const int panel_rows = p.ppt > 0 ? p.page : kBN;
       const uint32_t box_bytes = static_cast<uint32_t>(panel_rows) * 128u * L::kPanels;
+      const uint32_t q_bytes = static_cast<uint32_t>(p.G * p.tpt) * 128u * L::kPanels;
       int slot = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, n_pieces = 0;
+      uint32_t q_loads0 = 0, q_loads1 = 0;
       bool ok = true, bad_page = false;
       int issued = 0;  // ring items whose copies were started
-      for (int j = 0; ok && j < n_tiles; ++j, cur.advance(p)) {
+      Cursor ahead = cur;
+      for (int j = 0; ok && j < n_tiles; ++j, cur = ahead) {
         int key0, nv, pg, r0;
         cur.span(p, key0, nv, pg, r0);
-        // boxes of the tile: one per lane
-        const int boxes = p.ppt > 0 ? (nv + p.page - 1) / p.page : (nv > 0 ? 1 : 0);
-        int id = 0;
-        bool mine = lane < boxes;
-        if (mine) {
-          id = p.table[(size_t)cur.b * p.max_pages + pg + lane];
-          if (id < 0 || id >= p.n_pages) {
-            bad_page = true;
-            mine = false;
-          }
+        const int id = next_id;
+        ahead.advance(p);
+        if (j + 1 < n_tiles) next_id = page_id(ahead);
+        bool mine = id != INT_MIN;
+        if (mine && (id < 0 || id >= p.n_pages)) {
+          bad_page = true;
+          mine = false;
         }
+        const uint64_t pol = cur.n_qg > 1 ? keep : pass;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
 #pragma unroll
         for (int kvi = 0; kvi < 2; ++kvi) {
           if (lane == 0) {
             ok = mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag, p.status);
             if (ok) {
-              if (kvi == 0) info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0);
+              if (kvi == 0)
+                info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0) | (cur.last ? 4 : 0);
               if (bytes > 0) mbar_arrive_expect_tx(&full[slot], bytes);
               else mbar_arrive(&full[slot]);
             }
@@ -472,6 +508,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             slot = 0;
             phase ^= 1u;
           }
+          if (kvi == 0 && cur.first) {
+            // the piece's Q tiles, once the last piece's scores are done
+            if (lane == 0) {
+              if (n_pieces > 0)
+                ok = mbar_wait_bounded(q_empty, (n_pieces - 1) & 1, abort_flag, p.status);
+              if (ok) {
+                for (int m = 0; m < cur.n_mt; ++m) {
+                  mbar_arrive_expect_tx(&q_full[m], q_bytes);
+#pragma unroll
+                  for (int pn = 0; pn < L::kPanels; ++pn)
+                    tma_load_4d(smem + L::kQOff + m * L::kQBytes + pn * (kMT * 128), &tmQ,
+                                &q_full[m], pn * 64, 0, cur.kvh,
+                                cur.q0 + (cur.qg * 2 + m) * p.tpt, l2_policy_evict_first());
+                  if (m == 0) ++q_loads0;
+                  else ++q_loads1;
+                }
+              }
+            }
+            ++n_pieces;
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+          }
         }
       }
       if (bad_page) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
@@ -480,60 +538,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         int no_abort = 0;
         for (int x = max(0, issued - L::kRing); x < issued; ++x)
           mbar_wait_bounded(&full[x % L::kRing], (x / L::kRing) & 1, &no_abort, p.status);
+        if (q_loads0 > 0) mbar_wait_bounded(&q_full[0], (q_loads0 - 1) & 1, &no_abort, p.status);
+        if (q_loads1 > 0) mbar_wait_bounded(&q_full[1], (q_loads1 - 1) & 1, &no_abort, p.status);
       }
       __syncwarp();
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
-      // Order per tile j: PV(0,j), QK(0,j+1), PV(1,j), QK(1,j+1): while one
-      // warpgroup computes its softmax the tensor core works on the other M
-      // tile.
-      if (lane == 0) {
+      // A unit is one score buffer m on one key tile: both buffers on every
+      // tile (two M tiles), or buffers in turn (one).  A buffer's next QK^T
+      // follows its PV, so at most two units wait for their softmax, and
+      // while one warpgroup computes the tensor core works for the other.
+      // The whole warp walks the loop, so that everything an instruction needs
+      // stays warp-uniform; one elected lane issues.
+      {
         constexpr uint32_t idesc_qk = umma_idesc_bf16(kMT, kBN, 0);
         constexpr uint32_t idesc_pv = umma_idesc_bf16(kMT, DH, 1);
         const uint64_t dq0 = umma_desc_sw128(smem_u32(smem + L::kQOff));
         const uint64_t dk0 = umma_desc_sw128(smem_u32(smem + L::kRingOff));
         const uint64_t dv0 = umma_desc_sw128_lbo(smem_u32(smem + L::kRingOff), L::kPanel, 1024);
-        auto issue_qk = [&](int m, int st) {
-          const uint64_t dq = dq0 + (uint64_t)((m * L::kQBytes) >> 4);
+        auto issue_qk = [&](int m, int qm, int st, bool q_done) {
+          const uint64_t dq = dq0 + (uint64_t)((qm * L::kQBytes) >> 4);
           const uint64_t dk = dk0 + (uint64_t)((st * L::kItem) >> 4);
           const uint32_t d = tmem_s + m * kBN;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            constexpr uint32_t qpanel = (kMT * 128) >> 4, kpanel = L::kPanel >> 4;
-            umma_bf16(d, dq + (kk >> 2) * qpanel + (kk & 3) * 2,
-                      dk + (kk >> 2) * kpanel + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < DH / 16; ++kk) {
+              constexpr uint32_t qpanel = (kMT * 128) >> 4, kpanel = L::kPanel >> 4;
+              umma_bf16(d, dq + (kk >> 2) * qpanel + (kk & 3) * 2,
+                        dk + (kk >> 2) * kpanel + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&s_full[m]);
+            if (q_done) umma_commit(&empty[st]);
           }
-          umma_commit(&s_full[m]);
+          __syncwarp();
         };
-        auto issue_pv = [&](int m, int st, uint32_t acc0) {
+        auto issue_pv = [&](int m, int st, uint32_t acc0, bool v_done) {
           const uint64_t dv = dv0 + (uint64_t)((st * L::kItem) >> 4);
           const uint32_t d = tmem_o + m * DH;
           const uint32_t pcol = tmem_s + m * kBN;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            // 16 keys: 8 columns of packed P, two 8-row groups of V
-            umma_bf16_ts(d, pcol + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
-                         kk > 0 ? 1u : acc0);
-          umma_commit(&pv_done[m]);
-        };
-        uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // completed waits per barrier
-        int ks = 0;
-        uint32_t kph = 0;
-        bool ok = mbar_wait_bounded(&full[0], 0, abort_flag, p.status);
-        int cur = ok ? info[0] : 0;
-        if (ok) ok = mbar_wait_bounded(&q_full[0], nq0++ & 1, abort_flag, p.status);
-        if (ok) {
-          tc_fence_after();
-          issue_qk(0, 0);
-          if (cur & 2) {
-            ok = mbar_wait_bounded(&q_full[1], nq1++ & 1, abort_flag, p.status);
-            if (ok) {
-              tc_fence_after();
-              issue_qk(1, 0);
-            }
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              // 16 keys: 8 columns of packed P, two 8-row groups of V
+              umma_bf16_ts(d, pcol + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                           kk > 0 ? 1u : acc0);
+            umma_commit(&pv_done[m]);
+            if (v_done) umma_commit(&empty[st]);
           }
-          umma_commit(&empty[0]);
-        }
+          __syncwarp();
+        };
+        // units whose PV is still to come, oldest first: bit 0 buffer, bit 1
+        // O starts over, bit 2 last user of the V tile, bits 8.. ring slot,
+        // bit 16 its phase
+        int pend0 = -1, pend1 = -1;
+        uint32_t np = 0, nq = 0;  // parities of the next waits on p_full / q_full, bit m
+        auto pop = [&]() -> bool {
+          const int u = pend0;
+          pend0 = pend1;
+          pend1 = -1;
+          const int m = u & 1, vs = (u >> 8) & 0xff;
+          if (!mbar_wait_bounded(&full[vs], (u >> 16) & 1, abort_flag, p.status) ||
+              !mbar_wait_bounded(&p_full[m], (np >> m) & 1u, abort_flag, p.status))
+            return false;
+          np ^= 1u << m;
+          tc_fence_after();
+          issue_pv(m, vs, (u & 2) ? 0u : 1u, (u & 4) != 0);
+          return true;
+        };
+        int ks = 0, at = 0;  // ring slot of K, tile of the piece
+        uint32_t kph = 0;
+        bool ok = true;
         for (int j = 0; ok && j < n_tiles; ++j) {
           int vs = ks + 1;
           uint32_t vph = kph;
@@ -541,45 +615,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             vs = 0;
             vph ^= 1u;
           }
+          if (pend1 >= 0 && !pop()) break;
+          if (!mbar_wait_bounded(&full[ks], kph, abort_flag, p.status)) break;
+          const int word = __shfl_sync(0xffffffffu, info[ks], 0);
+          const bool first = (word & 1) != 0, two = (word & 2) != 0;
+          if (first) at = 0;
+          for (int m = two ? 0 : at & 1;; ++m) {
+            while (ok && ((pend0 >= 0 && (pend0 & 1) == m) || (pend1 >= 0 && (pend1 & 1) == m)))
+              ok = pop();
+            if (!ok) break;
+            const int qm = two ? m : 0;
+            if (first) {
+              ok = mbar_wait_bounded(&q_full[qm], (nq >> qm) & 1u, abort_flag, p.status);
+              if (!ok) break;
+              nq ^= 1u << qm;
+            }
+            tc_fence_after();
+            const bool fresh = two ? first : at < 2, done = !two || m == 1;
+            issue_qk(m, qm, ks, done);
+            const int u = m | (fresh ? 2 : 0) | (done ? 4 : 0) | (vs << 8) | ((int)vph << 16);
+            if (pend0 < 0) pend0 = u;
+            else pend1 = u;
+            if (done) break;
+          }
+          if (!ok) break;
+          if ((word & 4) && elect_one()) umma_commit(q_empty);
+          __syncwarp();
+          ++at;
           ks = vs + 1;
           kph = vph;
           if (ks == L::kRing) {
             ks = 0;
             kph ^= 1u;
           }
-          const bool has_next = j + 1 < n_tiles;
-          const bool two = (cur & 2) != 0;
-          const uint32_t acc0 = (cur & 1) ? 0u : 1u;
-          if (!mbar_wait_bounded(&full[vs], vph, abort_flag, p.status) ||
-              !mbar_wait_bounded(&p_full[0], np0++ & 1, abort_flag, p.status))
-            break;
-          tc_fence_after();
-          issue_pv(0, vs, acc0);
-          if (!two) umma_commit(&empty[vs]);
-          int nxt = 0;
-          if (has_next) {
-            if (!mbar_wait_bounded(&full[ks], kph, abort_flag, p.status)) break;
-            nxt = info[ks];
-            if ((nxt & 1) && !mbar_wait_bounded(&q_full[0], nq0++ & 1, abort_flag, p.status)) break;
-            tc_fence_after();
-            issue_qk(0, ks);
-            if (!(nxt & 2)) umma_commit(&empty[ks]);
-          }
-          if (two) {
-            if (!mbar_wait_bounded(&p_full[1], np1++ & 1, abort_flag, p.status)) break;
-            tc_fence_after();
-            issue_pv(1, vs, acc0);
-            umma_commit(&empty[vs]);
-          }
-          if (has_next && (nxt & 2)) {
-            if ((nxt & 1) && !mbar_wait_bounded(&q_full[1], nq1++ & 1, abort_flag, p.status)) break;
-            tc_fence_after();
-            issue_qk(1, ks);
-            umma_commit(&empty[ks]);
-          }
-          cur = nxt;
         }
-        umma_commit(drain);
+        while (ok && pend0 >= 0) ok = pop();
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
         int no_abort = 0;
         mbar_wait_bounded(drain, 0, &no_abort, p.status);
       }
@@ -593,55 +665,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t srow = tmem_s + lane_off + m * kBN;
     const int tok_l = rl / p.G, g = rl - tok_l * p.G;  // token of the M tile, head of the group
-    uint8_t* qtile = smem + L::kQOff + m * L::kQBytes;
-    auto load_q = [&](const Cursor& x) {
-      if (rl == 0) {
-        const uint32_t bytes = static_cast<uint32_t>(p.G * p.tpt) * 128u * L::kPanels;
-        mbar_arrive_expect_tx(&q_full[m], bytes);
-#pragma unroll
-        for (int pn = 0; pn < L::kPanels; ++pn)
-          tma_load_4d(qtile + pn * (kMT * 128), &tmQ, &q_full[m], pn * 64, 0, x.kvh,
-                      x.q0 + (x.qg * 2 + m) * p.tpt, l2_policy_evict_first());
-      }
-    };
-    uint32_t tcount = 0;
-    bool q_ready = false;
+    uint32_t tcount = 0;          // units of this warpgroup so far
+    uint32_t halves = 0;          // one-tile pieces the second warpgroup took part in
     float m_used = -INFINITY, l_run = 0.f;
-    int jj = 0, piece_lt0 = 0;
+    int at = 0, units = 0;        // tile of the piece, this warpgroup's units in it
+    int piece_lt0 = 0, piece_n = 0;
     bool finite = true;
     Cursor cur;
     cur.init(start, t0, t1, p);
     for (int j = 0; j < n_tiles; ++j, cur.advance(p)) {
-      if (m >= cur.n_mt) continue;
-      const int tok = (cur.qg * 2 + m) * p.tpt + tok_l;
-      const bool valid = tok_l < p.tpt && tok < cur.qlen;
+      const bool alt = cur.n_mt == 1;
       if (cur.first) {
-        if (!q_ready) load_q(cur);
-        q_ready = false;
         m_used = -INFINITY;
         l_run = 0.f;
-        jj = 0;
+        at = units = 0;
         piece_lt0 = cur.lt;
+        piece_n = min(cur.ntiles - cur.lt, t1 - cur.t);
       }
+      const int here = at++;
+      if (alt && (here & 1) != m) continue;
+      const int tok = (cur.qg * 2 + (alt ? 0 : m)) * p.tpt + tok_l;
+      const bool valid = tok_l < p.tpt && tok < cur.qlen;
       int key0, nv, pg, r0;
       cur.span(p, key0, nv, pg, r0);
       // slots of the tile this row sees
       const int limit = valid ? min(nv, cur.kv - cur.qlen + tok + 1 - key0) : 0;
       if (!mbar_wait_bounded(&s_full[m], tcount & 1, abort_flag, p.status)) break;
       tc_fence_after();
-      if (cur.last && j + 1 < n_tiles) {
-        // every QK of this piece is done: fetch the next piece's Q now
-        Cursor nx = cur;
-        nx.advance(p);
-        if (m < nx.n_mt) {
-          load_q(nx);
-          q_ready = true;
-        }
-      }
-      if (m == 0 && nv < cur.filled(p, r0)) {
+      if ((alt || m == 0) && nv < cur.filled(p, r0)) {
         // The tile's V rows from nv on belong to no slot of the segment and
-        // may hold anything: cleared once they have landed (PV of either M
-        // tile is issued after this warpgroup's arrival below).
+        // may hold anything: cleared once they have landed (the tile's PVs are
+        // issued after this warpgroup's arrival below).
         const int item = 2 * j + 1, vs = item % L::kRing;
         if (!mbar_wait_bounded(&full[vs], (item / L::kRing) & 1, abort_flag, p.status)) break;
         uint8_t* vt = smem + L::kRingOff + vs * L::kItem;
@@ -682,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, need)) {
           const float new_m = need ? mx : m_used;
           const float corr = (need && m_used != -INFINITY) ? ex2_approx(m_used - new_m) : 1.f;
-          if (jj > 0) {
-            // O holds earlier tiles (their PV precedes this tile's QK)
+          if (units > 0) {
+            // O holds earlier units (their PV precedes this unit's QK)
 #pragma unroll 1
             for (int ch = 0; ch < DH / 32; ++ch) {
               float o[32];
@@ -722,68 +776,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_run += s0 + s1;
         tmem_st_wait();
       }
+      // the first PV of a piece overwrites O: the second half's of the last
+      // one-tile piece must have been read
+      if (m == 1 && units == 0 && halves > 0 &&
+          !mbar_wait_bounded(half_free, (halves - 1) & 1, abort_flag, p.status))
+        break;
       tc_fence_before();
       mbar_arrive(&p_full[m]);
-      if (cur.last) {
-        grid_dep_wait();
-        if (!mbar_wait_bounded(&pv_done[m], tcount & 1, abort_flag, p.status)) break;
+      const uint32_t unit = tcount++;
+      ++units;
+      if (alt ? here + 2 < piece_n : !cur.last) continue;
+
+      // ---- this warpgroup's share of the piece is complete ----
+      if (!mbar_wait_bounded(&pv_done[m], unit & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      if (alt && m == 1) {
+        half_ml[rl] = make_float2(m_used, l_run);
+        ++halves;
+        tc_fence_before();
+        mbar_arrive(half_ready);
+        continue;
+      }
+      grid_dep_wait();  // the results go where the stream order lets them
+      float w0 = 1.f, w1 = 0.f;
+      const bool both = alt && piece_n > 1;
+      if (both) {
+        if (!mbar_wait_bounded(half_ready, halves & 1, abort_flag, p.status)) break;
+        ++halves;
         tc_fence_after();
-        const bool any = __any_sync(0xffffffffu, valid);
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-        // a NaN sum is no empty row
-        const float norm = l_run == l_run ? inv : l_run;
-        __nv_bfloat16* out =
-            p.out + ((size_t)(cur.q0 + tok) * p.Hq + cur.kvh * p.G + g) * DH;
-        if (!any) {
-          // nothing to write
-        } else if (piece_lt0 == 0 && cur.lt == cur.ntiles - 1) {
+        const float2 h = half_ml[rl];
+        const float M = fmaxf(m_used, h.x);
+        w0 = l_run == 0.f ? 0.f : ex2_approx(m_used - M);
+        w1 = h.y == 0.f ? 0.f : ex2_approx(h.x - M);
+        l_run = l_run * w0 + h.y * w1;
+        m_used = M;
+      }
+      // an empty row is zero; a NaN sum is no empty row
+      const float inv = l_run == 0.f ? 0.f : l_run > 0.f ? 1.f / l_run : l_run;
+      w0 *= inv;
+      w1 *= inv;
+      auto row32 = [&](int ch, float (&o)[32]) {
+        tmem_ld32(tmem_o + lane_off + (both ? 0 : m) * DH + ch * 32, o);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] *= w0;
+        if (both) {
+          float x[32];
+          tmem_ld32(tmem_o + lane_off + DH + ch * 32, x);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = fmaf(x[c], w1, o[c]);
+        }
+      };
+      __nv_bfloat16* out = p.out + ((size_t)(cur.q0 + tok) * p.Hq + cur.kvh * p.G + g) * DH;
+      if (!__any_sync(0xffffffffu, valid)) {
+        // nothing to write
+      } else if (piece_lt0 == 0 && piece_n == cur.ntiles) {
 #pragma unroll 1
-          for (int ch = 0; ch < DH / 32; ++ch) {
-            float o[32];
-            tmem_ld32(tmem_o + lane_off + m * DH + ch * 32, o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = l_run == 0.f ? 0.f : o[c] * norm;
-            if (valid) finite = store_row32<DH>(out + ch * 32, o) && finite;
-          }
-        } else {
-          const int s0 = t0 + j - cur.lt;  // the segment's first tile
-          const int c0 = s0 / per;
-          const int n_pieces = (s0 + cur.ntiles - 1) / per - c0 + 1;
-          const size_t slot = piece_slot(blockIdx.x, per, s0);
-          const int row = m * kMT + rl;
-          float4* dst = reinterpret_cast<float4*>(p.o_part) + slot * (DH / 4) * kRows + row;
+        for (int ch = 0; ch < DH / 32; ++ch) {
+          float o[32];
+          row32(ch, o);
+          if (valid) finite = store_row32<DH>(out + ch * 32, o) && finite;
+        }
+      } else {
+        const int s0 = t0 + j - cur.lt;  // the segment's first tile
+        const int c0 = s0 / per;
+        const int n_pieces = (s0 + cur.ntiles - 1) / per - c0 + 1;
+        const size_t slot = piece_slot(blockIdx.x, per, s0);
+        const int row = m * kMT + rl;
+        float4* dst = reinterpret_cast<float4*>(p.o_part) + slot * (DH / 4) * kRows + row;
 #pragma unroll 1
-          for (int ch = 0; ch < DH / 32; ++ch) {
-            float o[32];
-            tmem_ld32(tmem_o + lane_off + m * DH + ch * 32, o);
+        for (int ch = 0; ch < DH / 32; ++ch) {
+          float o[32];
+          row32(ch, o);
+          if (valid) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = l_run == 0.f ? 0.f : o[c] * norm;
-            if (valid) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                dst[(ch * 8 + c) * kRows] =
-                    make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            }
-          }
-          if (valid)
-            p.lse_part[slot * kRows + row] = l_run > 0.f ? m_used + log2f(l_run)
-                                             : l_run == 0.f ? -INFINITY : l_run;
-          // release this warp's rows, count them in; the last piece merges
-          __threadfence();
-          __syncwarp();
-          unsigned int before = 0u;
-          if (lane == 0)
-            before = atomicAdd(&p.piece_count[c0 * 8 + (warp - 4)], 1u);
-          before = __shfl_sync(0xffffffffu, before, 0);
-          if (before == static_cast<unsigned int>(n_pieces - 1)) {
-            __threadfence();
-            if (valid) finite = merge_row<DH>(p, out, c0, n_pieces, per, s0, row) && finite;
+            for (int c = 0; c < 8; ++c)
+              dst[(ch * 8 + c) * kRows] =
+                  make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
-        tc_fence_before();
+        if (valid)
+          p.lse_part[slot * kRows + row] =
+              l_run > 0.f ? m_used + log2f(l_run) : l_run == 0.f ? -INFINITY : l_run;
+        // release this warp's rows, count them in; the last piece merges
+        __threadfence();
+        __syncwarp();
+        unsigned int before = 0u;
+        if (lane == 0) before = atomicAdd(&p.piece_count[c0 * 8 + (warp - 4)], 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == static_cast<unsigned int>(n_pieces - 1)) {
+          __threadfence();
+          if (valid) finite = merge_row<DH>(p, out, c0, n_pieces, per, s0, row) && finite;
+        }
       }
-      ++tcount;
-      ++jj;
+      tc_fence_before();
+      if (both) mbar_arrive(half_free);
     }
     if (!finite) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
   }
