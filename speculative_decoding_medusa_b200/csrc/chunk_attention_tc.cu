@@ -35,6 +35,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "abi_internal.h"
 #include "attn_common.cuh"
 #include "chunk_attention.cuh"
@@ -48,8 +50,8 @@ constexpr int kBN = 128;       // keys per tile
 constexpr int kMT = 128;       // rows per M tile
 constexpr int kRows = 256;     // rows per segment
 constexpr int kThreads = 384;
-constexpr int kRegsLow = 96;   // registers a thread: producer and MMA warpgroup
-constexpr int kRegsHigh = 200;  // softmax warpgroups
+constexpr int kRegsLow = 72;   // registers a thread: producer and MMA warpgroup
+constexpr int kRegsHigh = 216;  // softmax warpgroups
 constexpr float kLazy = 8.f;   // rescale O only when the maximum grows by 2^8
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMinTiles = 4;   // smallest tile range a CTA takes
@@ -79,6 +81,33 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+constexpr int kPolyEvery = 4;  // one pair of exponentials in kPolyEvery by polynomial
+
+// 2^x of a pair by fp32 arithmetic: x = n + f, |f| <= 1/2, a minimax
+// polynomial of degree 5 for 2^f (relative error 2^-22) and n added to the
+// exponent; x below -126 counts as -126.  It takes some of the exponentials
+// off the special-function unit, which alone would bound the softmax.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  float x0, x1;
+  f32x2_unpack(x2, x0, x1);
+  const uint64_t x = f32x2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const uint64_t t = f32x2_add(x, f32x2_pack(kMagic, kMagic));
+  const uint64_t nf = f32x2_add(t, f32x2_pack(-kMagic, -kMagic));
+  const uint64_t f = f32x2_fma(nf, f32x2_pack(-1.f, -1.f), x);
+  auto both = [](float c) { return f32x2_pack(c, c); };
+  uint64_t q = f32x2_fma(both(0.0013276472454890609f), f, both(0.009675540961325169f));
+  q = f32x2_fma(q, f, both(0.05550713092088699f));
+  q = f32x2_fma(q, f, both(0.24022120237350464f));
+  q = f32x2_fma(q, f, both(0.6931469440460205f));
+  q = f32x2_fma(q, f, both(1.0000001192092896f));
+  float t0, t1, q0, q1;
+  f32x2_unpack(t, t0, t1);
+  f32x2_unpack(q, q0, q1);
+  return f32x2_pack(__int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23)),
+                    __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23)));
+}
+
 template <int DH>
 struct Smem {
   static constexpr int kPanels = DH / 64;
@@ -89,9 +118,9 @@ struct Smem {
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = 2 * kQBytes;
   static constexpr int kBarOff = kRingOff + kRing * kItem;
-  // full[ring], empty[ring], q_full[2], s_full[2], p_full[2], pv_done[2], q_empty, half_ready,
-  // half_free, drain, exit
-  static constexpr int kNumBars = 2 * kRing + 13;
+  // full[ring], empty[ring], q_full[2], s_full[2], p_full[2][2], pv_done[2], q_empty,
+  // half_ready, half_free, drain, exit
+  static constexpr int kNumBars = 2 * kRing + 15;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // holder, abort, ok, info[ring]
   static constexpr int kStartOff = kMiscOff + 16 + kRing * 4;
   static constexpr int kHalfOff = (kStartOff + 16 + 7) & ~7;  // float2 {base, sum}[128] of the second half
@@ -146,10 +175,13 @@ struct Cursor {
     group(p);
     flags();
   }
-  __device__ __forceinline__ void advance(const TcParams& p) {
-    ++t;
+  __device__ __forceinline__ void advance(const TcParams& p) { skip(1, p); }
+  // n tiles on, at most to the first tile of the next segment
+  __device__ __forceinline__ void skip(int n, const TcParams& p) {
+    t += n;
     if (t >= t1) return;
-    if (++lt == ntiles) {
+    lt += n;
+    if (lt == ntiles) {
       lt = 0;
       if (++qg == n_qg) {
         qg = 0;
@@ -277,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = bars + 2 * L::kRing;
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 2;
+  uint64_t* pv_done = p_full + 4;  // p_full[2 * m + half]: keys 0-63, 64-127
   uint64_t* q_empty = pv_done + 2;
   uint64_t* half_ready = q_empty + 1;
   uint64_t* half_free = half_ready + 1;
@@ -402,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int m = 0; m < 2; ++m) {
       mbar_init(&q_full[m], 1);
       mbar_init(&s_full[m], 1);
-      mbar_init(&p_full[m], 128);
+      mbar_init(&p_full[2 * m], 128);
+      mbar_init(&p_full[2 * m + 1], 128);
       mbar_init(&pv_done[m], 1);
     }
     mbar_init(q_empty, 1);
@@ -572,18 +605,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         };
-        auto issue_pv = [&](int m, int st, uint32_t acc0, bool v_done) {
-          const uint64_t dv = dv0 + (uint64_t)((st * L::kItem) >> 4);
+        // half of a unit's PV: 64 keys
+        auto issue_pv = [&](int m, int st, int half, uint32_t acc0, bool v_done) {
+          const uint64_t dv = dv0 + (uint64_t)((st * L::kItem + half * 64 * 128) >> 4);
           const uint32_t d = tmem_o + m * DH;
-          const uint32_t pcol = tmem_s + m * kBN;
+          const uint32_t pcol = tmem_s + m * kBN + half * 32;
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               // 16 keys: 8 columns of packed P, two 8-row groups of V
               umma_bf16_ts(d, pcol + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
                            kk > 0 ? 1u : acc0);
-            umma_commit(&pv_done[m]);
-            if (v_done) umma_commit(&empty[st]);
+            if (half == 1) {
+              umma_commit(&pv_done[m]);
+              if (v_done) umma_commit(&empty[st]);
+            }
           }
           __syncwarp();
         };
@@ -598,11 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           pend1 = -1;
           const int m = u & 1, vs = (u >> 8) & 0xff;
           if (!mbar_wait_bounded(&full[vs], (u >> 16) & 1, abort_flag, p.status) ||
-              !mbar_wait_bounded(&p_full[m], (np >> m) & 1u, abort_flag, p.status))
+              !mbar_wait_bounded(&p_full[2 * m], (np >> m) & 1u, abort_flag, p.status))
+            return false;
+          tc_fence_after();
+          issue_pv(m, vs, 0, (u & 2) ? 0u : 1u, false);
+          if (!mbar_wait_bounded(&p_full[2 * m + 1], (np >> m) & 1u, abort_flag, p.status))
             return false;
           np ^= 1u << m;
           tc_fence_after();
-          issue_pv(m, vs, (u & 2) ? 0u : 1u, (u & 4) != 0);
+          issue_pv(m, vs, 1, 1u, (u & 4) != 0);
           return true;
         };
         int ks = 0, at = 0;  // ring slot of K, tile of the piece
@@ -665,130 +705,183 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t srow = tmem_s + lane_off + m * kBN;
     const int tok_l = rl / p.G, g = rl - tok_l * p.G;  // token of the M tile, head of the group
-    uint32_t tcount = 0;          // units of this warpgroup so far
-    uint32_t halves = 0;          // one-tile pieces the second warpgroup took part in
+    uint32_t tcount = 0;  // units of this warpgroup so far
+    uint32_t halves = 0;  // one-tile pieces the second warpgroup took part in
     float m_used = -INFINITY, l_run = 0.f;
-    int at = 0, units = 0;        // tile of the piece, this warpgroup's units in it
-    int piece_lt0 = 0, piece_n = 0;
+    int units = 0;  // this warpgroup's units in the piece
     bool finite = true;
+    const uint64_t scale2 = f32x2_pack(p.scale_log2, p.scale_log2);
+
+    // One unit's scores to weights: the row's 128 scores come out of TMEM, the
+    // maximum and the sum stay in the thread, P goes back packed over the
+    // scores in two halves, so the first half's PV starts under the second.
+    // kFull: every slot of the tile is visible to every row of the warp;
+    // otherwise the row sees the first `limit`.
+    auto unit = [&](auto full_tag, int limit) {
+      constexpr bool kFull = decltype(full_tag)::value;
+      float sv[kBN];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[2][32];
+        tmem_ld32_raw(srow + h * 64, r[0]);
+        tmem_ld32_raw(srow + h * 64 + 32, r[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tmem_regs_after_wait(r[q]);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sv[h * 64 + q * 32 + c] = __uint_as_float(r[q][c]);
+        }
+      }
+      if (!kFull) {
+#pragma unroll
+        for (int c = 0; c < kBN; ++c)
+          if (c >= limit) sv[c] = -INFINITY;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < kBN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], sv[c], sv[c + 1]);
+      const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * p.scale_log2;
+      // The exponent base is a running maximum that only moves when a tile
+      // exceeds it by more than 2^8 (the stale base cancels in O / l).
+      const bool need = (m_used == -INFINITY) ? (mx != -INFINITY) : (mx > m_used + kLazy);
+      if (__any_sync(0xffffffffu, need)) {
+        const float new_m = need ? mx : m_used;
+        const float corr = (need && m_used != -INFINITY) ? ex2_approx(m_used - new_m) : 1.f;
+        if (units > 0) {
+          // O holds earlier units (their PV precedes this unit's QK)
+#pragma unroll 1
+          for (int ch = 0; ch < DH / 32; ++ch) {
+            float o[32];
+            const uint32_t ta = tmem_o + lane_off + m * DH + ch * 32;
+            tmem_ld32(ta, o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] *= corr;
+            tmem_st32(ta, o);
+          }
+        }
+        l_run *= corr;
+        m_used = new_m;
+      }
+      const float nbase = m_used == -INFINITY ? 0.f : -m_used;
+      const uint64_t nbase2 = f32x2_pack(nbase, nbase);
+      uint64_t part[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (h == 1 && e == 8) {
+            // the first half's P is in place
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[2 * m]);
+          }
+          const int c = h * 64 + 2 * e;
+          const uint64_t x2 = f32x2_fma(f32x2_pack(sv[c], sv[c + 1]), scale2, nbase2);
+          uint64_t a2;
+          if (kFull && e % kPolyEvery == kPolyEvery - 1) {
+            a2 = exp2_poly2(x2);
+          } else {
+            float x0, x1;
+            f32x2_unpack(x2, x0, x1);
+            a2 = f32x2_pack(ex2_approx(x0), ex2_approx(x1));
+          }
+          part[e & 3] = f32x2_add(part[e & 3], a2);
+          float a0, a1;
+          f32x2_unpack(a2, a0, a1);
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(a0, a1);
+          pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        tmem_st32_u(srow + h * 32, pk);
+      }
+      float s0, s1;
+      f32x2_unpack(f32x2_add(f32x2_add(part[0], part[1]), f32x2_add(part[2], part[3])), s0, s1);
+      l_run += s0 + s1;
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[2 * m + 1]);
+    };
+
+    // tiles of 128 consecutive slots: tile lt starts at slot 128 lt
+    const bool even_tiles = p.ppt > 0 ? p.kt == kBN : p.page % kBN == 0;
     Cursor cur;
     cur.init(start, t0, t1, p);
-    for (int j = 0; j < n_tiles; ++j, cur.advance(p)) {
+    int j0 = 0;  // first tile of the piece, in the CTA's range
+    bool ok = true;
+    for (; ok && j0 < n_tiles;) {
+      const int piece_lt0 = cur.lt;
+      const int piece_n = min(cur.ntiles - cur.lt, n_tiles - j0);
       const bool alt = cur.n_mt == 1;
-      if (cur.first) {
-        m_used = -INFINITY;
-        l_run = 0.f;
-        at = units = 0;
-        piece_lt0 = cur.lt;
-        piece_n = min(cur.ntiles - cur.lt, t1 - cur.t);
-      }
-      const int here = at++;
-      if (alt && (here & 1) != m) continue;
       const int tok = (cur.qg * 2 + (alt ? 0 : m)) * p.tpt + tok_l;
       const bool valid = tok_l < p.tpt && tok < cur.qlen;
-      int key0, nv, pg, r0;
-      cur.span(p, key0, nv, pg, r0);
-      // slots of the tile this row sees
-      const int limit = valid ? min(nv, cur.kv - cur.qlen + tok + 1 - key0) : 0;
-      if (!mbar_wait_bounded(&s_full[m], tcount & 1, abort_flag, p.status)) break;
-      tc_fence_after();
-      if ((alt || m == 0) && nv < cur.filled(p, r0)) {
-        // The tile's V rows from nv on belong to no slot of the segment and
-        // may hold anything: cleared once they have landed (the tile's PVs are
-        // issued after this warpgroup's arrival below).
-        const int item = 2 * j + 1, vs = item % L::kRing;
-        if (!mbar_wait_bounded(&full[vs], (item / L::kRing) & 1, abort_flag, p.status)) break;
-        uint8_t* vt = smem + L::kRingOff + vs * L::kItem;
-        for (int row = nv + quad; row < kBN; row += 4) {
-          if (lane < 8 * L::kPanels)
-            *reinterpret_cast<uint4*>(vt + (lane >> 3) * L::kPanel + row * 128 + (lane & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+      const int row_vis = cur.kv - cur.qlen + tok + 1;  // slots the row sees
+      const bool any = __any_sync(0xffffffffu, valid);
+      // leading tiles that every row of the warp sees whole; rows of no query
+      // take any score
+      const int warp_vis = __reduce_min_sync(0xffffffffu, valid ? max(row_vis, 0) : 0x7fffffff);
+      const int lt_full = even_tiles ? warp_vis / kBN : 0;
+      m_used = -INFINITY;
+      l_run = 0.f;
+      units = 0;
+      for (int x = alt ? m : 0; x < piece_n; x += alt ? 2 : 1) {
+        if (!mbar_wait_bounded(&s_full[m], tcount & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
         }
-        fence_proxy_async_smem();
-      }
-      // warps without a query row only keep the pipeline going
-      if (__any_sync(0xffffffffu, valid)) {
-        float sv[kBN];
-        {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32_raw(srow + q * 32, r[q]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_regs_after_wait(r[q]);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) sv[q * 32 + c] = __uint_as_float(r[q][c]);
-          }
+        tc_fence_after();
+        // the first PV of a piece overwrites O: the second half's of the last
+        // one-tile piece must have been read
+        if (m == 1 && units == 0 && halves > 0 &&
+            !mbar_wait_bounded(half_free, (halves - 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
         }
-        if (!__all_sync(0xffffffffu, limit >= kBN)) {
-#pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if (c >= limit) sv[c] = -INFINITY;
-        }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kBN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], sv[c], sv[c + 1]);
-        const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * p.scale_log2;
-        // The exponent base is a running maximum that only moves when a tile
-        // exceeds it by more than 2^8 (the stale base cancels in O / l).
-        const bool need = (m_used == -INFINITY) ? (mx != -INFINITY) : (mx > m_used + kLazy);
-        if (__any_sync(0xffffffffu, need)) {
-          const float new_m = need ? mx : m_used;
-          const float corr = (need && m_used != -INFINITY) ? ex2_approx(m_used - new_m) : 1.f;
-          if (units > 0) {
-            // O holds earlier units (their PV precedes this unit's QK)
-#pragma unroll 1
-            for (int ch = 0; ch < DH / 32; ++ch) {
-              float o[32];
-              const uint32_t ta = tmem_o + lane_off + m * DH + ch * 32;
-              tmem_ld32(ta, o);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] *= corr;
-              tmem_st32(ta, o);
+        cur.lt = piece_lt0 + x;
+        if (any && cur.lt < lt_full) {
+          unit(std::true_type{}, kBN);
+        } else {
+          int key0, nv, pg, r0;
+          cur.span(p, key0, nv, pg, r0);
+          if ((alt || m == 0) && nv < cur.filled(p, r0)) {
+            // The tile's V rows from nv on belong to no slot of the segment
+            // and may hold anything: cleared once they have landed (the
+            // tile's PVs are issued after this warpgroup's arrival).
+            const int item = 2 * (j0 + x) + 1, vs = item % L::kRing;
+            if (!mbar_wait_bounded(&full[vs], (item / L::kRing) & 1, abort_flag, p.status)) {
+              ok = false;
+              break;
             }
+            uint8_t* vt = smem + L::kRingOff + vs * L::kItem;
+            for (int row = nv + quad; row < kBN; row += 4) {
+              if (lane < 8 * L::kPanels)
+                *reinterpret_cast<uint4*>(vt + (lane >> 3) * L::kPanel + row * 128 +
+                                          (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
           }
-          l_run *= corr;
-          m_used = new_m;
-        }
-        const float nbase = m_used == -INFINITY ? 0.f : -m_used;
-        const uint64_t scale2 = f32x2_pack(p.scale_log2, p.scale_log2);
-        const uint64_t nbase2 = f32x2_pack(nbase, nbase);
-        uint64_t part[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int hq = 0; hq < 2; ++hq) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int c = hq * 64 + 2 * e;
-            float x0, x1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(sv[c], sv[c + 1]), scale2, nbase2), x0, x1);
-            const float a0 = ex2_approx(x0);
-            const float a1 = ex2_approx(x1);
-            part[e & 3] = f32x2_add(part[e & 3], f32x2_pack(a0, a1));
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a0, a1);
-            pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+          if (any) {
+            unit(std::false_type{}, valid ? min(nv, row_vis - key0) : kBN);
+          } else {
+            // warps without a query row only keep the pipeline going
+            tc_fence_before();
+            mbar_arrive(&p_full[2 * m]);
+            mbar_arrive(&p_full[2 * m + 1]);
           }
-          tmem_st32_u(srow + hq * 32, pk);
         }
-        float s0, s1;
-        f32x2_unpack(f32x2_add(f32x2_add(part[0], part[1]), f32x2_add(part[2], part[3])), s0, s1);
-        l_run += s0 + s1;
-        tmem_st_wait();
+        ++tcount;
+        ++units;
       }
-      // the first PV of a piece overwrites O: the second half's of the last
-      // one-tile piece must have been read
-      if (m == 1 && units == 0 && halves > 0 &&
-          !mbar_wait_bounded(half_free, (halves - 1) & 1, abort_flag, p.status))
-        break;
-      tc_fence_before();
-      mbar_arrive(&p_full[m]);
-      const uint32_t unit = tcount++;
-      ++units;
-      if (alt ? here + 2 < piece_n : !cur.last) continue;
+      if (!ok) break;
+      const int j_piece = j0;
+      j0 += piece_n;
+      cur.lt = piece_lt0;
+      const Cursor done = cur;
+      cur.skip(piece_n, p);
+      if (units == 0) continue;
 
       // ---- this warpgroup's share of the piece is complete ----
-      if (!mbar_wait_bounded(&pv_done[m], unit & 1, abort_flag, p.status)) break;
+      if (!mbar_wait_bounded(&pv_done[m], (tcount - 1) & 1, abort_flag, p.status)) break;
       tc_fence_after();
       if (alt && m == 1) {
         half_ml[rl] = make_float2(m_used, l_run);
@@ -826,10 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; ++c) o[c] = fmaf(x[c], w1, o[c]);
         }
       };
-      __nv_bfloat16* out = p.out + ((size_t)(cur.q0 + tok) * p.Hq + cur.kvh * p.G + g) * DH;
-      if (!__any_sync(0xffffffffu, valid)) {
+      __nv_bfloat16* out = p.out + ((size_t)(done.q0 + tok) * p.Hq + done.kvh * p.G + g) * DH;
+      if (!any) {
         // nothing to write
-      } else if (piece_lt0 == 0 && piece_n == cur.ntiles) {
+      } else if (piece_lt0 == 0 && piece_n == done.ntiles) {
 #pragma unroll 1
         for (int ch = 0; ch < DH / 32; ++ch) {
           float o[32];
@@ -837,9 +930,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid) finite = store_row32<DH>(out + ch * 32, o) && finite;
         }
       } else {
-        const int s0 = t0 + j - cur.lt;  // the segment's first tile
+        const int s0 = t0 + j_piece - piece_lt0;  // the segment's first tile
         const int c0 = s0 / per;
-        const int n_pieces = (s0 + cur.ntiles - 1) / per - c0 + 1;
+        const int n_pieces = (s0 + done.ntiles - 1) / per - c0 + 1;
         const size_t slot = piece_slot(blockIdx.x, per, s0);
         const int row = m * kMT + rl;
         float4* dst = reinterpret_cast<float4*>(p.o_part) + slot * (DH / 4) * kRows + row;
