@@ -54,7 +54,12 @@ constexpr int kRegsLow = 72;   // registers a thread: producer and MMA warpgroup
 constexpr int kRegsHigh = 216;  // softmax warpgroups
 constexpr float kLazy = 8.f;   // rescale O only when the maximum grows by 2^8
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMinTiles = 4;   // smallest tile range a CTA takes
+// What a CTA's range is measured in: the cost of a tile of two M tiles, of a
+// tile of one, and of a segment's start and end (its Q, its first scores, its
+// output).
+constexpr int kTwoCost = 4, kOneCost = 3;
+constexpr int kSegCost = 8;
+constexpr int kMinCost = 8;    // smallest range a CTA takes
 constexpr int kMaxB = 1024;
 
 struct TcParams {
@@ -123,7 +128,7 @@ struct Smem {
   static constexpr int kNumBars = 2 * kRing + 15;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // holder, abort, ok, info[ring]
   static constexpr int kStartOff = kMiscOff + 16 + kRing * 4;
-  static constexpr int kHalfOff = (kStartOff + 16 + 7) & ~7;  // float2 {base, sum}[128] of the second half
+  static constexpr int kHalfOff = (kStartOff + 20 + 7) & ~7;  // float2 {base, sum}[128] of the second half
   static constexpr int kBytes = kHalfOff + kMT * 8;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -142,11 +147,24 @@ __device__ __forceinline__ int group_vis(int qlen, int kv, int qg, const TcParam
   return max(0, kv - qlen + min(qlen, (qg + 1) * 2 * p.tpt));
 }
 
+__device__ __forceinline__ int group_mt(int qlen, int qg, const TcParams& p) {
+  return qlen - qg * 2 * p.tpt > p.tpt ? 2 : 1;
+}
+// length of a query group's segment on the axis below
+__device__ __forceinline__ int group_cost(int qlen, int kv, int qg, const TcParams& p) {
+  return tiles_of(group_vis(qlen, kv, qg, p), p) *
+             (group_mt(qlen, qg, p) == 2 ? kTwoCost : kOneCost) +
+         kSegCost;
+}
+
+// Walks the tiles of a CTA's range.  Segments lie end to end on one axis, each
+// tile wt long, kSegCost after its last; a tile belongs to the CTA in whose
+// stretch of the axis it starts.
 struct Cursor {
-  int t, t0, t1;
   int b, kvh, qg, n_qg, q0, qlen, kv;
-  int lt, ntiles, vis, n_mt;
-  bool first, last;
+  int lt, ntiles, vis, n_mt, wt;
+  int seg, end;  // start of the segment, end of the CTA's range
+  bool live, first, last;
 
   __device__ __forceinline__ void sequence(const TcParams& p) {
     q0 = p.cu_q[b];
@@ -157,37 +175,45 @@ struct Cursor {
   __device__ __forceinline__ void group(const TcParams& p) {
     vis = group_vis(qlen, kv, qg, p);
     ntiles = tiles_of(vis, p);
-    n_mt = qlen - qg * 2 * p.tpt > p.tpt ? 2 : 1;
+    n_mt = group_mt(qlen, qg, p);
+    wt = n_mt == 2 ? kTwoCost : kOneCost;
   }
-  __device__ __forceinline__ void flags() {
-    first = t == t0 || lt == 0;
-    last = t == t1 - 1 || lt == ntiles - 1;
+  // tiles of the segment from lt on that are the CTA's
+  __device__ __forceinline__ int piece() const {
+    return min(ntiles - lt, (end - seg - lt * wt + wt - 1) / wt);
   }
-  // s: {b, kvh, qg, lt} of tile t0
-  __device__ __forceinline__ void init(const int* s, int t0_, int t1_, const TcParams& p) {
-    t = t0 = t0_;
-    t1 = t1_;
+  // s: {b, kvh, qg, lt, seg}
+  __device__ __forceinline__ void init(const int* s, int end_, const TcParams& p) {
     b = s[0];
     kvh = s[1];
     qg = s[2];
     lt = s[3];
+    seg = s[4];
+    end = end_;
     sequence(p);
     group(p);
-    flags();
+    live = first = true;
+    last = piece() == 1;
   }
   __device__ __forceinline__ void advance(const TcParams& p) { skip(1, p); }
   // n tiles on, at most to the first tile of the next segment
   __device__ __forceinline__ void skip(int n, const TcParams& p) {
-    t += n;
-    if (t >= t1) return;
     lt += n;
-    if (lt == ntiles) {
+    first = false;
+    if (lt < ntiles) {
+      live = seg + lt * wt < end;
+    } else {
+      const int next = seg + ntiles * wt + kSegCost;
+      live = next < end;
+      if (!live) return;
+      seg = next;
       lt = 0;
+      first = true;
       if (++qg == n_qg) {
         qg = 0;
         if (++kvh == p.Hkv) {
           kvh = 0;
-          do {  // a later sequence with new tokens exists: t < t1 <= total
+          do {  // a later sequence with new tokens exists: the axis goes on
             ++b;
             sequence(p);
           } while (qlen == 0);
@@ -195,7 +221,7 @@ struct Cursor {
       }
       group(p);
     }
-    flags();
+    last = lt == ntiles - 1 || seg + (lt + 1) * wt >= end;
   }
   // first slot of the tile and how many of its slots the segment sees
   __device__ __forceinline__ void span(const TcParams& p, int& key0, int& nv, int& pg, int& r0) const {
@@ -244,8 +270,8 @@ __global__ void chunk_zero_kernel(unsigned int* __restrict__ cnt, int n) {
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) cnt[i] = 0u;
 }
 
-// slot of the workspace that holds the piece of a segment (first tile s0,
-// global) in CTA c
+// slot of the workspace that holds the piece of a segment (which starts at s0)
+// in CTA c
 __device__ __forceinline__ int piece_slot(int c, int per, int s0) {
   return 2 * c + (c * per >= s0 ? 0 : 1);
 }
@@ -322,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* start = reinterpret_cast<int*>(smem + L::kStartOff);     // {b, kvh, qg, lt}
   float2* half_ml = reinterpret_cast<float2*>(smem + L::kHalfOff);
 
-  // ---- schedule: cum[b] = tiles of the sequences before b (in the ring) ----
+  // ---- schedule: cum[b] = length of the sequences before b (in the ring) ----
   long long* cum = reinterpret_cast<long long*>(smem + L::kRingOff);
   long long* wsum = cum + kMaxB + 1;
   if (tid == 0) *sched_bad = 0;
@@ -340,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       continue;
     }
     long long n = 0;
-    for (int g = 0; g < n_qg; ++g) n += tiles_of(group_vis(a1 - a0, kv, g, p), p);
+    for (int g = 0; g < n_qg; ++g) n += group_cost(a1 - a0, kv, g, p);
     cum[b + 1] = n * p.Hkv;
   }
   __syncthreads();
@@ -353,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qlen = p.cu_q[b + 1] - p.cu_q[b], kv = p.kv_len[b];
     const int n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
     long long n = 0;
-    for (int g = lane; g < n_qg; g += 32) n += tiles_of(group_vis(qlen, kv, g, p), p);
+    for (int g = lane; g < n_qg; g += 32) n += group_cost(qlen, kv, g, p);
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     __syncwarp();
     if (lane == 0) cum[b + 1] = n * p.Hkv;
@@ -384,14 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int total = static_cast<int>(cum[p.B]);
-  const int per = max(kMinTiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int per = max(kMinCost, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   const long long t0l = (long long)blockIdx.x * per;
   if (t0l >= total) return;
   const int t0 = static_cast<int>(t0l);
   const int t1 = min(total, t0 + per);
-  const int n_tiles = t1 - t0;
   if (warp == 2) {
-    // the segment of tile t0
+    // the first tile that starts at t0 or later
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -405,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qlen = p.cu_q[lo + 1] - p.cu_q[lo], kv = p.kv_len[lo];
     int g0 = 0;
     for (;;) {
-      const int n = tiles_of(group_vis(qlen, kv, g0 + lane, p), p);
+      // beyond the last group the costs only have to be positive
+      const int n = group_cost(qlen, kv, g0 + lane, p);
       int s = n;
       for (int o = 1; o < 32; o <<= 1) {
         const int a = __shfl_up_sync(0xffffffffu, s, o);
@@ -415,15 +441,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (over != 0u) {
         const int at = __ffs(over) - 1;
         if (lane == at) {
+          const int in = rem - (s - n);  // t0 within the segment
+          const int wt = group_mt(qlen, g0 + at, p) == 2 ? kTwoCost : kOneCost;
           start[0] = lo;
           start[1] = kvh;
           start[2] = g0 + at;
-          start[3] = rem - (s - n);
+          start[3] = (in + wt - 1) / wt;
+          start[4] = t0 - in;
         }
         break;
       }
       rem -= __shfl_sync(0xffffffffu, s, 31);
       g0 += 32;
+    }
+  }
+  __syncthreads();
+  {
+    // past the segment's last tile: the next segment, if the range has one
+    Cursor c;
+    c.init(start, t1, p);
+    const bool move = c.lt >= c.ntiles;
+    if (move) c.skip(0, p);
+    __syncthreads();
+    if (move && !c.live) return;
+    if (c.seg + c.lt * c.wt >= t1) return;
+    if (move && tid == 0) {
+      start[0] = c.b;
+      start[1] = c.kvh;
+      start[2] = c.qg;
+      start[3] = c.lt;
+      start[4] = c.seg;
     }
   }
   if (tid == 0) {
@@ -484,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K/V that several query groups read stays in L2, the rest passes by
       const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
       Cursor cur;
-      cur.init(start, t0, t1, p);
+      cur.init(start, t1, p);
       // A tile's page ids (one per lane) are fetched a tile ahead: the read
       // would otherwise hold up the copies of every tile.
       auto page_id = [&](const Cursor& x) {
@@ -503,12 +550,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, bad_page = false;
       int issued = 0;  // ring items whose copies were started
       Cursor ahead = cur;
-      for (int j = 0; ok && j < n_tiles; ++j, cur = ahead) {
+      for (; ok && cur.live; cur = ahead) {
         int key0, nv, pg, r0;
         cur.span(p, key0, nv, pg, r0);
         const int id = next_id;
         ahead.advance(p);
-        if (j + 1 < n_tiles) next_id = page_id(ahead);
+        if (ahead.live) next_id = page_id(ahead);
         bool mine = id != INT_MIN;
         if (mine && (id < 0 || id >= p.n_pages)) {
           bad_page = true;
@@ -522,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag, p.status);
             if (ok) {
               if (kvi == 0)
-                info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0) | (cur.last ? 4 : 0);
+                info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0) | (cur.last ? 4 : 0) |
+                             (ahead.live ? 0 : 8);
               if (bytes > 0) mbar_arrive_expect_tx(&full[slot], bytes);
               else mbar_arrive(&full[slot]);
             }
@@ -648,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ks = 0, at = 0;  // ring slot of K, tile of the piece
         uint32_t kph = 0;
         bool ok = true;
-        for (int j = 0; ok && j < n_tiles; ++j) {
+        for (bool more = true; ok && more;) {
           int vs = ks + 1;
           uint32_t vph = kph;
           if (vs == L::kRing) {
@@ -659,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait_bounded(&full[ks], kph, abort_flag, p.status)) break;
           const int word = __shfl_sync(0xffffffffu, info[ks], 0);
           const bool first = (word & 1) != 0, two = (word & 2) != 0;
+          more = (word & 8) == 0;
           if (first) at = 0;
           for (int m = two ? 0 : at & 1;; ++m) {
             while (ok && ((pend0 >= 0 && (pend0 & 1) == m) || (pend1 >= 0 && (pend1 & 1) == m)))
@@ -803,15 +852,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&p_full[2 * m + 1]);
     };
 
-    // tiles of 128 consecutive slots: tile lt starts at slot 128 lt
-    const bool even_tiles = p.ppt > 0 ? p.kt == kBN : p.page % kBN == 0;
+    // how many leading tiles are 128 consecutive slots from slot 128 lt on
+    // (all, unless pages end inside tiles)
+    const int even_lt = p.ppt > 0 ? (p.kt == kBN ? INT_MAX : 0)
+                                  : (p.page % kBN == 0 ? INT_MAX : p.page / kBN);
     Cursor cur;
-    cur.init(start, t0, t1, p);
-    int j0 = 0;  // first tile of the piece, in the CTA's range
+    cur.init(start, t1, p);
+    int j0 = 0;  // tiles before the piece
     bool ok = true;
-    for (; ok && j0 < n_tiles;) {
+    while (ok && cur.live) {
       const int piece_lt0 = cur.lt;
-      const int piece_n = min(cur.ntiles - cur.lt, n_tiles - j0);
+      const int piece_n = cur.piece();
       const bool alt = cur.n_mt == 1;
       const int tok = (cur.qg * 2 + (alt ? 0 : m)) * p.tpt + tok_l;
       const bool valid = tok_l < p.tpt && tok < cur.qlen;
@@ -820,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // leading tiles that every row of the warp sees whole; rows of no query
       // take any score
       const int warp_vis = __reduce_min_sync(0xffffffffu, valid ? max(row_vis, 0) : 0x7fffffff);
-      const int lt_full = even_tiles ? warp_vis / kBN : 0;
+      const int lt_full = min(warp_vis / kBN, even_lt);
       m_used = -INFINITY;
       l_run = 0.f;
       units = 0;
@@ -873,7 +924,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++units;
       }
       if (!ok) break;
-      const int j_piece = j0;
       j0 += piece_n;
       cur.lt = piece_lt0;
       const Cursor done = cur;
@@ -930,9 +980,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid) finite = store_row32<DH>(out + ch * 32, o) && finite;
         }
       } else {
-        const int s0 = t0 + j_piece - piece_lt0;  // the segment's first tile
+        const int s0 = done.seg;
         const int c0 = s0 / per;
-        const int n_pieces = (s0 + done.ntiles - 1) / per - c0 + 1;
+        const int n_pieces = (s0 + (done.ntiles - 1) * done.wt) / per - c0 + 1;
         const size_t slot = piece_slot(blockIdx.x, per, s0);
         const int row = m * kMT + rl;
         float4* dst = reinterpret_cast<float4*>(p.o_part) + slot * (DH / 4) * kRows + row;
