@@ -128,11 +128,11 @@ struct Smem {
   static constexpr int kNumBars = 2 * kRing + 15;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // holder, abort, ok, info[ring]
   static constexpr int kStartOff = kMiscOff + 16 + kRing * 4;
-  static constexpr int kHalfOff = (kStartOff + 20 + 7) & ~7;  // float2 {base, sum}[128] of the second half
+  static constexpr int kHalfOff = (kStartOff + 40 + 7) & ~7;  // float2 {base, sum}[128] of the second half
   static constexpr int kBytes = kHalfOff + kMT * 8;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  static_assert((kMaxB + 1) * 8 + 16 * 8 <= kRing * kItem, "schedule fits in the ring");
+  static_assert((kMaxB + 1) * 4 <= kRing * kItem, "schedule fits in the ring");
 };
 
 // key tiles that cover `vis` slots (at least one, so an empty row is written)
@@ -182,15 +182,18 @@ struct Cursor {
   __device__ __forceinline__ int piece() const {
     return min(ntiles - lt, (end - seg - lt * wt + wt - 1) / wt);
   }
-  // s: {b, kvh, qg, lt, seg}
+  // s: {b, kvh, qg, lt, seg, q0, qlen, kv}
   __device__ __forceinline__ void init(const int* s, int end_, const TcParams& p) {
     b = s[0];
     kvh = s[1];
     qg = s[2];
     lt = s[3];
     seg = s[4];
+    q0 = s[5];
+    qlen = s[6];
+    kv = s[7];
     end = end_;
-    sequence(p);
+    n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
     group(p);
     live = first = true;
     last = piece() == 1;
@@ -276,43 +279,228 @@ __device__ __forceinline__ int piece_slot(int c, int per, int s0) {
   return 2 * c + (c * per >= s0 ? 0 : 1);
 }
 
-// The merge of a row's pieces (CTAs c0 .. c0 + n - 1) by the last to arrive.
+// The merge of the pieces (CTAs c0 .. c0 + n - 1) of a warp's rows by the last
+// to arrive: weights 2^(lse - max lse) over their sum.  `rows`: lanes with a
+// row; row0: lane 0's row of the segment.  Partials of other CTAs are read past
+// L1 (they were released by a fence before their count).
 template <int DH>
-__device__ __noinline__ bool merge_row(const TcParams& p, __nv_bfloat16* out, int c0, int n, int per,
-                                       int s0, int row) {
+__device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, unsigned int rows,
+                                        int c0, int n, int per, int s0, int row0) {
+  const int lane = threadIdx.x & 31;
+  const bool valid = (rows >> lane) & 1u;
+  bool finite = true;
+  if (__popc(rows) <= 8) {
+    // few rows (single tokens): the warp takes a row's pieces together, lanes
+    // over the columns, four pieces' loads in flight
+    constexpr int kCols = DH / 32;  // columns a lane
+    for (unsigned int left = rows; left != 0u; left &= left - 1) {
+      const int src = __ffs(left) - 1, row = row0 + src;
+      float M = -INFINITY, sum = 0.f;
+      for (int k0 = 0; k0 < n; k0 += 32) {
+        const int k = k0 + lane;
+        const float l =
+            k < n ? __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row) : -INFINITY;
+        float mx = l;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float Mn = fmaxf(M, mx);
+        float e = l == -INFINITY ? 0.f : exp2f(l - Mn);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+        sum = (M == -INFINITY ? 0.f : sum * exp2f(M - Mn)) + e;
+        M = Mn;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : sum;
+      float acc[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const size_t slot = piece_slot(c0 + k, per, s0);
+        const float l = __ldcg(p.lse_part + slot * kRows + row);
+        // columns 4 g .. 4 g + 3 of the row are one group of 4 floats
+        const float* v = p.o_part + ((slot * (DH / 4) + lane * kCols / 4) * kRows + row) * 4 +
+                         (lane * kCols) % 4;
+        float x[kCols];
+        if (kCols == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(v));
+          x[0] = y.x;
+          x[1] = y.y;
+          x[kCols - 2] = y.z;
+          x[kCols - 1] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(v));
+          x[0] = y.x;
+          x[kCols - 1] = y.y;
+        }
+        const float w = l == -INFINITY ? 0.f : exp2f(l - M) * inv;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] += w * x[c];
+      }
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), src));
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2) {
+        finite = finite && fabsf(acc[c]) < INFINITY && fabsf(acc[c + 1]) < INFINITY;
+        *reinterpret_cast<__nv_bfloat162*>(dst + lane * kCols + c) =
+            __floats2bfloat162_rn(acc[c], acc[c + 1]);
+      }
+    }
+    return finite;
+  }
+  // a row per lane
+  const int row = row0 + lane;
   float M = -INFINITY;
+#pragma unroll 4
   for (int k = 0; k < n; ++k)
     M = fmaxf(M, __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row));
-  float wsum = 0.f;
+  float sum = 0.f;
+#pragma unroll 4
   for (int k = 0; k < n; ++k) {
-    const float lse = __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row);
-    wsum += lse == -INFINITY ? 0.f : exp2f(lse - M);
+    const float l = __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row);
+    sum += l == -INFINITY ? 0.f : exp2f(l - M);
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  bool finite = true;
+  const float inv = sum > 0.f ? 1.f / sum : sum;
 #pragma unroll 1
   for (int ch = 0; ch < DH / 32; ++ch) {
     float acc[32];
 #pragma unroll
     for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+#pragma unroll 2
     for (int k = 0; k < n; ++k) {
       const size_t slot = piece_slot(c0 + k, per, s0);
-      const float lse = __ldcg(p.lse_part + slot * kRows + row);
-      const float w = lse == -INFINITY ? 0.f : exp2f(lse - M) * inv;
+      const float l = __ldcg(p.lse_part + slot * kRows + row);
       const float4* src = reinterpret_cast<const float4*>(p.o_part) +
                           (slot * (DH / 4) + ch * 8) * kRows + row;
+      float4 v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = __ldcg(src + c * kRows);
+      const float w = l == -INFINITY ? 0.f : exp2f(l - M) * inv;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float4 v = __ldcg(src + c * kRows);
-        acc[4 * c] += w * v.x;
-        acc[4 * c + 1] += w * v.y;
-        acc[4 * c + 2] += w * v.z;
-        acc[4 * c + 3] += w * v.w;
+        acc[4 * c] += w * v[c].x;
+        acc[4 * c + 1] += w * v[c].y;
+        acc[4 * c + 2] += w * v[c].z;
+        acc[4 * c + 3] += w * v[c].w;
       }
     }
-    finite = store_row32<DH>(out + ch * 32, acc) && finite;
+    if (valid) finite = store_row32<DH>(out + ch * 32, acc) && finite;
   }
   return finite;
+}
+
+// One warp finds the CTA's stretch of the axis and the first tile that starts
+// in it: out = {b, kvh, qg, lt, seg, q0, qlen, kv, end, length of a stretch},
+// end 0 when no tile does or a length is out of range (reported).  cum (shared
+// memory, B + 1 words): length of the sequences before b.
+template <int DH>
+__device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, int cta, int grid) {
+  const int lane = threadIdx.x & 31;
+  bool ok = true;
+  long long run = 0;
+  if (lane == 0) cum[0] = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int qlen = 0, kv = 0;
+    if (b < p.B) {
+      const int a0 = p.cu_q[b], a1 = p.cu_q[b + 1];
+      kv = p.kv_len[b];
+      qlen = a1 - a0;
+      ok = ok && a0 >= 0 && a1 >= a0 && a1 <= p.T && kv >= 0 &&
+           kv <= (long long)p.max_pages * p.page;
+    }
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const int n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
+    long long n = 0;
+    if (n_qg <= 4)
+      for (int g = 0; g < n_qg; ++g) n += group_cost(qlen, kv, g, p);
+    // long chunks: the lanes share their query groups
+    for (unsigned int todo = __ballot_sync(0xffffffffu, n_qg > 4); todo != 0u; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int q = __shfl_sync(0xffffffffu, qlen, src), k = __shfl_sync(0xffffffffu, kv, src);
+      const int groups = __shfl_sync(0xffffffffu, n_qg, src);
+      long long s = 0;
+      for (int g = lane; g < groups; g += 32) s += group_cost(q, k, g, p);
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == src) n = s;
+    }
+    n *= p.Hkv;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long a = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += a;
+    }
+    n += run;
+    if (n > 0x7fffffffLL) ok = false;
+    if (b < p.B) cum[b + 1] = static_cast<int>(n);
+    run = __shfl_sync(0xffffffffu, n, 31);
+    if (!__all_sync(0xffffffffu, ok)) break;
+  }
+  __syncwarp();
+  if (!__all_sync(0xffffffffu, ok)) {
+    if (lane == 0) {
+      if (cta == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      out[8] = 0;
+    }
+    return;
+  }
+  const int total = static_cast<int>(run);
+  const int per = max(kMinCost, (total + grid - 1) / grid);
+  const long long first = (long long)cta * per;
+  if (first >= total) {
+    if (lane == 0) out[8] = 0;
+    return;
+  }
+  const int t0 = static_cast<int>(first), t1 = min(total, t0 + per);
+  int lo = 0, hi = p.B;  // cum[lo] <= t0 < cum[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= t0) lo = mid;
+    else hi = mid;
+  }
+  const int per_head = (cum[lo + 1] - cum[lo]) / p.Hkv;
+  int rem = t0 - cum[lo];
+  int s[8] = {lo, rem / per_head, 0, 0, 0, p.cu_q[lo], 0, p.kv_len[lo]};
+  rem -= s[1] * per_head;
+  s[6] = p.cu_q[lo + 1] - s[5];
+  for (int g0 = 0;; g0 += 32) {
+    // beyond the last group the costs only have to be positive
+    const int n = group_cost(s[6], s[7], g0 + lane, p);
+    int c = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += a;
+    }
+    const unsigned int over = __ballot_sync(0xffffffffu, c > rem);
+    if (over != 0u) {
+      const int at = __ffs(over) - 1;
+      const int in = __shfl_sync(0xffffffffu, rem - (c - n), at);  // t0 within the segment
+      const int wt = group_mt(s[6], g0 + at, p) == 2 ? kTwoCost : kOneCost;
+      s[2] = g0 + at;
+      s[3] = (in + wt - 1) / wt;
+      s[4] = t0 - in;
+      break;
+    }
+    rem -= __shfl_sync(0xffffffffu, c, 31);
+  }
+  Cursor c;
+  c.init(s, t1, p);
+  if (c.lt >= c.ntiles) {
+    c.skip(0, p);  // past the last tile: the next segment, if the stretch has one
+  } else {
+    c.live = c.seg + c.lt * c.wt < t1;
+  }
+  if (lane == 0) {
+    out[0] = c.b;
+    out[1] = c.kvh;
+    out[2] = c.qg;
+    out[3] = c.lt;
+    out[4] = c.seg;
+    out[5] = c.q0;
+    out[6] = c.qlen;
+    out[7] = c.kv;
+    out[8] = c.live ? t1 : 0;
+    out[9] = per;
+  }
 }
 
 template <int DH>
@@ -343,137 +531,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* exit_bar = drain + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  volatile int* sched_bad = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
   int* info = reinterpret_cast<int*>(smem + L::kMiscOff + 16);  // per ring slot, with each K
-  int* start = reinterpret_cast<int*>(smem + L::kStartOff);     // {b, kvh, qg, lt}
+  int* start = reinterpret_cast<int*>(smem + L::kStartOff);     // what schedule() finds
   float2* half_ml = reinterpret_cast<float2*>(smem + L::kHalfOff);
 
-  // ---- schedule: cum[b] = length of the sequences before b (in the ring) ----
-  long long* cum = reinterpret_cast<long long*>(smem + L::kRingOff);
-  long long* wsum = cum + kMaxB + 1;
-  if (tid == 0) *sched_bad = 0;
-  __syncthreads();
-  for (int b = tid; b < p.B; b += kThreads) {
-    const int a0 = p.cu_q[b], a1 = p.cu_q[b + 1], kv = p.kv_len[b];
-    if (a0 < 0 || a1 < a0 || a1 > p.T || kv < 0 || kv > (long long)p.max_pages * p.page) {
-      *sched_bad = 1;
-      cum[b + 1] = 0;
-      continue;
-    }
-    const int n_qg = (a1 - a0 + 2 * p.tpt - 1) / (2 * p.tpt);
-    if (n_qg > 4) {
-      cum[b + 1] = -1;  // left to a warp
-      continue;
-    }
-    long long n = 0;
-    for (int g = 0; g < n_qg; ++g) n += group_cost(a1 - a0, kv, g, p);
-    cum[b + 1] = n * p.Hkv;
-  }
-  __syncthreads();
-  if (*sched_bad) {
-    if (tid == 0 && blockIdx.x == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-    return;
-  }
-  for (int b = warp; b < p.B; b += kThreads / 32) {
-    if (cum[b + 1] >= 0) continue;
-    const int qlen = p.cu_q[b + 1] - p.cu_q[b], kv = p.kv_len[b];
-    const int n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
-    long long n = 0;
-    for (int g = lane; g < n_qg; g += 32) n += group_cost(qlen, kv, g, p);
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    __syncwarp();
-    if (lane == 0) cum[b + 1] = n * p.Hkv;
-  }
-  __syncthreads();
-  {  // inclusive scan over the sequences
-    const int each = (p.B + kThreads - 1) / kThreads;
-    long long n = 0;
-    for (int i = tid * each; i < min(p.B, (tid + 1) * each); ++i) n += cum[i + 1];
-    long long s = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += a;
-    }
-    if (lane == 31) wsum[warp] = s;
-    __syncthreads();
-    s -= n;
-    for (int w = 0; w < warp; ++w) s += wsum[w];
-    for (int i = tid * each; i < min(p.B, (tid + 1) * each); ++i) {
-      s += cum[i + 1];
-      cum[i + 1] = s;
-    }
-    if (tid == 0) cum[0] = 0;
-  }
-  __syncthreads();
-  if (cum[p.B] > 0x7fffffffLL) {
-    if (tid == 0 && blockIdx.x == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-    return;
-  }
-  const int total = static_cast<int>(cum[p.B]);
-  const int per = max(kMinCost, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const long long t0l = (long long)blockIdx.x * per;
-  if (t0l >= total) return;
-  const int t0 = static_cast<int>(t0l);
-  const int t1 = min(total, t0 + per);
-  if (warp == 2) {
-    // the first tile that starts at t0 or later
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid] <= t0) lo = mid;
-      else hi = mid;
-    }
-    const int per_head = static_cast<int>((cum[lo + 1] - cum[lo]) / p.Hkv);
-    int rem = t0 - static_cast<int>(cum[lo]);
-    const int kvh = rem / per_head;
-    rem -= kvh * per_head;
-    const int qlen = p.cu_q[lo + 1] - p.cu_q[lo], kv = p.kv_len[lo];
-    int g0 = 0;
-    for (;;) {
-      // beyond the last group the costs only have to be positive
-      const int n = group_cost(qlen, kv, g0 + lane, p);
-      int s = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += a;
-      }
-      const unsigned int over = __ballot_sync(0xffffffffu, s > rem);
-      if (over != 0u) {
-        const int at = __ffs(over) - 1;
-        if (lane == at) {
-          const int in = rem - (s - n);  // t0 within the segment
-          const int wt = group_mt(qlen, g0 + at, p) == 2 ? kTwoCost : kOneCost;
-          start[0] = lo;
-          start[1] = kvh;
-          start[2] = g0 + at;
-          start[3] = (in + wt - 1) / wt;
-          start[4] = t0 - in;
-        }
-        break;
-      }
-      rem -= __shfl_sync(0xffffffffu, s, 31);
-      g0 += 32;
-    }
-  }
-  __syncthreads();
-  {
-    // past the segment's last tile: the next segment, if the range has one
-    Cursor c;
-    c.init(start, t1, p);
-    const bool move = c.lt >= c.ntiles;
-    if (move) c.skip(0, p);
-    __syncthreads();
-    if (move && !c.live) return;
-    if (c.seg + c.lt * c.wt >= t1) return;
-    if (move && tid == 0) {
-      start[0] = c.b;
-      start[1] = c.kvh;
-      start[2] = c.qg;
-      start[3] = c.lt;
-      start[4] = c.seg;
-    }
-  }
-  if (tid == 0) {
+  // ---- barriers, tensor memory and (one warp) the CTA's range ----
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
+    schedule<DH>(p, reinterpret_cast<int*>(smem + L::kRingOff), start, blockIdx.x, gridDim.x);
+    fence_proxy_async_smem();  // the ring is the copies' from here on
+  } else if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -492,31 +561,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(exit_bar, kThreads);
     *abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, kTmemCols);
-    tmem_relinquish();
-  }
-  __syncthreads();  // the schedule in the ring has been read
-  // Rows that no copy ever writes are cleared once: of the Q tiles past their
-  // tokens, of the key tiles past a full tile's slots (their weights are zero,
-  // but 0 * NaN is not).
-  {
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    const int q_rows = p.G * p.tpt;
-    if (q_rows < kMT) {
-      for (int i = tid; i < 2 * L::kQBytes / 16; i += kThreads)
-        reinterpret_cast<uint4*>(smem + L::kQOff)[i] = z;
-    }
-    if (p.ppt > 0 && p.kt < kBN) {
-      for (int i = tid; i < L::kRing * L::kItem / 16; i += kThreads)
-        reinterpret_cast<uint4*>(smem + L::kRingOff)[i] = z;
-    }
-    fence_proxy_async_smem();
-  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (start[8] == 0) {  // no tile is this CTA's
+    if (warp == 1) tmem_dealloc(*tmem_holder, kTmemCols);
+    return;
+  }
+  const int t1 = start[8], per = start[9];
+  // Rows that no copy ever writes are cleared once: of the Q tiles past their
+  // tokens, of the key tiles past a full tile's slots (their weights are zero,
+  // but 0 * NaN is not).
+  if (p.G * p.tpt < kMT || (p.ppt > 0 && p.kt < kBN)) {
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < L::kBarOff / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = z;
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   const uint32_t tmem_base = *tmem_holder;
   const uint32_t tmem_o = tmem_base;           // O[m]: DH columns each
   const uint32_t tmem_s = tmem_base + 2 * DH;  // S[m], then P[m]: 128 columns each
@@ -526,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 "register split exceeds the launch's allocation");
   if (warp < 4) {
     warpgroup_regs_dec<kRegsLow>();
-    if (warp == 0) {
-      // ---------------- TMA producer ----------------
+    if (warp == 0 || warp == 2) {
+      // ---------------- TMA producers: K and Q (warp 0), V (warp 2) ----------------
+      const bool is_v = warp == 2;
       // K/V that several query groups read stays in L2, the rest passes by
       const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
       Cursor cur;
@@ -544,11 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int panel_rows = p.ppt > 0 ? p.page : kBN;
       const uint32_t box_bytes = static_cast<uint32_t>(panel_rows) * 128u * L::kPanels;
       const uint32_t q_bytes = static_cast<uint32_t>(p.G * p.tpt) * 128u * L::kPanels;
-      int slot = 0;
+      int slot = is_v ? 1 : 0;
       uint32_t phase = 0, n_pieces = 0;
       uint32_t q_loads0 = 0, q_loads1 = 0;
       bool ok = true, bad_page = false;
-      int issued = 0;  // ring items whose copies were started
+      int issued = 0;  // copies of this warp's tiles that were started
       Cursor ahead = cur;
       for (; ok && cur.live; cur = ahead) {
         int key0, nv, pg, r0;
@@ -561,64 +628,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           bad_page = true;
           mine = false;
         }
-        const uint64_t pol = cur.n_qg > 1 ? keep : pass;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag, p.status);
+          if (ok) {
+            if (!is_v)
+              info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0) | (cur.last ? 4 : 0) |
+                           (ahead.live ? 0 : 8);
+            if (bytes > 0) mbar_arrive_expect_tx(&full[slot], bytes);
+            else mbar_arrive(&full[slot]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        ++issued;
+        if (mine) {
+          const uint64_t pol = cur.n_qg > 1 ? keep : pass;
+          uint8_t* dst = smem + L::kRingOff + slot * L::kItem + lane * panel_rows * 128;
 #pragma unroll
-        for (int kvi = 0; kvi < 2; ++kvi) {
+          for (int pn = 0; pn < L::kPanels; ++pn)
+            tma_load_4d(dst + pn * L::kPanel, is_v ? &tmV : &tmK, &full[slot], pn * 64, r0, cur.kvh,
+                        id, pol);
+        }
+        if (!is_v && cur.first) {
+          // the piece's Q tiles, once the last piece's scores are done
           if (lane == 0) {
-            ok = mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag, p.status);
+            if (n_pieces > 0)
+              ok = mbar_wait_bounded(q_empty, (n_pieces - 1) & 1, abort_flag, p.status);
             if (ok) {
-              if (kvi == 0)
-                info[slot] = (cur.first ? 1 : 0) | (cur.n_mt > 1 ? 2 : 0) | (cur.last ? 4 : 0) |
-                             (ahead.live ? 0 : 8);
-              if (bytes > 0) mbar_arrive_expect_tx(&full[slot], bytes);
-              else mbar_arrive(&full[slot]);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          ++issued;
-          if (mine) {
-            uint8_t* dst = smem + L::kRingOff + slot * L::kItem + lane * panel_rows * 128;
+              for (int m = 0; m < cur.n_mt; ++m) {
+                mbar_arrive_expect_tx(&q_full[m], q_bytes);
 #pragma unroll
-            for (int pn = 0; pn < L::kPanels; ++pn)
-              tma_load_4d(dst + pn * L::kPanel, kvi == 0 ? &tmK : &tmV, &full[slot], pn * 64, r0,
-                          cur.kvh, id, pol);
-          }
-          if (++slot == L::kRing) {
-            slot = 0;
-            phase ^= 1u;
-          }
-          if (kvi == 0 && cur.first) {
-            // the piece's Q tiles, once the last piece's scores are done
-            if (lane == 0) {
-              if (n_pieces > 0)
-                ok = mbar_wait_bounded(q_empty, (n_pieces - 1) & 1, abort_flag, p.status);
-              if (ok) {
-                for (int m = 0; m < cur.n_mt; ++m) {
-                  mbar_arrive_expect_tx(&q_full[m], q_bytes);
-#pragma unroll
-                  for (int pn = 0; pn < L::kPanels; ++pn)
-                    tma_load_4d(smem + L::kQOff + m * L::kQBytes + pn * (kMT * 128), &tmQ,
-                                &q_full[m], pn * 64, 0, cur.kvh,
-                                cur.q0 + (cur.qg * 2 + m) * p.tpt, l2_policy_evict_first());
-                  if (m == 0) ++q_loads0;
-                  else ++q_loads1;
-                }
+                for (int pn = 0; pn < L::kPanels; ++pn)
+                  tma_load_4d(smem + L::kQOff + m * L::kQBytes + pn * (kMT * 128), &tmQ, &q_full[m],
+                              pn * 64, 0, cur.kvh, cur.q0 + (cur.qg * 2 + m) * p.tpt, pass);
+                if (m == 0) ++q_loads0;
+                else ++q_loads1;
               }
             }
-            ++n_pieces;
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
           }
+          ++n_pieces;
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        slot += 2;
+        if (slot >= L::kRing) {
+          slot -= L::kRing;
+          phase ^= 1u;
         }
       }
       if (bad_page) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-      // every copy started has landed before the CTA may end
+      // every copy started has landed before the CTA may end (the copies of
+      // slots that were used again have been consumed)
       if (lane == 0) {
         int no_abort = 0;
-        for (int x = max(0, issued - L::kRing); x < issued; ++x)
-          mbar_wait_bounded(&full[x % L::kRing], (x / L::kRing) & 1, &no_abort, p.status);
+        for (int x = max(0, issued - L::kRing); x < issued; ++x) {
+          const int item = 2 * x + (is_v ? 1 : 0);
+          if (item < 2 * issued - L::kRing) continue;
+          mbar_wait_bounded(&full[item % L::kRing], (item / L::kRing) & 1, &no_abort, p.status);
+        }
         if (q_loads0 > 0) mbar_wait_bounded(&q_full[0], (q_loads0 - 1) & 1, &no_abort, p.status);
         if (q_loads1 > 0) mbar_wait_bounded(&q_full[1], (q_loads1 - 1) & 1, &no_abort, p.status);
       }
@@ -1008,7 +1075,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == static_cast<unsigned int>(n_pieces - 1)) {
           __threadfence();
-          if (valid) finite = merge_row<DH>(p, out, c0, n_pieces, per, s0, row) && finite;
+          finite = merge_rows<DH>(p, out, __ballot_sync(0xffffffffu, valid), c0, n_pieces, per, s0,
+                                  row - lane) && finite;
         }
       }
       tc_fence_before();
