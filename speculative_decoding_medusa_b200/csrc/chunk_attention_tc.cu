@@ -61,6 +61,7 @@ constexpr int kTwoCost = 4, kOneCost = 3;
 constexpr int kSegCost = 8;
 constexpr int kMinCost = 8;    // smallest range a CTA takes
 constexpr int kMaxB = 1024;
+constexpr int kFewRows = 8;    // rows of a warp whose pieces the whole warp merges
 
 struct TcParams {
   const int32_t *table, *cu_q, *kv_len;
@@ -70,7 +71,8 @@ struct TcParams {
   int B, T, Hq, Hkv, G, tpt;  // tpt: tokens per M tile
   float scale_log2;
   __nv_bfloat16* out;
-  float* o_part;             // [2 * grid][dh / 4][256] groups of 4 floats
+  float* o_part;             // [2 * grid] pieces of [8] warps' rows: groups of 4 columns
+                             // [dh / 4][32 rows], or whole rows [32][dh] (kFewRows)
   float* lse_part;           // [2 * grid][256]
   unsigned int* piece_count;  // [grid][8] pieces written, per warp of the segment that
                               // starts in the CTA and leaves it (zeroed per call)
@@ -289,61 +291,106 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
   const int lane = threadIdx.x & 31;
   const bool valid = (rows >> lane) & 1u;
   bool finite = true;
-  if (__popc(rows) <= 8) {
-    // few rows (single tokens): the warp takes a row's pieces together, lanes
-    // over the columns, four pieces' loads in flight
+  if (__popc(rows) <= kFewRows) {
+    // few rows (single tokens): the warp takes four rows together, lanes over
+    // the pieces for the weights, then over the columns; a step's loads of
+    // all four rows are in flight together
     constexpr int kCols = DH / 32;  // columns a lane
-    for (unsigned int left = rows; left != 0u; left &= left - 1) {
-      const int src = __ffs(left) - 1, row = row0 + src;
-      float M = -INFINITY, sum = 0.f;
+    constexpr int kR = 4, kK = 2;   // rows and pieces of a step
+    for (unsigned int left = rows; left != 0u;) {
+      int src[kR];
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        src[i] = left != 0u ? __ffs(left) - 1 : -1;
+        left &= left - 1;
+      }
+      float M[kR], sum[kR], l[kR];
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        M[i] = -INFINITY;
+        sum[i] = 0.f;
+      }
       for (int k0 = 0; k0 < n; k0 += 32) {
-        const int k = k0 + lane;
-        const float l =
-            k < n ? __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row) : -INFINITY;
-        float mx = l;
+        const float* lse = p.lse_part + (size_t)piece_slot(c0 + k0 + lane, per, s0) * kRows + row0;
+        float mx[kR], e[kR];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float Mn = fmaxf(M, mx);
-        float e = l == -INFINITY ? 0.f : exp2f(l - Mn);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
-        sum = (M == -INFINITY ? 0.f : sum * exp2f(M - Mn)) + e;
-        M = Mn;
-      }
-      const float inv = sum > 0.f ? 1.f / sum : sum;
-      float acc[kCols];
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const size_t slot = piece_slot(c0 + k, per, s0);
-        const float l = __ldcg(p.lse_part + slot * kRows + row);
-        // columns 4 g .. 4 g + 3 of the row are one group of 4 floats
-        const float* v = p.o_part + ((slot * (DH / 4) + lane * kCols / 4) * kRows + row) * 4 +
-                         (lane * kCols) % 4;
-        float x[kCols];
-        if (kCols == 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(v));
-          x[0] = y.x;
-          x[1] = y.y;
-          x[kCols - 2] = y.z;
-          x[kCols - 1] = y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(v));
-          x[0] = y.x;
-          x[kCols - 1] = y.y;
+        for (int i = 0; i < kR; ++i) {
+          l[i] = k0 + lane < n && src[i] >= 0 ? __ldcg(lse + src[i]) : -INFINITY;
+          mx[i] = l[i];
         }
-        const float w = l == -INFINITY ? 0.f : exp2f(l - M) * inv;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] += w * x[c];
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kR; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+          mx[i] = fmaxf(M[i], mx[i]);
+          e[i] = l[i] == -INFINITY ? 0.f : exp2f(l[i] - mx[i]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kR; ++i) e[i] += __shfl_xor_sync(0xffffffffu, e[i], o);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+          sum[i] = (M[i] == -INFINITY ? 0.f : sum[i] * exp2f(M[i] - mx[i])) + e[i];
+          M[i] = mx[i];
+        }
       }
-      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), src));
+      float inv[kR], acc[kR][kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 2) {
-        finite = finite && fabsf(acc[c]) < INFINITY && fabsf(acc[c + 1]) < INFINITY;
-        *reinterpret_cast<__nv_bfloat162*>(dst + lane * kCols + c) =
-            __floats2bfloat162_rn(acc[c], acc[c + 1]);
+      for (int i = 0; i < kR; ++i) {
+        inv[i] = sum[i] > 0.f ? 1.f / sum[i] : sum[i];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[i][c] = 0.f;
+      }
+      for (int k = 0; k < n; k += kK) {
+        float x[kK][kR][kCols], lk[kK][kR];
+#pragma unroll
+        for (int d = 0; d < kK; ++d) {
+          const size_t slot = piece_slot(c0 + min(k + d, n - 1), per, s0);
+          const float* v = p.o_part + (slot * kRows + row0) * DH + lane * kCols;  // whole rows
+          const float* lse = p.lse_part + slot * kRows + row0;
+#pragma unroll
+          for (int i = 0; i < kR; ++i) {
+            const int r = max(src[i], 0);
+            if (kCols == 4) {
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(v + r * DH));
+              x[d][i][0] = y.x;
+              x[d][i][1] = y.y;
+              x[d][i][kCols - 2] = y.z;
+              x[d][i][kCols - 1] = y.w;
+            } else {
+              const float2 y = __ldcg(reinterpret_cast<const float2*>(v + r * DH));
+              x[d][i][0] = y.x;
+              x[d][i][kCols - 1] = y.y;
+            }
+            lk[d][i] = __ldcg(lse + r);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < kK; ++d)
+#pragma unroll
+          for (int i = 0; i < kR; ++i) {
+            const float w = k + d >= n || src[i] < 0 || lk[d][i] == -INFINITY
+                                ? 0.f
+                                : exp2f(lk[d][i] - M[i]) * inv[i];
+            // a weight of zero adds nothing, whatever the partial holds
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) acc[i][c] += w == 0.f ? 0.f : w * x[d][i][c];
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(out), max(src[i], 0)));
+        if (src[i] < 0) continue;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 2) {
+          finite = finite && fabsf(acc[i][c]) < INFINITY && fabsf(acc[i][c + 1]) < INFINITY;
+          *reinterpret_cast<__nv_bfloat162*>(dst + lane * kCols + c) =
+              __floats2bfloat162_rn(acc[i][c], acc[i][c + 1]);
+        }
       }
     }
     return finite;
@@ -371,10 +418,10 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
       const size_t slot = piece_slot(c0 + k, per, s0);
       const float l = __ldcg(p.lse_part + slot * kRows + row);
       const float4* src = reinterpret_cast<const float4*>(p.o_part) +
-                          (slot * (DH / 4) + ch * 8) * kRows + row;
+                          (slot * kRows + row0) * (DH / 4) + ch * 8 * 32 + lane;
       float4 v[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = __ldcg(src + c * kRows);
+      for (int c = 0; c < 8; ++c) v[c] = __ldcg(src + c * 32);
       const float w = l == -INFINITY ? 0.f : exp2f(l - M) * inv;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -398,15 +445,17 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
   const int lane = threadIdx.x & 31;
   bool ok = true;
   long long run = 0;
+  int q0 = 0, qlen = 0, kv = 0;  // of this lane's sequence
   if (lane == 0) cum[0] = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int qlen = 0, kv = 0;
+    qlen = kv = 0;
     if (b < p.B) {
-      const int a0 = p.cu_q[b], a1 = p.cu_q[b + 1];
+      const int a1 = p.cu_q[b + 1];
+      q0 = p.cu_q[b];
       kv = p.kv_len[b];
-      qlen = a1 - a0;
-      ok = ok && a0 >= 0 && a1 >= a0 && a1 <= p.T && kv >= 0 &&
+      qlen = a1 - q0;
+      ok = ok && q0 >= 0 && a1 >= q0 && a1 <= p.T && kv >= 0 &&
            kv <= (long long)p.max_pages * p.page;
     }
     if (!__all_sync(0xffffffffu, ok)) break;
@@ -459,9 +508,17 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
   }
   const int per_head = (cum[lo + 1] - cum[lo]) / p.Hkv;
   int rem = t0 - cum[lo];
-  int s[8] = {lo, rem / per_head, 0, 0, 0, p.cu_q[lo], 0, p.kv_len[lo]};
+  int s[8] = {lo, rem / per_head, 0, 0, 0, 0, 0, 0};
   rem -= s[1] * per_head;
-  s[6] = p.cu_q[lo + 1] - s[5];
+  if (p.B <= 32) {
+    s[5] = __shfl_sync(0xffffffffu, q0, lo);
+    s[6] = __shfl_sync(0xffffffffu, qlen, lo);
+    s[7] = __shfl_sync(0xffffffffu, kv, lo);
+  } else {
+    s[5] = p.cu_q[lo];
+    s[6] = p.cu_q[lo + 1] - s[5];
+    s[7] = p.kv_len[lo];
+  }
   for (int g0 = 0;; g0 += 32) {
     // beyond the last group the costs only have to be positive
     const int n = group_cost(s[6], s[7], g0 + lane, p);
@@ -1052,7 +1109,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_pieces = (s0 + (done.ntiles - 1) * done.wt) / per - c0 + 1;
         const size_t slot = piece_slot(blockIdx.x, per, s0);
         const int row = m * kMT + rl;
-        float4* dst = reinterpret_cast<float4*>(p.o_part) + slot * (DH / 4) * kRows + row;
+        // Many rows in a warp: groups of 4 columns of all rows, so that its
+        // lanes write 512 bytes side by side.  Few: whole rows, which the
+        // merging warp reads 512 bytes at a time.
+        const unsigned int mask = __ballot_sync(0xffffffffu, valid);
+        const bool few = __popc(mask) <= kFewRows;
+        float4* dst = reinterpret_cast<float4*>(p.o_part) +
+                      (slot * kRows + row - lane) * (DH / 4) + (few ? lane * (DH / 4) : lane);
+        const int step = few ? 1 : 32;
 #pragma unroll 1
         for (int ch = 0; ch < DH / 32; ++ch) {
           float o[32];
@@ -1060,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              dst[(ch * 8 + c) * kRows] =
+              dst[(ch * 8 + c) * step] =
                   make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
@@ -1075,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == static_cast<unsigned int>(n_pieces - 1)) {
           __threadfence();
-          finite = merge_rows<DH>(p, out, __ballot_sync(0xffffffffu, valid), c0, n_pieces, per, s0,
+          finite = merge_rows<DH>(p, out, mask, c0, n_pieces, per, s0,
                                   row - lane) && finite;
         }
       }
