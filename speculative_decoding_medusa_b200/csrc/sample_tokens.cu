@@ -45,8 +45,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kGroups = kBins / 32;
-constexpr int kShort = 128;  // tokens a block may put on the short list
+constexpr int kList = 1024;  // tokens on the short list, kList / cluster from each block
 constexpr int kMaxCluster = 8;
+// Top tokens looked for when only top_p bounds a row; a row whose top_k is at
+// most kTopWanted, or whose mass they reach, needs no histogram of its tokens.
+constexpr int kTopWanted = 256;
+constexpr size_t kManyBytes = 65536;  // of a row in a block when there are many rows
 constexpr int kExpTable = 256;
 constexpr uint32_t kLowestKey = 0x00800000u;  // key of the lowest finite float
 
@@ -89,6 +93,16 @@ struct Elem<float> {
     z[3] = __uint_as_float(r.w);
   }
   static constexpr uint32_t kNegInf = 0xff800000u;  // filler word
+  // NaN if any is
+  __device__ static float max2(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+  }
+  __device__ static float max_of(uint4 r) {
+    return max2(max2(__uint_as_float(r.x), __uint_as_float(r.y)),
+                max2(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -102,6 +116,15 @@ struct Elem<__nv_bfloat16> {
     }
   }
   static constexpr uint32_t kNegInf = 0xff80ff80u;
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {  // pairs
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static float max_of(uint4 r) {
+    const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
+    return Elem<float>::max2(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
 };
 
 // The weight exp((z - max) / T) in units of 2^-42: 2^y with y = (z - max) *
@@ -135,11 +158,6 @@ struct Weight {
 };
 
 // what a block tells the others of its cluster
-struct Extremes {
-  float hi, lo;  // largest logit, smallest finite logit
-  int arg;       // lowest id of the largest
-  int bad;       // a NaN or +inf
-};
 struct Sums {
   unsigned long long mass;
   unsigned int count;
@@ -158,12 +176,9 @@ struct Cut {
 };
 
 struct Shared {
-  Extremes ext[kMaxCluster];
-  Sums group[kMaxCluster][kGroups];
+  float hi[kMaxCluster];  // largest logit (NaN: there is one)
   Sums part[kMaxCluster];
-  unsigned long long mine[kShort];  // short list: key and complemented id
-  unsigned long long list[kMaxCluster][kShort];
-  unsigned long long sorted[kMaxCluster * kShort];
+  unsigned long long list_mass[kMaxCluster];  // weights of every token of the block
   unsigned int list_n[kMaxCluster];
   uint32_t kmin[kMaxCluster], kmax[kMaxCluster];
   double table[kExpTable];
@@ -173,8 +188,16 @@ struct Shared {
   int cut_id;
   unsigned long long red64[kWarps];
   unsigned int red32[kWarps], red32b[kWarps];
-  float redf[kWarps], redg[kWarps];
+  float redf[kWarps];
 };
+
+// dynamic shared memory after the slice: histogram (counts, low and high words
+// of the mass; the sorted list lies over the mass words), short lists and
+// group sums of every block
+__host__ __device__ constexpr size_t sample_extra_smem(int C) {
+  return 3 * kBins * 4 + kList * 8 + (size_t)C * kGroups * sizeof(Sums);
+}
+static_assert(kList * 8 <= 2 * kBins * 4, "sorted list over the mass words");
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams p) {
@@ -194,6 +217,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   uint32_t* h_cnt = reinterpret_cast<uint32_t*>(dyn + (size_t)n_vec * 16);
   uint32_t* h_lo = h_cnt + kBins;
   uint32_t* h_hi = h_lo + kBins;
+  unsigned long long* sorted = reinterpret_cast<unsigned long long*>(h_lo);
+  // the short lists: words of key and complemented id, cap from each block
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(h_hi + kBins);
+  Sums* group = reinterpret_cast<Sums*>(list + kList);
+  const int cap = kList / C;
   __shared__ Shared sh;
 
   const float temp = p.temperature != nullptr ? p.temperature[r] : 1.f;
@@ -205,12 +233,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   bool bad = !(u >= 0.f && u < 1.f) || !(temp >= 0.f) || !(top_p >= 0.f) ||
              !(min_p >= 0.f && min_p <= 1.f) || src_row < 0 || src_row >= p.n_rows || isinf(temp);
 
-  // ---- the slice into shared memory; extremes ----
+  // ---- the slice into shared memory; its largest logit ----
   // Blocks split the row at 16-byte boundaries of its address: element i of
   // the split is token i - off.
-  float hi = -INFINITY, lo = INFINITY;
-  int arg = 0x7fffffff;
-  bool nan = false;
+  float hi = -INFINITY;
   int base = 0;
   if (!bad) {
     const T* row = static_cast<const T*>(p.logits) + (size_t)src_row * p.row_stride;
@@ -251,98 +277,106 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         const int v = v0 + f * kThreads;
         if (v >= n_vec) break;
         slice[v] = raw[f];
-        float z[VE];
-        Elem<T>::unpack(raw[f], z);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          if (!(z[i] < INFINITY)) nan = true;
-          if (z[i] > hi) {
-            hi = z[i];
-            arg = base + v * VE + i;
-          }
-          if (z[i] > -INFINITY) lo = fminf(lo, z[i]);
-        }
+        hi = Elem<float>::max2(hi, Elem<T>::max_of(raw[f]));
       }
     }
   }
   if (tid >= n_vec && tid < kExpTable) sh.table[tid] = exp2((double)tid / kExpTable);
-  for (int o = 16; o > 0; o >>= 1) {
-    const float oh = __shfl_xor_sync(0xffffffffu, hi, o);
-    const int oa = __shfl_xor_sync(0xffffffffu, arg, o);
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    if (better(oh, oa, hi, arg)) {
-      hi = oh;
-      arg = oa;
-    }
-  }
-  nan = __any_sync(0xffffffffu, nan);
-  if (lane == 0) {
-    sh.redf[warp] = hi;
-    sh.redg[warp] = lo;
-    sh.red32[warp] = static_cast<unsigned int>(arg);
-    sh.red32b[warp] = nan ? 1u : 0u;
-  }
+  const float own_hi = hi;  // the largest of this thread's tokens
+  for (int o = 16; o > 0; o >>= 1)
+    hi = Elem<float>::max2(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  if (lane == 0) sh.redf[warp] = hi;
   __syncthreads();
   if (tid < C) {
-    Extremes e{-INFINITY, INFINITY, 0x7fffffff, 0};
-    for (int w = 0; w < kWarps; ++w) {
-      const int a = static_cast<int>(sh.red32[w]);
-      if (better(sh.redf[w], a, e.hi, e.arg)) {
-        e.hi = sh.redf[w];
-        e.arg = a;
-      }
-      e.lo = fminf(e.lo, sh.redg[w]);
-      e.bad |= static_cast<int>(sh.red32b[w]);
-    }
-    *cluster.map_shared_rank(&sh.ext[rank], tid) = e;
+    hi = sh.redf[0];
+    for (int w = 1; w < kWarps; ++w) hi = Elem<float>::max2(hi, sh.redf[w]);
+    *cluster.map_shared_rank(&sh.hi[rank], tid) = hi;
   }
   cluster.sync();
-  float zlo = INFINITY;
-  hi = -INFINITY;
-  arg = 0x7fffffff;
-  for (int c = 0; c < C; ++c) {
-    const Extremes e = sh.ext[c];
-    if (better(e.hi, e.arg, hi, arg)) {
-      hi = e.hi;
-      arg = e.arg;
-    }
-    zlo = fminf(zlo, e.lo);
-    if (e.bad) bad = true;
-  }
-  if (!(hi > -INFINITY)) bad = true;
-  if (bad || temp == 0.f || top_k == 1) {
+  hi = sh.hi[0];
+  for (int c = 1; c < C; ++c) hi = Elem<float>::max2(hi, sh.hi[c]);
+  if (!(hi > -INFINITY && hi < INFINITY)) bad = true;  // NaN, +inf, or no finite logit
+  if (bad) {
     if (rank == 0 && tid == 0) {
-      if (bad) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-      p.tokens[r] = bad ? -1 : arg;
-      if (p.kept != nullptr) p.kept[r] = bad ? 0 : 1;
+      report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      p.tokens[r] = -1;
+      if (p.kept != nullptr) p.kept[r] = 0;
     }
     return;  // the whole cluster takes this branch, after its last exchange
+  }
+  if (temp == 0.f || top_k == 1) {
+    // the lowest id of the largest
+    int first = 0x7fffffff;
+    for (int v = tid; v < n_vec; v += kThreads) {
+      const uint4 raw = slice[v];
+      if (Elem<T>::max_of(raw) < hi) continue;
+      float z[VE];
+      Elem<T>::unpack(raw, z);
+#pragma unroll
+      for (int i = VE - 1; i >= 0; --i)
+        if (z[i] == hi) first = min(first, base + v * VE + i);
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.red32[warp] = static_cast<unsigned int>(first);
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kWarps; ++w) first = min(first, static_cast<int>(sh.red32[w]));
+      cluster.map_shared_rank(&sh.part[rank], 0)->first = first;
+    }
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+      for (int c = 0; c < C; ++c) first = min(first, sh.part[c].first);
+      p.tokens[r] = first;
+      if (p.kept != nullptr) p.kept[r] = 1;
+    }
+    return;
   }
 
   const double c_log2 = 1.4426950408889634074 / (double)temp;  // log2(e) / T
   const double zmax = widen(hi);
   const Weight weight{sh.table, zmax, c_log2 * kExpTable};
   // bins of level 0: linear in the logit, over the range that can carry mass
-  // or, if that is smaller, the row's own
-  const float range = fminf(hi - zlo, 32.f * temp);
-  const float bin_scale = range > 0.f ? fminf((float)(kBins - 1) / range, 1e30f) : 0.f;
+  const float bin_scale = fminf((float)(kBins - 1) / (32.f * temp), 1e30f);
   auto bin0 = [&](float z) -> uint32_t {
     return static_cast<uint32_t>(fminf((hi - z) * bin_scale, (float)(kBins - 1)));
   };
   const bool by_k = top_k > 0 && top_k < p.V;
   const bool by_p = top_p < 1.f;
 
-  // One histogram over the cluster: `pick(z, bin)` says whether a finite
-  // logit counts and in which bin.  Afterwards every block holds every
-  // block's sums of each group of 32 bins, and the blocks' own bins stay in
-  // place for find().
-  auto histogram = [&](bool counts, bool masses, auto pick) {
+  auto clear_bins = [&]() {
     for (int i = tid; i < kBins; i += kThreads) {
       h_cnt[i] = 0u;
       h_lo[i] = 0u;
       h_hi[i] = 0u;
     }
     __syncthreads();
+  };
+  // a weight to its bin: two 32-bit words with a carry (64-bit shared-memory
+  // additions measured 1.5 times slower)
+  auto add_mass = [&](uint32_t bin, unsigned long long w) {
+    const uint32_t wl = static_cast<uint32_t>(w);
+    const uint32_t wh =
+        static_cast<uint32_t>(w >> 32) + (atomicAdd(&h_lo[bin], wl) + wl < wl ? 1u : 0u);
+    if (wh != 0u) atomicAdd(&h_hi[bin], wh);
+  };
+  // the sums of every group of 32 bins to every block
+  auto publish = [&]() {
+    __syncthreads();
+    for (int g = warp; g < kGroups; g += kWarps) {
+      const int bin = g * 32 + lane;
+      const unsigned int n = __reduce_add_sync(0xffffffffu, h_cnt[bin]);
+      unsigned long long m = (static_cast<unsigned long long>(h_hi[bin]) << 32) + h_lo[bin];
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane < C) *cluster.map_shared_rank(&group[rank * kGroups + g], lane) = Sums{m, n, 0};
+    }
+    cluster.sync();
+  };
+  // One histogram over the cluster: `pick(z, bin)` says whether a finite
+  // logit counts and in which bin.  Afterwards every block holds every
+  // block's sums of each group of 32 bins, and the blocks' own bins stay in
+  // place for find().
+  auto histogram = [&](bool counts, bool masses, auto pick) {
+    clear_bins();
     for (int v = tid; v < n_vec; v += kThreads) {
       float z[VE];
       Elem<T>::unpack(slice[v], z);
@@ -357,9 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
           unsigned long long w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
-          // two 32-bit words with a carry (64-bit shared-memory additions
-          // measured 1.5 times slower)
-          uint32_t old[4];
+          uint32_t old[4];  // as add_mass, four at a time
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             old[i] = in[i] && w[i] != 0ull ? atomicAdd(&h_lo[bin[i]], static_cast<uint32_t>(w[i])) : 0u;
@@ -377,15 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         }
       }
     }
-    __syncthreads();
-    for (int g = warp; g < kGroups; g += kWarps) {
-      const int bin = g * 32 + lane;
-      const unsigned int n = __reduce_add_sync(0xffffffffu, h_cnt[bin]);
-      unsigned long long m = (static_cast<unsigned long long>(h_hi[bin]) << 32) + h_lo[bin];
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (lane < C) *cluster.map_shared_rank(&sh.group[rank][g], lane) = Sums{m, n, 0};
-    }
-    cluster.sync();
+    publish();
   };
 
   // The last bin with tokens before which the count (or the mass) is below
@@ -405,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
           if (c >= C) break;
-          const Sums t = sh.group[c][2 * lane + x];
+          const Sums t = group[c * kGroups + 2 * lane + x];
           s[x].mass += t.mass;
           s[x].count += t.count;
         }
@@ -493,7 +517,169 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   };
 
   // The exact cut inside bin b of the current histogram.
-  bool crowded = false;  // a crowded bin has used the histogram
+  // Tokens for which in(z) holds onto the short list of every block, and
+  // (masses) the weights of all tokens.  none(m): no token of a vector whose
+  // largest is m.  False when a block has too many; n: their number.
+  auto gather = [&](auto in, auto none, bool masses, unsigned int& n,
+                    unsigned long long& mass) -> bool {
+    unsigned long long* mine = list + rank * cap;
+    if (tid == 0) sh.n_local = 0u;
+    __syncthreads();
+    unsigned long long m = 0ull;
+    for (int v = tid; v < n_vec; v += kThreads) {
+      const uint4 raw = slice[v];
+      const bool skip = none(Elem<T>::max_of(raw));
+      if (skip && !masses) continue;
+      float z[VE];
+      Elem<T>::unpack(raw, z);
+      if (masses) {
+#pragma unroll
+        for (int i0 = 0; i0 < VE; i0 += 4) {
+          unsigned long long w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
+          m += (w[0] + w[1]) + (w[2] + w[3]);
+        }
+      }
+      if (!skip) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (in(z[i])) {
+            const unsigned int at = atomicAdd(&sh.n_local, 1u);
+            if (at < (unsigned int)cap)
+              mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
+                         (0xffffffffu - static_cast<uint32_t>(base + v * VE + i));
+          }
+      }
+    }
+    if (masses) {
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane == 0) sh.red64[warp] = m;
+    }
+    __syncthreads();
+    if (tid < C) {
+      *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local;
+      m = 0ull;
+      if (masses)
+        for (int w = 0; w < kWarps; ++w) m += sh.red64[w];
+      *cluster.map_shared_rank(&sh.list_mass[rank], tid) = m;
+    }
+    const int n_mine = static_cast<int>(min(sh.n_local, (unsigned int)cap));
+    for (int e = tid; e < n_mine * C; e += kThreads) {
+      const int c = e / n_mine, i = e - c * n_mine;
+      if (c != rank) *cluster.map_shared_rank(&mine[i], c) = mine[i];
+    }
+    cluster.sync();
+    bool fits = true;
+    n = 0u;
+    mass = 0ull;
+    for (int c = 0; c < C; ++c) {
+      fits = fits && sh.list_n[c] <= (unsigned int)cap;
+      n += sh.list_n[c];
+      mass += sh.list_mass[c];
+    }
+    return fits;
+  };
+
+  // The lists as one array in the order of the tokens, largest first, and the
+  // mass before the thread's two words 2 tid and 2 tid + 1 in it (given what
+  // lies before the list).  Thread t holds word t (and t + kThreads when there
+  // are more); a bitonic network exchanges them by shuffles, and through
+  // shared memory for distances of a warp or more.
+  bool dirty = false;  // the histogram has been written over
+  auto sort_list = [&](unsigned int n, unsigned long long mass0, bool masses,
+                       unsigned long long (&w)[2]) -> unsigned long long {
+    dirty = true;
+    int size = 32;
+    while (size < (int)n) size <<= 1;
+    {
+      unsigned int at = 0u;
+      for (int c = 0; c < C; ++c) {
+        for (int i = tid; i < (int)sh.list_n[c]; i += kThreads) sorted[at + i] = list[c * cap + i];
+        at += sh.list_n[c];
+      }
+      for (int i = n + tid; i < size; i += kThreads) sorted[i] = 0ull;
+    }
+    __syncthreads();
+    const bool wide = size > kThreads;
+    const bool act = warp * 32 < size;
+    unsigned long long e0 = act ? sorted[tid] : 0ull;
+    unsigned long long e1 = wide ? sorted[tid + kThreads] : 0ull;
+    auto keep = [&](unsigned long long mine, unsigned long long other, int x, int k, int j) {
+      const bool larger = ((x & j) == 0) == ((x & k) == 0);
+      return (mine > other) == larger ? mine : other;
+    };
+    for (int k = 2; k <= size; k <<= 1) {
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        if (j == kThreads) {  // the thread's own two words
+          const unsigned long long a = keep(e0, e1, tid, k, j);
+          e1 = keep(e1, e0, tid + kThreads, k, j);
+          e0 = a;
+        } else if (j >= 32) {
+          __syncthreads();
+          if (act) sorted[tid] = e0;
+          if (wide) sorted[tid + kThreads] = e1;
+          __syncthreads();
+          if (act) e0 = keep(e0, sorted[tid ^ j], tid, k, j);
+          if (wide) e1 = keep(e1, sorted[(tid + kThreads) ^ j], tid + kThreads, k, j);
+        } else if (act) {
+          e0 = keep(e0, __shfl_xor_sync(0xffffffffu, e0, j), tid, k, j);
+          if (wide) e1 = keep(e1, __shfl_xor_sync(0xffffffffu, e1, j), tid + kThreads, k, j);
+        }
+      }
+    }
+    __syncthreads();
+    if (act) sorted[tid] = e0;
+    if (wide) sorted[tid + kThreads] = e1;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      w[x] = masses && 2 * tid + x < (int)n
+                 ? weight(value_of(static_cast<uint32_t>(sorted[2 * tid + x] >> 32)))
+                 : 0ull;
+    unsigned long long m = w[0] + w[1];
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, m, o);
+      if (lane >= o) m += y;
+    }
+    if (lane == 31) sh.red64[warp] = m;
+    __syncthreads();
+    m += mass0 - w[0] - w[1];
+    for (int x = 0; x < warp; ++x) m += sh.red64[x];
+    return m;
+  };
+  // the last of the sorted words for which stay(i, mass before) holds
+  auto last_of = [&](unsigned int n, unsigned long long before,
+                     const unsigned long long (&w)[2], auto stay) -> Cut {
+    int last = -1;
+    unsigned long long mass = 0ull;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = 2 * tid + x;
+      if (i < (int)n && stay(i, before)) {
+        last = i;
+        mass = before + w[x];
+      }
+      before += w[x];
+    }
+    const unsigned int votes = __ballot_sync(0xffffffffu, last >= 0);
+    if (votes != 0u && lane == 31 - __clz(votes)) sh.red32[warp] = last + 1;
+    if (votes == 0u && lane == 0) sh.red32[warp] = 0u;
+    __syncthreads();
+    unsigned int best = 0u;
+    for (int x = 0; x < kWarps; ++x) best = max(best, sh.red32[x]);
+    if (last >= 0 && (unsigned int)last + 1u == best) {
+      const unsigned long long e = sorted[last];
+      sh.cut = Cut{mass, static_cast<uint32_t>(e >> 32),
+                   static_cast<int>(0xffffffffu - static_cast<uint32_t>(e))};
+    }
+    __syncthreads();
+    const Cut cut = sh.cut;
+    __syncthreads();
+    return cut;
+  };
+
+  // The exact cut inside bin b of the current histogram.
   auto resolve = [&](bool by_mass, Bin b, bool again) -> Cut {
     const unsigned long long limit = b.limit;
     bool level0 = true;
@@ -505,125 +691,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         const uint32_t k = key_of(z);
         return k >= plo && k <= phi;
       };
-      // the bin's tokens onto the list of every block
-      if (tid == 0) sh.n_local = 0u;
-      __syncthreads();
-      for (int v = tid; v < n_vec; v += kThreads) {
-        float z[VE];
-        Elem<T>::unpack(slice[v], z);
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (in_bin(z[i])) {
-            const unsigned int at = atomicAdd(&sh.n_local, 1u);
-            if (at < (unsigned int)kShort)
-              sh.mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
-                            (0xffffffffu - static_cast<uint32_t>(base + v * VE + i));
-          }
-      }
-      __syncthreads();
-      if (tid < C) *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local;
-      {
-        const int n = static_cast<int>(min(sh.n_local, (unsigned int)kShort));
-        for (int e = tid; e < n * C; e += kThreads) {
-          const int c = e / n, i = e - c * n;
-          *cluster.map_shared_rank(&sh.list[rank][i], c) = sh.mine[i];
-        }
-      }
-      cluster.sync();
-      bool fits = true;
-      unsigned int n = 0u;
-      for (int c = 0; c < C; ++c) {
-        fits = fits && sh.list_n[c] <= (unsigned int)kShort;
-        n += sh.list_n[c];
-      }
-      if (fits) {
-        // All of the bin, sorted into the order of the tokens: words of key
-        // and complemented id, largest first.  Thread t holds word t (and
-        // t + kThreads when there are more); a bitonic network exchanges them
-        // by shuffles, and through shared memory for distances of a warp or
-        // more.
-        int size = 32;
-        while (size < (int)n) size <<= 1;
-        {
-          unsigned int at = 0u;
-          for (int c = 0; c < C; ++c) {
-            for (int i = tid; i < (int)sh.list_n[c]; i += kThreads) sh.sorted[at + i] = sh.list[c][i];
-            at += sh.list_n[c];
-          }
-          for (int i = n + tid; i < size; i += kThreads) sh.sorted[i] = 0ull;
-        }
-        __syncthreads();
-        const bool wide = size > kThreads;
-        const bool act = warp * 32 < size;
-        unsigned long long e0 = act ? sh.sorted[tid] : 0ull;
-        unsigned long long e1 = wide ? sh.sorted[tid + kThreads] : 0ull;
-        auto keep = [&](unsigned long long mine, unsigned long long other, int x, int k, int j) {
-          const bool larger = ((x & j) == 0) == ((x & k) == 0);
-          return (mine > other) == larger ? mine : other;
-        };
-        for (int k = 2; k <= size; k <<= 1) {
-          for (int j = k >> 1; j > 0; j >>= 1) {
-            if (j == kThreads) {  // the thread's own two words
-              const unsigned long long a = keep(e0, e1, tid, k, j);
-              e1 = keep(e1, e0, tid + kThreads, k, j);
-              e0 = a;
-            } else if (j >= 32) {
-              __syncthreads();
-              if (act) sh.sorted[tid] = e0;
-              if (wide) sh.sorted[tid + kThreads] = e1;
-              __syncthreads();
-              if (act) e0 = keep(e0, sh.sorted[tid ^ j], tid, k, j);
-              if (wide) e1 = keep(e1, sh.sorted[(tid + kThreads) ^ j], tid + kThreads, k, j);
-            } else if (act) {
-              e0 = keep(e0, __shfl_xor_sync(0xffffffffu, e0, j), tid, k, j);
-              if (wide) e1 = keep(e1, __shfl_xor_sync(0xffffffffu, e1, j), tid + kThreads, k, j);
-            }
-          }
-        }
-        __syncthreads();
-        if (act) sh.sorted[tid] = e0;
-        if (wide) sh.sorted[tid + kThreads] = e1;
-        __syncthreads();
-        // mass before each token: two tokens a thread
-        unsigned long long w[2] = {0ull, 0ull};
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (by_p && 2 * tid + x < (int)n)
-            w[x] = weight(value_of(static_cast<uint32_t>(sh.sorted[2 * tid + x] >> 32)));
-        unsigned long long m = w[0] + w[1];
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long y = __shfl_up_sync(0xffffffffu, m, o);
-          if (lane >= o) m += y;
-        }
-        if (lane == 31) sh.red64[warp] = m;
-        __syncthreads();
-        m += b.mass - w[0] - w[1];
-        for (int x = 0; x < warp; ++x) m += sh.red64[x];
-        // the last token that stays: one thread holds it
-        int last = -1;
-        unsigned long long mass = 0ull;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int i = 2 * tid + x;
-          if (i < (int)n && (by_mass ? m : (unsigned long long)b.count + i) < limit) {
-            last = i;
-            mass = m + w[x];
-          }
-          m += w[x];
-        }
-        const unsigned int votes = __ballot_sync(0xffffffffu, last >= 0);
-        if (votes != 0u && lane == 31 - __clz(votes)) sh.red32[warp] = last + 1;
-        if (votes == 0u && lane == 0) sh.red32[warp] = 0u;
-        __syncthreads();
-        unsigned int best = 0u;
-        for (int x = 0; x < kWarps; ++x) best = max(best, sh.red32[x]);
-        if (last >= 0 && (unsigned int)last + 1u == best) {
-          const unsigned long long e = sh.sorted[last];
-          sh.cut = Cut{mass, static_cast<uint32_t>(e >> 32),
-                       static_cast<int>(0xffffffffu - static_cast<uint32_t>(e))};
-        }
-        __syncthreads();
-        const Cut cut = sh.cut;
+      unsigned int n;
+      unsigned long long unused;
+      auto none = [&](float m) {
+        if (level0) return bin0(m) > b.bin;  // (-inf: the last bin, in_bin looks)
+        return key_of(m) < plo;
+      };
+      if (gather(in_bin, none, false, n, unused)) {
+        unsigned long long w[2];
+        const unsigned long long m = sort_list(n, b.mass, by_p, w);
+        const Cut cut = last_of(n, m, w, [&](int i, unsigned long long before) {
+          return (by_mass ? before : (unsigned long long)b.count + i) < limit;
+        });
         if (again) cluster.sync();  // the lists will be written again
         return cut;
       }
@@ -717,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         cluster.sync();
         return Cut{b.mass + m * w, kmin, sh.cut_id};
       }
-      crowded = true;
+      dirty = true;
       int shift = 0;
       while (((kmax - kmin) >> shift) >= (uint32_t)kBins) ++shift;
       histogram(true, by_p, [&](float z, uint32_t& bin) {
@@ -742,30 +821,92 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       bin = bin0(z);
       return true;
     };
-    histogram(by_k, by_p, all);
-    unsigned long long limit = 0ull;  // top_p of the whole row
-    bool k_cut = false;
-    if (by_k) {
+    auto group_count = [&]() {
       unsigned int count = 0u;
-      for (int i = lane; i < C * kGroups; i += 32) count += sh.group[i / kGroups][i % kGroups].count;
-      k_cut = (unsigned int)top_k < __reduce_add_sync(0xffffffffu, count);
-    }
-    if (k_cut) {
-      const Bin b = find(false, (unsigned long long)top_k, 0u, 0ull);
-      const Cut cut = resolve(false, b, by_p);
-      cut_key = cut.key;
-      cut_id = cut.id;
-      if (by_p) {
-        limit = p_limit(cut.mass);
-        if (crowded) histogram(true, true, all);
+      for (int i = lane; i < C * kGroups; i += 32) count += group[i].count;
+      return __reduce_add_sync(0xffffffffu, count);
+    };
+    auto group_mass = [&]() {
+      unsigned long long mass = 0ull;
+      for (int i = lane; i < C * kGroups; i += 32) mass += group[i].mass;
+      for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      return mass;
+    };
+    // The top tokens first: when k of the threads' largest lie at or above a
+    // bin's edge, so do the k largest of the row, and not many more.
+    bool found = false;
+    if (!by_k || top_k <= kTopWanted) {
+      clear_bins();
+      if (own_hi > -INFINITY) {
+        const uint32_t bin = bin0(own_hi);
+        atomicAdd(&h_cnt[bin], 1u);
+        if (!by_k) add_mass(bin, weight(own_hi));
       }
+      publish();
+      const unsigned int want = by_k ? static_cast<unsigned int>(top_k) : kTopWanted;
+      Bin b = find(false, want, 0u, 0ull);
+      if (group_count() < want) b.bin = kBins - 1;  // too few threads hold a token: all of them
+      // Without top_k the list serves only if it reaches top_p of the mass:
+      // not tried when the threads' largest above the edge are short of top_p
+      // of all the threads' largest, which are a part of the whole mass.
+      bool fits = false;
+      unsigned int n = 0u;
+      unsigned long long total = 0ull;
+      if (by_k || (double)b.mass >= (double)top_p * (double)group_mass())
+        fits = gather([&](float z) { return z > -INFINITY && bin0(z) <= b.bin; },
+                      [&](float m) { return bin0(m) > b.bin; }, !by_k, n, total);
+      if (fits) {
+        unsigned long long w[2];
+        const unsigned long long m = sort_list(n, 0ull, by_p, w);
+        Cut cut;
+        if (by_k) {
+          const int k = min(top_k, (int)n);  // fewer: the row has no more
+          cut = last_of(n, m, w, [&](int i, unsigned long long) { return i < k; });
+          if (by_p) {
+            const unsigned long long limit = p_limit(cut.mass);
+            cut = last_of(n, m, w, [&](int i, unsigned long long before) {
+              return i < k && before < limit;
+            });
+          }
+          found = true;
+        } else {
+          const unsigned long long limit = p_limit(total);
+          cut = last_of(n, m, w,
+                        [&](int, unsigned long long before) { return before < limit; });
+          found = cut.mass >= limit;  // otherwise the list ends before the cut
+        }
+        if (found) {
+          cut_key = cut.key;
+          cut_id = cut.id;
+        }
+      }
+      if (!found) cluster.sync();  // the lists and bins will be written again
     }
-    if (by_p) {
-      const Bin b = find(true, limit, 0u, 0ull);
-      const Cut cut = resolve(true, b, false);
-      if (cut.key > cut_key || (cut.key == cut_key && cut.id < cut_id)) {
+    if (!found) {
+      histogram(by_k, by_p, all);
+      dirty = false;
+      unsigned long long limit = 0ull;  // top_p of the whole row
+      bool k_cut = false;
+      if (by_k) {
+        k_cut = (unsigned int)top_k < group_count();
+      }
+      if (k_cut) {
+        const Bin b = find(false, (unsigned long long)top_k, 0u, 0ull);
+        const Cut cut = resolve(false, b, by_p);
         cut_key = cut.key;
         cut_id = cut.id;
+        if (by_p) {
+          limit = p_limit(cut.mass);
+          if (dirty) histogram(true, true, all);
+        }
+      }
+      if (by_p) {
+        const Bin b = find(true, limit, 0u, 0ull);
+        const Cut cut = resolve(true, b, false);
+        if (cut.key > cut_key || (cut.key == cut_key && cut.id < cut_id)) {
+          cut_key = cut.key;
+          cut_id = cut.id;
+        }
       }
     }
   }
@@ -782,16 +923,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // warp w takes the vectors [w * seg, (w + 1) * seg) of the slice, 32 at a time
   const int seg = (n_vec + kWarps * 32 - 1) / (kWarps * 32) * 32;
   const int v_begin = warp * seg, v_end = min(n_vec, v_begin + seg);
-  auto stays = [&](float z, int id) {
-    const uint32_t k = key_of(z);
-    return k > cut_key || (k == cut_key && id <= cut_id);
-  };
+  const float cut_z = value_of(cut_key);
+  auto stays = [&](float z, int id) { return z > cut_z || (z == cut_z && id <= cut_id); };
   unsigned long long mass = 0ull;
   unsigned int count = 0u;
   int first = 0x7fffffff;
   for (int v = v_begin + lane; v < v_end; v += 32) {
+    const uint4 raw = slice[v];
+    if (Elem<T>::max_of(raw) < cut_z) continue;
     float z[VE];
-    Elem<T>::unpack(slice[v], z);
+    Elem<T>::unpack(raw, z);
 #pragma unroll
     for (int i0 = 0; i0 < VE; i0 += 4) {
       bool in[4];
@@ -886,13 +1027,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 template <typename T>
 medusa_status_t launch_sample(SampleParams& p, cudaStream_t stream) {
   constexpr int VE = Elem<T>::kVec;
-  // a cluster holds the row in shared memory; more blocks than that needs
-  // only while a block still has 4096 tokens
+  // A cluster holds the row in shared memory.  Few rows: more blocks for each
+  // while a block still has 4096 tokens.  Many: as few as leave two blocks to
+  // an SM (a step's barriers cost a block the same whatever its share).
+  const bool few = p.R * kMaxCluster <= 2 * device_sm_count();
   int C = 1;
-  while (C < kMaxCluster && p.V > 4096 * C) C *= 2;
+  while (C < kMaxCluster && (few ? p.V > 4096 * C : (size_t)p.V * sizeof(T) > kManyBytes * C)) C *= 2;
   const int span = p.V + VE - 1;  // the row and its offset in a 16-byte word
   p.slice = ((span + C - 1) / C + 32 * VE - 1) / (32 * VE) * (32 * VE);
-  const size_t smem = (size_t)p.slice * sizeof(T) + 3 * kBins * sizeof(uint32_t);
+  const size_t smem = (size_t)p.slice * sizeof(T) + sample_extra_smem(C);
   if (cudaFuncSetAttribute(sample_tokens_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return fail(MEDUSA_ERR_CUDA, "cudaFuncSetAttribute(sample_tokens) failed");
