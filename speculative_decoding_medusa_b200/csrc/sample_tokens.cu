@@ -50,6 +50,7 @@ constexpr int kMaxCluster = 8;
 // Top tokens looked for when only top_p bounds a row; a row whose top_k is at
 // most kTopWanted, or whose mass they reach, needs no histogram of its tokens.
 constexpr int kTopWanted = 256;
+constexpr int kRankBelow = 256;  // lists up to here are ranked by counting, not sorted
 constexpr size_t kManyBytes = 65536;  // of a row in a block when there are many rows
 constexpr int kExpTable = 256;
 constexpr uint32_t kLowestKey = 0x00800000u;  // key of the lowest finite float
@@ -176,7 +177,8 @@ struct Cut {
 };
 
 struct Shared {
-  float hi[kMaxCluster];  // largest logit (NaN: there is one)
+  float hi[kMaxCluster];    // largest logit (NaN: there is one)
+  float edge[kMaxCluster];  // a bound below the block's share of the top tokens
   Sums part[kMaxCluster];
   unsigned long long list_mass[kMaxCluster];  // weights of every token of the block
   unsigned int list_n[kMaxCluster];
@@ -186,7 +188,7 @@ struct Shared {
   Cut cut;
   unsigned int n_local;
   int cut_id;
-  unsigned long long red64[kWarps];
+  unsigned long long red64[kWarps], red64b[kWarps];
   unsigned int red32[kWarps], red32b[kWarps];
   float redf[kWarps];
 };
@@ -287,14 +289,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     hi = Elem<float>::max2(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   if (lane == 0) sh.redf[warp] = hi;
   __syncthreads();
+  // The share-th largest of the block's threads' largest, to its top 16 bits
+  // (found bit by bit): with every block's, at least `want` tokens of the row
+  // lie at or above the least of them, and not many more.
+  const bool by_k = top_k > 1 && top_k < p.V;
+  const bool by_p = top_p < 1.f;
+  const bool top_list = by_k ? top_k <= kTopWanted : by_p;
+  float edge = -INFINITY;
+  if (top_list) {
+    const int want = by_k ? top_k : kTopWanted / 2;
+    const int share = (want + C - 1) / C;
+    const uint32_t own = own_hi > -INFINITY ? key_of(own_hi) : 0u;
+    uint32_t k = 0u;
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
+      if (__syncthreads_count(own >= (k | bit)) >= share) k |= bit;
+    if (k > 0u) edge = value_of(k);
+  }
   if (tid < C) {
     hi = sh.redf[0];
     for (int w = 1; w < kWarps; ++w) hi = Elem<float>::max2(hi, sh.redf[w]);
     *cluster.map_shared_rank(&sh.hi[rank], tid) = hi;
+    *cluster.map_shared_rank(&sh.edge[rank], tid) = edge;
   }
   cluster.sync();
   hi = sh.hi[0];
-  for (int c = 1; c < C; ++c) hi = Elem<float>::max2(hi, sh.hi[c]);
+  edge = sh.edge[0];
+  for (int c = 1; c < C; ++c) {
+    hi = Elem<float>::max2(hi, sh.hi[c]);
+    edge = fminf(edge, sh.edge[c]);
+  }
   if (!(hi > -INFINITY && hi < INFINITY)) bad = true;  // NaN, +inf, or no finite logit
   if (bad) {
     if (rank == 0 && tid == 0) {
@@ -337,12 +361,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   const Weight weight{sh.table, zmax, c_log2 * kExpTable};
   // bins of level 0: linear in the logit, over the range that can carry mass
   const float bin_scale = fminf((float)(kBins - 1) / (32.f * temp), 1e30f);
+  // (rounded to an integer by the addition of 2^23)
   auto bin0 = [&](float z) -> uint32_t {
-    return static_cast<uint32_t>(fminf((hi - z) * bin_scale, (float)(kBins - 1)));
+    return __float_as_uint(fminf((hi - z) * bin_scale, (float)(kBins - 1)) + 8388608.f) -
+           0x4b000000u;
   };
-  const bool by_k = top_k > 0 && top_k < p.V;
-  const bool by_p = top_p < 1.f;
-
+  // the largest float of a bin beyond b: tokens above it are in bins 0 .. b
+  auto below_bin = [&](uint32_t b) -> float {
+    uint32_t k = kLowestKey - 1;  // key of -inf
+    for (uint32_t bit = 0x80000000u; bit != 0u; bit >>= 1) {
+      const uint32_t t = k + bit;
+      if (t > k && t <= key_of(hi) && bin0(value_of(t)) > b) k = t;
+    }
+    return value_of(k);
+  };
   auto clear_bins = [&]() {
     for (int i = tid; i < kBins; i += kThreads) {
       h_cnt[i] = 0u;
@@ -351,13 +383,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     }
     __syncthreads();
   };
-  // a weight to its bin: two 32-bit words with a carry (64-bit shared-memory
+  // weights to their bins: two 32-bit words with a carry (64-bit shared-memory
   // additions measured 1.5 times slower)
-  auto add_mass = [&](uint32_t bin, unsigned long long w) {
-    const uint32_t wl = static_cast<uint32_t>(w);
-    const uint32_t wh =
-        static_cast<uint32_t>(w >> 32) + (atomicAdd(&h_lo[bin], wl) + wl < wl ? 1u : 0u);
-    if (wh != 0u) atomicAdd(&h_hi[bin], wh);
+  auto add_mass4 = [&](const uint32_t (&bin)[4], const unsigned long long (&w)[4]) {
+    uint32_t old[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      old[i] = w[i] != 0ull ? atomicAdd(&h_lo[bin[i]], static_cast<uint32_t>(w[i])) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t wl = static_cast<uint32_t>(w[i]);
+      const uint32_t wh = static_cast<uint32_t>(w[i] >> 32) + (old[i] + wl < wl ? 1u : 0u);
+      if (wh != 0u) atomicAdd(&h_hi[bin[i]], wh);
+    }
   };
   // the sums of every group of 32 bins to every block
   auto publish = [&]() {
@@ -390,17 +428,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         if (masses) {
           unsigned long long w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
-          uint32_t old[4];  // as add_mass, four at a time
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            old[i] = in[i] && w[i] != 0ull ? atomicAdd(&h_lo[bin[i]], static_cast<uint32_t>(w[i])) : 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t wh = static_cast<uint32_t>(w[i] >> 32) +
-                                (old[i] + static_cast<uint32_t>(w[i]) < old[i] ? 1u : 0u);
-            if (in[i] && wh != 0u) atomicAdd(&h_hi[bin[i]], wh);
-          }
+          for (int i = 0; i < 4; ++i) w[i] = in[i] ? weight(z[i0 + i]) : 0ull;
+          add_mass4(bin, w);
         }
         if (counts) {
 #pragma unroll
@@ -517,18 +546,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   };
 
   // The exact cut inside bin b of the current histogram.
-  // Tokens for which in(z) holds onto the short list of every block, and
-  // (masses) the weights of all tokens.  none(m): no token of a vector whose
-  // largest is m.  False when a block has too many; n: their number.
-  auto gather = [&](auto in, auto none, bool masses, unsigned int& n,
+  // The tokens with below < z <= top onto the short list of every block; with
+  // `masses` also the weights of all tokens, with `bins` these into their
+  // bins.  False when a block has too many; n: their number.
+  auto gather = [&](float below, float top, bool masses, bool bins, unsigned int& n,
                     unsigned long long& mass) -> bool {
     unsigned long long* mine = list + rank * cap;
     if (tid == 0) sh.n_local = 0u;
+    if (bins) clear_bins();
     __syncthreads();
     unsigned long long m = 0ull;
     for (int v = tid; v < n_vec; v += kThreads) {
       const uint4 raw = slice[v];
-      const bool skip = none(Elem<T>::max_of(raw));
+      const bool skip = !(Elem<T>::max_of(raw) > below);
       if (skip && !masses) continue;
       float z[VE];
       Elem<T>::unpack(raw, z);
@@ -539,12 +569,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
           m += (w[0] + w[1]) + (w[2] + w[3]);
+          if (bins) {
+            const uint32_t bin[4] = {bin0(z[i0]), bin0(z[i0 + 1]), bin0(z[i0 + 2]),
+                                     bin0(z[i0 + 3])};
+            add_mass4(bin, w);
+          }
         }
       }
       if (!skip) {
 #pragma unroll
         for (int i = 0; i < VE; ++i)
-          if (in(z[i])) {
+          if (z[i] > below && z[i] <= top) {
             const unsigned int at = atomicAdd(&sh.n_local, 1u);
             if (at < (unsigned int)cap)
               mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
@@ -583,55 +618,81 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 
   // The lists as one array in the order of the tokens, largest first, and the
   // mass before the thread's two words 2 tid and 2 tid + 1 in it (given what
-  // lies before the list).  Thread t holds word t (and t + kThreads when there
-  // are more); a bitonic network exchanges them by shuffles, and through
-  // shared memory for distances of a warp or more.
+  // lies before the list).  A long list goes through a bitonic network: thread
+  // t holds word t (and t + kThreads when there are more), exchanged by
+  // shuffles, and through shared memory for distances of a warp or more.
   bool dirty = false;  // the histogram has been written over
   auto sort_list = [&](unsigned int n, unsigned long long mass0, bool masses,
                        unsigned long long (&w)[2]) -> unsigned long long {
     dirty = true;
-    int size = 32;
-    while (size < (int)n) size <<= 1;
-    {
-      unsigned int at = 0u;
-      for (int c = 0; c < C; ++c) {
-        for (int i = tid; i < (int)sh.list_n[c]; i += kThreads) sorted[at + i] = list[c * cap + i];
-        at += sh.list_n[c];
+    unsigned long long e[2];  // the thread's words of the lists, wherever they lie
+    int at[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int c = (tid + x * kThreads) / cap, i = (tid + x * kThreads) - c * cap;
+      at[x] = -1;
+      e[x] = 0ull;
+      if (c < C && i < (int)sh.list_n[c]) {
+        at[x] = i;
+        for (int o = 0; o < c; ++o) at[x] += sh.list_n[o];
+        e[x] = list[tid + x * kThreads];
+        sorted[at[x]] = e[x];
       }
-      for (int i = n + tid; i < size; i += kThreads) sorted[i] = 0ull;
     }
-    __syncthreads();
-    const bool wide = size > kThreads;
-    const bool act = warp * 32 < size;
-    unsigned long long e0 = act ? sorted[tid] : 0ull;
-    unsigned long long e1 = wide ? sorted[tid + kThreads] : 0ull;
-    auto keep = [&](unsigned long long mine, unsigned long long other, int x, int k, int j) {
-      const bool larger = ((x & j) == 0) == ((x & k) == 0);
-      return (mine > other) == larger ? mine : other;
-    };
-    for (int k = 2; k <= size; k <<= 1) {
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        if (j == kThreads) {  // the thread's own two words
-          const unsigned long long a = keep(e0, e1, tid, k, j);
-          e1 = keep(e1, e0, tid + kThreads, k, j);
-          e0 = a;
-        } else if (j >= 32) {
-          __syncthreads();
-          if (act) sorted[tid] = e0;
-          if (wide) sorted[tid + kThreads] = e1;
-          __syncthreads();
-          if (act) e0 = keep(e0, sorted[tid ^ j], tid, k, j);
-          if (wide) e1 = keep(e1, sorted[(tid + kThreads) ^ j], tid + kThreads, k, j);
-        } else if (act) {
-          e0 = keep(e0, __shfl_xor_sync(0xffffffffu, e0, j), tid, k, j);
-          if (wide) e1 = keep(e1, __shfl_xor_sync(0xffffffffu, e1, j), tid + kThreads, k, j);
+    if (n <= kRankBelow) {
+      // short: every word's rank by counting the larger ones
+      __syncthreads();
+      int rk[2] = {0, 0};
+      if (__any_sync(0xffffffffu, at[0] >= 0 || at[1] >= 0)) {
+#pragma unroll 4
+        for (int i = 0; i < (int)n; ++i) {
+          const unsigned long long o = sorted[i];
+          rk[0] += o > e[0] ? 1 : 0;
+          rk[1] += o > e[1] ? 1 : 0;
         }
       }
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (at[x] >= 0) sorted[rk[x]] = e[x];
+      __syncthreads();
+    } else {
+      int size = 32;
+      while (size < (int)n) size <<= 1;
+      for (int i = n + tid; i < size; i += kThreads) sorted[i] = 0ull;
+      __syncthreads();
+      const bool wide = size > kThreads;
+      const bool act = warp * 32 < size;
+      unsigned long long e0 = act ? sorted[tid] : 0ull;
+      unsigned long long e1 = wide ? sorted[tid + kThreads] : 0ull;
+      auto keep = [&](unsigned long long mine, unsigned long long other, int x, int k, int j) {
+        const bool larger = ((x & j) == 0) == ((x & k) == 0);
+        return (mine > other) == larger ? mine : other;
+      };
+      for (int k = 2; k <= size; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+          if (j == kThreads) {  // the thread's own two words
+            const unsigned long long a = keep(e0, e1, tid, k, j);
+            e1 = keep(e1, e0, tid + kThreads, k, j);
+            e0 = a;
+          } else if (j >= 32) {
+            __syncthreads();
+            if (act) sorted[tid] = e0;
+            if (wide) sorted[tid + kThreads] = e1;
+            __syncthreads();
+            if (act) e0 = keep(e0, sorted[tid ^ j], tid, k, j);
+            if (wide) e1 = keep(e1, sorted[(tid + kThreads) ^ j], tid + kThreads, k, j);
+          } else if (act) {
+            e0 = keep(e0, __shfl_xor_sync(0xffffffffu, e0, j), tid, k, j);
+            if (wide) e1 = keep(e1, __shfl_xor_sync(0xffffffffu, e1, j), tid + kThreads, k, j);
+          }
+        }
+      }
+      __syncthreads();
+      if (act) sorted[tid] = e0;
+      if (wide) sorted[tid + kThreads] = e1;
+      __syncthreads();
     }
-    __syncthreads();
-    if (act) sorted[tid] = e0;
-    if (wide) sorted[tid + kThreads] = e1;
-    __syncthreads();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
       w[x] = masses && 2 * tid + x < (int)n
@@ -682,22 +743,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // The exact cut inside bin b of the current histogram.
   auto resolve = [&](bool by_mass, Bin b, bool again) -> Cut {
     const unsigned long long limit = b.limit;
-    bool level0 = true;
-    uint32_t plo = 0u, phi = 0xffffffffu;  // key interval of the bin (levels >= 1)
+    // the bin's tokens: below < z <= top
+    float below = below_bin(b.bin), top = b.bin > 0u ? below_bin(b.bin - 1u) : hi;
     for (;;) {
-      auto in_bin = [&](float z) {
-        if (!(z > -INFINITY)) return false;
-        if (level0) return bin0(z) == b.bin;
-        const uint32_t k = key_of(z);
-        return k >= plo && k <= phi;
-      };
+      auto in_bin = [&](float z) { return z > below && z <= top; };
       unsigned int n;
       unsigned long long unused;
-      auto none = [&](float m) {
-        if (level0) return bin0(m) > b.bin;  // (-inf: the last bin, in_bin looks)
-        return key_of(m) < plo;
-      };
-      if (gather(in_bin, none, false, n, unused)) {
+      if (gather(below, top, false, false, n, unused)) {
         unsigned long long w[2];
         const unsigned long long m = sort_list(n, b.mass, by_p, w);
         const Cut cut = last_of(n, m, w, [&](int i, unsigned long long before) {
@@ -806,10 +858,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         return true;
       });
       b = find(by_mass, limit, b.count, b.mass);  // the same limit
-      level0 = false;
-      phi = kmax - (b.bin << shift);
-      const uint32_t width = (1u << shift) - 1u;
-      plo = phi - kmin > width ? phi - width : kmin;
+      const uint32_t last = kmax - (b.bin << shift), width = (1u << shift) - 1u;
+      top = value_of(last);
+      below = value_of((last - kmin > width ? last - width : kmin) - 1u);
     }
   };
 
@@ -821,69 +872,85 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       bin = bin0(z);
       return true;
     };
+    // whether the listed tokens' mass is at least `limit` (before they are sorted)
+    auto list_reaches = [&](unsigned long long limit) {
+      unsigned long long m = 0ull;
+      for (int e = tid; e < C * cap; e += kThreads) {
+        const int c = e / cap;
+        if (e - c * cap < (int)sh.list_n[c])
+          m += weight(value_of(static_cast<uint32_t>(list[e] >> 32)));
+      }
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane == 0) sh.red64[warp] = m;
+      __syncthreads();
+      m = 0ull;
+      for (int w = 0; w < kWarps; ++w) m += sh.red64[w];
+      __syncthreads();
+      return m >= limit;
+    };
     auto group_count = [&]() {
       unsigned int count = 0u;
       for (int i = lane; i < C * kGroups; i += 32) count += group[i].count;
       return __reduce_add_sync(0xffffffffu, count);
     };
-    auto group_mass = [&]() {
-      unsigned long long mass = 0ull;
-      for (int i = lane; i < C * kGroups; i += 32) mass += group[i].mass;
-      for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-      return mass;
-    };
-    // The top tokens first: when k of the threads' largest lie at or above a
-    // bin's edge, so do the k largest of the row, and not many more.
-    bool found = false;
-    if (!by_k || top_k <= kTopWanted) {
-      clear_bins();
-      if (own_hi > -INFINITY) {
-        const uint32_t bin = bin0(own_hi);
-        atomicAdd(&h_cnt[bin], 1u);
-        if (!by_k) add_mass(bin, weight(own_hi));
+    // The top tokens first (from `edge` on): they hold the cut of a top_k, and
+    // that of a top_p when they reach it.
+    bool found = false, binned = false;
+    if (top_list) {
+      const float below = edge > -INFINITY ? value_of(key_of(edge) - 1u) : edge;
+      if (!by_k) {
+        // Whether they will is guessed from the block's threads' largest: when
+        // those above the edge are short of top_p of all, the weights go into
+        // their bins in the same pass.
+        const unsigned long long w = own_hi > -INFINITY ? weight(own_hi) : 0ull;
+        unsigned long long some = own_hi >= edge ? w : 0ull, whole = w;
+        for (int o = 16; o > 0; o >>= 1) {
+          some += __shfl_xor_sync(0xffffffffu, some, o);
+          whole += __shfl_xor_sync(0xffffffffu, whole, o);
+        }
+        if (lane == 0) {
+          sh.red64[warp] = some;
+          sh.red64b[warp] = whole;
+        }
+        __syncthreads();
+        some = whole = 0ull;
+        for (int x = 0; x < kWarps; ++x) {
+          some += sh.red64[x];
+          whole += sh.red64b[x];
+        }
+        binned = (double)some < (double)top_p * (double)whole;
+        __syncthreads();
       }
-      publish();
-      const unsigned int want = by_k ? static_cast<unsigned int>(top_k) : kTopWanted;
-      Bin b = find(false, want, 0u, 0ull);
-      if (group_count() < want) b.bin = kBins - 1;  // too few threads hold a token: all of them
-      // Without top_k the list serves only if it reaches top_p of the mass:
-      // not tried when the threads' largest above the edge are short of top_p
-      // of all the threads' largest, which are a part of the whole mass.
-      bool fits = false;
-      unsigned int n = 0u;
-      unsigned long long total = 0ull;
-      if (by_k || (double)b.mass >= (double)top_p * (double)group_mass())
-        fits = gather([&](float z) { return z > -INFINITY && bin0(z) <= b.bin; },
-                      [&](float m) { return bin0(m) > b.bin; }, !by_k, n, total);
-      if (fits) {
+      unsigned int n;
+      unsigned long long total;
+      if (gather(below, hi, !by_k, binned, n, total)) {
         unsigned long long w[2];
-        const unsigned long long m = sort_list(n, 0ull, by_p, w);
-        Cut cut;
-        if (by_k) {
-          const int k = min(top_k, (int)n);  // fewer: the row has no more
-          cut = last_of(n, m, w, [&](int i, unsigned long long) { return i < k; });
-          if (by_p) {
-            const unsigned long long limit = p_limit(cut.mass);
-            cut = last_of(n, m, w, [&](int i, unsigned long long before) {
-              return i < k && before < limit;
-            });
+        const unsigned long long limit = by_k ? 0ull : p_limit(total);
+        if (by_k || list_reaches(limit)) {
+          const unsigned long long m = sort_list(n, 0ull, by_p, w);
+          Cut cut;
+          if (by_k) {
+            const int k = min(top_k, (int)n);  // fewer: the row has no more
+            cut = last_of(n, m, w, [&](int i, unsigned long long) { return i < k; });
+            if (by_p) {
+              const unsigned long long k_limit = p_limit(cut.mass);
+              cut = last_of(n, m, w, [&](int i, unsigned long long before) {
+                return i < k && before < k_limit;
+              });
+            }
+          } else {
+            cut = last_of(n, m, w, [&](int, unsigned long long before) { return before < limit; });
           }
           found = true;
-        } else {
-          const unsigned long long limit = p_limit(total);
-          cut = last_of(n, m, w,
-                        [&](int, unsigned long long before) { return before < limit; });
-          found = cut.mass >= limit;  // otherwise the list ends before the cut
-        }
-        if (found) {
           cut_key = cut.key;
           cut_id = cut.id;
         }
       }
-      if (!found) cluster.sync();  // the lists and bins will be written again
+      if (!found) cluster.sync();  // the lists will be written again
     }
     if (!found) {
-      histogram(by_k, by_p, all);
+      if (binned) publish();
+      else histogram(by_k, by_p, all);
       dirty = false;
       unsigned long long limit = 0ull;  // top_p of the whole row
       bool k_cut = false;
