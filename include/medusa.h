@@ -778,8 +778,8 @@ MEDUSA_API medusa_status_t medusa_chunk_attention(const void* q, long long q_str
  * Limits: 1 <= V <= 327680 (fp32) or 655360 (bf16); R >= 0, R, n_rows <= 65535;
  *   row_stride >= V.
  * Device checks: a NaN or +inf logit, a row without a finite logit, u outside
- *   [0, 1), a NaN or negative parameter, min_p above 1, row_idx outside
- *   [0, n_rows); that row's token is -1 and kept 0.
+ *   [0, 1), a NaN or negative parameter, temperature above 1e30, min_p above
+ *   1, row_idx outside [0, n_rows); that row's token is -1 and kept 0.
  * ---------------------------------------------------------------------- */
 MEDUSA_API medusa_status_t medusa_sample_tokens(const void* logits, medusa_dtype_t dt,
                                                 long long row_stride, int n_rows,

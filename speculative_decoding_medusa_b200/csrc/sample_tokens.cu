@@ -53,6 +53,7 @@ constexpr int kTopWanted = 256;
 constexpr int kRankBelow = 256;  // lists up to here are ranked by counting, not sorted
 constexpr size_t kManyBytes = 65536;  // of a row in a block when there are many rows
 constexpr int kExpTable = 256;
+constexpr float kMaxTemperature = 1e30f;  // 32 T must stay finite
 constexpr uint32_t kLowestKey = 0x00800000u;  // key of the lowest finite float
 
 struct SampleParams {
@@ -77,9 +78,8 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // A finite float as a double by its bits; zero and subnormals become values
 // of that size (below 2^-126), which no logit difference notices.
 __device__ __forceinline__ double widen(float z) {
-  const uint32_t b = __float_as_uint(z);
-  const uint32_t hi = ((b >> 3) & 0x0fffffffu) + 0x38000000u;
-  return __hiloint2double(static_cast<int>(hi | (b & 0x80000000u)), static_cast<int>(b << 29));
+  const int b = __float_as_int(z);
+  return __hiloint2double(((b >> 3) & static_cast<int>(0x8fffffffu)) + 0x38000000, b << 29);
 }
 
 template <typename T>
@@ -131,30 +131,32 @@ struct Elem<__nv_bfloat16> {
 // The weight exp((z - max) / T) in units of 2^-42: 2^y with y = (z - max) *
 // log2(e) / T split as y = n + j / 256 + r / 256, |r| <= 1/2: a table of
 // 2^(j / 256) and the Taylor polynomial of 2^(r / 256) to the third power
-// (the fourth term is below 2^-42).  Ten fp64 operations and a table read;
-// the rounding to an integer is the addition of 1.5 * 2^10, whose last bit
-// is 2^-42.
+// (the fourth term is below 2^-42).  Nine fp64 operations, a table read and
+// ten integer ones; the rounding to an integer is the addition of 1.5 * 2^10,
+// whose last bit is 2^-42.  Logits are held to `floor` (y = -46) first, where
+// the weight rounds to nothing.
 struct Weight {
   const double* table;
   double zmax, c;  // c: 256 * log2(e) / T
+  float floor;
 
   __device__ __forceinline__ unsigned long long operator()(float z) const {
     constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52
-    constexpr double kRound = 1536.0;              // 1.5 * 2^10
+    constexpr double kRound = 1536.0;              // 1.5 * 2^10: its low word is zero
     constexpr double kL = 2.7076061740622863e-3;   // ln 2 / 256
-    const double dz = widen(z) - zmax;
+    const double dz = widen(fmaxf(z, floor)) - zmax;
     const double kd = fma(dz, c, kMagic);
     const int k = __double2loint(kd);
-    const double kf = kd - kMagic;
-    const double r = fma(dz, c, -kf);
+    const double r = fma(dz, c, -(kd - kMagic));
     const double t = table[k & (kExpTable - 1)];
     const double q = fma(fma(kL * kL * kL / 6.0, r, kL * kL / 2.0), r, kL);
     double v = fma(t * r, q, t);
-    v = __hiloint2double(__double2hiint(v) + (k >> 8) * (1 << 20), __double2loint(v));
-    const unsigned long long w = static_cast<unsigned long long>(
-        __double_as_longlong(v + kRound) - __double_as_longlong(kRound));
-    // below 2^-44 of the largest: nothing
-    return kf < -44.0 * kExpTable ? 0ull : w;
+    v = __hiloint2double(__double2hiint(v) + (k & -kExpTable) * (1 << 12), __double2loint(v)) +
+        kRound;
+    return (static_cast<unsigned long long>(
+                static_cast<uint32_t>(__double2hiint(v) - __double2hiint(kRound)))
+            << 32) |
+           static_cast<uint32_t>(__double2loint(v));
   }
 };
 
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   const float min_p = p.min_p != nullptr ? p.min_p[r] : 0.f;
   const int src_row = p.row_idx != nullptr ? p.row_idx[r] : r;
   bool bad = !(u >= 0.f && u < 1.f) || !(temp >= 0.f) || !(top_p >= 0.f) ||
-             !(min_p >= 0.f && min_p <= 1.f) || src_row < 0 || src_row >= p.n_rows || isinf(temp);
+             !(min_p >= 0.f && min_p <= 1.f) || src_row < 0 || src_row >= p.n_rows || temp > kMaxTemperature;
 
   // ---- the slice into shared memory; its largest logit ----
   // Blocks split the row at 16-byte boundaries of its address: element i of
@@ -356,11 +358,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return;
   }
 
-  const double c_log2 = 1.4426950408889634074 / (double)temp;  // log2(e) / T
+  // Exponents are bounded on both sides: logits are held to y = -46, and a T
+  // far below the distance to the next float under the largest counts as a
+  // 64th of it (every other weight is zero either way).  With the lowest
+  // float for the largest, T means nothing.
+  const float next = value_of(key_of(hi) - 1u);
   const double zmax = widen(hi);
-  const Weight weight{sh.table, zmax, c_log2 * kExpTable};
-  // bins of level 0: linear in the logit, over the range that can carry mass
-  const float bin_scale = fminf((float)(kBins - 1) / (32.f * temp), 1e30f);
+  const double t_eff =
+      fmax(key_of(hi) == kLowestKey ? 1.0 : (double)temp, (zmax - widen(next)) / 64.0);
+  const Weight weight{sh.table, zmax, 1.4426950408889634074 / t_eff * kExpTable,
+                      fminf(hi - 32.f * temp, next)};
+  // bins of level 0: linear in the logit over 16 T below the largest (weights
+  // down to 1e-7), the rest of the row in the last
+  const float bin_scale = fminf((float)(kBins - 1) / (16.f * temp), 1e30f);
   // (rounded to an integer by the addition of 2^23)
   auto bin0 = [&](float z) -> uint32_t {
     return __float_as_uint(fminf((hi - z) * bin_scale, (float)(kBins - 1)) + 8388608.f) -
@@ -979,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   }
   if (min_p > 0.f) {
     // w >= min_p: a bound on the logit, rounded up to a float
-    const float z_min = __double2float_ru((double)hi + log2((double)min_p) / c_log2);
+    const float z_min = __double2float_ru((double)hi + log((double)min_p) * (double)temp);
     if (z_min > -INFINITY && key_of(z_min) > cut_key) {
       cut_key = key_of(z_min);
       cut_id = 0x7fffffff;
