@@ -376,15 +376,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return __float_as_uint(fminf((hi - z) * bin_scale, (float)(kBins - 1)) + 8388608.f) -
            0x4b000000u;
   };
-  // the largest float of a bin beyond b: tokens above it are in bins 0 .. b
-  auto below_bin = [&](uint32_t b) -> float {
-    uint32_t k = kLowestKey - 1;  // key of -inf
-    for (uint32_t bit = 0x80000000u; bit != 0u; bit >>= 1) {
-      const uint32_t t = k + bit;
-      if (t > k && t <= key_of(hi) && bin0(value_of(t)) > b) k = t;
-    }
-    return value_of(k);
-  };
   auto clear_bins = [&]() {
     for (int i = tid; i < kBins; i += kThreads) {
       h_cnt[i] = 0u;
@@ -555,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return static_cast<unsigned int>(min((unsigned long long)n, (limit - mass + w - 1) / w));
   };
 
-  // The exact cut inside bin b of the current histogram.
-  // The tokens with below < z <= top onto the short list of every block; with
-  // `masses` also the weights of all tokens, with `bins` these into their
-  // bins.  False when a block has too many; n: their number.
-  auto gather = [&](float below, float top, bool masses, bool bins, unsigned int& n,
+  // The tokens for which in(z) holds onto the short list of every block
+  // (none(m): no token of a vector whose largest is m); with `masses` also the
+  // weights of all tokens, with `bins` these into their bins.  False when a
+  // block has too many; n: their number.
+  auto gather = [&](auto in, auto none, bool masses, bool bins, unsigned int& n,
                     unsigned long long& mass) -> bool {
     unsigned long long* mine = list + rank * cap;
     if (tid == 0) sh.n_local = 0u;
@@ -568,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     unsigned long long m = 0ull;
     for (int v = tid; v < n_vec; v += kThreads) {
       const uint4 raw = slice[v];
-      const bool skip = !(Elem<T>::max_of(raw) > below);
+      const bool skip = none(Elem<T>::max_of(raw));
       if (skip && !masses) continue;
       float z[VE];
       Elem<T>::unpack(raw, z);
@@ -589,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       if (!skip) {
 #pragma unroll
         for (int i = 0; i < VE; ++i)
-          if (z[i] > below && z[i] <= top) {
+          if (in(z[i])) {
             const unsigned int at = atomicAdd(&sh.n_local, 1u);
             if (at < (unsigned int)cap)
               mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
@@ -632,11 +623,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // t holds word t (and t + kThreads when there are more), exchanged by
   // shuffles, and through shared memory for distances of a warp or more.
   bool dirty = false;  // the histogram has been written over
-  auto sort_list = [&](unsigned int n, unsigned long long mass0, bool masses,
-                       unsigned long long (&w)[2]) -> unsigned long long {
-    dirty = true;
-    unsigned long long e[2];  // the thread's words of the lists, wherever they lie
-    int at[2];
+  // the thread's words of the lists and their places in one array (-1: none)
+  auto list_words = [&](unsigned long long (&e)[2], int (&at)[2]) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int c = (tid + x * kThreads) / cap, i = (tid + x * kThreads) - c * cap;
@@ -646,7 +634,113 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         at[x] = i;
         for (int o = 0; o < c; ++o) at[x] += sh.list_n[o];
         e[x] = list[tid + x * kThreads];
-        sorted[at[x]] = e[x];
+      }
+    }
+  };
+  // Of the listed n tokens of bin b (which lie after b.count tokens of mass
+  // b.mass), those of the 256th of their key range that holds the cut, into
+  // the array, unsorted: n and what lies before them are updated.
+  auto narrow = [&](bool by_mass, Bin& b, unsigned int& n) {
+    dirty = true;
+    uint32_t* cnt = reinterpret_cast<uint32_t*>(sorted + kList);  // beside the array
+    uint32_t *lo = cnt + 256, *high = lo + 256;
+    unsigned long long e[2];
+    int at[2];
+    list_words(e, at);
+    uint32_t kmin = 0xffffffffu, kmax = 0u;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (at[x] >= 0) {
+        kmin = min(kmin, static_cast<uint32_t>(e[x] >> 32));
+        kmax = max(kmax, static_cast<uint32_t>(e[x] >> 32));
+      }
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
+    if (lane == 0) {
+      sh.red32[warp] = kmin;
+      sh.red32b[warp] = kmax;
+    }
+    for (int i = tid; i < 3 * 256; i += kThreads) cnt[i] = 0u;
+    if (tid == 0) sh.n_local = 0u;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      kmin = min(kmin, sh.red32[w]);
+      kmax = max(kmax, sh.red32b[w]);
+    }
+    int shift = 0;
+    while (((kmax - kmin) >> shift) >= 256u) ++shift;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (at[x] >= 0) {
+        const uint32_t key = static_cast<uint32_t>(e[x] >> 32), bin = (kmax - key) >> shift;
+        atomicAdd(&cnt[bin], 1u);
+        if (by_p) {
+          const unsigned long long w = weight(value_of(key));
+          const uint32_t wl = static_cast<uint32_t>(w);
+          const uint32_t wh =
+              static_cast<uint32_t>(w >> 32) + (atomicAdd(&lo[bin], wl) + wl < wl ? 1u : 0u);
+          if (wh != 0u) atomicAdd(&high[bin], wh);
+        }
+      }
+    __syncthreads();
+    if (warp == 0) {
+      // eight bins a lane
+      unsigned int c = 0u;
+      unsigned long long m = 0ull;
+      for (int i = 8 * lane; i < 8 * lane + 8; ++i) {
+        c += cnt[i];
+        m += (static_cast<unsigned long long>(high[i]) << 32) + lo[i];
+      }
+      unsigned int sc = c;
+      unsigned long long sm = m;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned int a = __shfl_up_sync(0xffffffffu, sc, o);
+        const unsigned long long d = __shfl_up_sync(0xffffffffu, sm, o);
+        if (lane >= o) {
+          sc += a;
+          sm += d;
+        }
+      }
+      sc += b.count - c;
+      sm += b.mass - m;
+      Bin f{};
+      bool some = false;
+      for (int i = 8 * lane; i < 8 * lane + 8; ++i) {
+        if (cnt[i] > 0u && (by_mass ? sm : (unsigned long long)sc) < b.limit) {
+          some = true;
+          f = Bin{sm, b.limit, sc, static_cast<uint32_t>(i)};
+        }
+        sc += cnt[i];
+        sm += (static_cast<unsigned long long>(high[i]) << 32) + lo[i];
+      }
+      const unsigned int votes = __ballot_sync(0xffffffffu, some);
+      if (lane == 31 - __clz(votes)) sh.bin = f;
+    }
+    __syncthreads();
+    b = sh.bin;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (at[x] >= 0 && (kmax - static_cast<uint32_t>(e[x] >> 32)) >> shift == b.bin)
+        sorted[atomicAdd(&sh.n_local, 1u)] = e[x];
+    __syncthreads();
+    n = sh.n_local;
+  };
+  // listed: the words are the lists' (otherwise the array's first n)
+  auto sort_list = [&](bool listed, unsigned int n, unsigned long long mass0, bool masses,
+                       unsigned long long (&w)[2]) -> unsigned long long {
+    dirty = true;
+    unsigned long long e[2];
+    int at[2];
+    if (listed) {
+      list_words(e, at);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (at[x] >= 0) sorted[at[x]] = e[x];
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        at[x] = tid + x * kThreads < (int)n ? tid + x * kThreads : -1;
+        e[x] = at[x] >= 0 ? sorted[at[x]] : 0ull;
       }
     }
     if (n <= kRankBelow) {
@@ -750,21 +844,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return cut;
   };
 
+  // The cut among the n listed tokens, which lie after b.count tokens of mass
+  // b.mass: the last before which the count (or the mass) is below b.limit.
+  auto list_cut = [&](bool by_mass, Bin b, unsigned int n) -> Cut {
+    const bool many = n > kRankBelow / 4;
+    if (many) narrow(by_mass, b, n);
+    unsigned long long w[2];
+    const unsigned long long m = sort_list(!many, n, b.mass, by_p, w);
+    return last_of(n, m, w, [&](int i, unsigned long long before) {
+      return (by_mass ? before : (unsigned long long)b.count + i) < b.limit;
+    });
+  };
+
   // The exact cut inside bin b of the current histogram.
   auto resolve = [&](bool by_mass, Bin b, bool again) -> Cut {
     const unsigned long long limit = b.limit;
-    // the bin's tokens: below < z <= top
-    float below = below_bin(b.bin), top = b.bin > 0u ? below_bin(b.bin - 1u) : hi;
+    bool level0 = true;
+    float below = 0.f, top = 0.f;  // the bin's tokens: below < z <= top (levels >= 1)
     for (;;) {
-      auto in_bin = [&](float z) { return z > below && z <= top; };
+      auto in_bin = [&](float z) {
+        if (level0) return z > -INFINITY && bin0(z) == b.bin;
+        return z > below && z <= top;
+      };
+      auto none = [&](float m) { return level0 ? bin0(m) > b.bin : !(m > below); };
       unsigned int n;
       unsigned long long unused;
-      if (gather(below, top, false, false, n, unused)) {
-        unsigned long long w[2];
-        const unsigned long long m = sort_list(n, b.mass, by_p, w);
-        const Cut cut = last_of(n, m, w, [&](int i, unsigned long long before) {
-          return (by_mass ? before : (unsigned long long)b.count + i) < limit;
-        });
+      if (gather(in_bin, none, false, false, n, unused)) {
+        const Cut cut = list_cut(by_mass, b, n);
         if (again) cluster.sync();  // the lists will be written again
         return cut;
       }
@@ -868,6 +974,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         return true;
       });
       b = find(by_mass, limit, b.count, b.mass);  // the same limit
+      level0 = false;
       const uint32_t last = kmax - (b.bin << shift), width = (1u << shift) - 1u;
       top = value_of(last);
       below = value_of((last - kmin > width ? last - width : kmin) - 1u);
@@ -907,7 +1014,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     // that of a top_p when they reach it.
     bool found = false, binned = false;
     if (top_list) {
-      const float below = edge > -INFINITY ? value_of(key_of(edge) - 1u) : edge;
       if (!by_k) {
         // Whether they will is guessed from the block's threads' largest: when
         // those above the edge are short of top_p of all, the weights go into
@@ -933,23 +1039,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       }
       unsigned int n;
       unsigned long long total;
-      if (gather(below, hi, !by_k, binned, n, total)) {
-        unsigned long long w[2];
-        const unsigned long long limit = by_k ? 0ull : p_limit(total);
+      if (gather([&](float z) { return z >= edge && z > -INFINITY; },
+                 [&](float m) { return m < edge; }, !by_k, binned, n, total)) {
+        const unsigned long long limit = by_k ? (unsigned long long)top_k : p_limit(total);
         if (by_k || list_reaches(limit)) {
-          const unsigned long long m = sort_list(n, 0ull, by_p, w);
-          Cut cut;
-          if (by_k) {
-            const int k = min(top_k, (int)n);  // fewer: the row has no more
-            cut = last_of(n, m, w, [&](int i, unsigned long long) { return i < k; });
-            if (by_p) {
-              const unsigned long long k_limit = p_limit(cut.mass);
-              cut = last_of(n, m, w, [&](int i, unsigned long long before) {
-                return i < k && before < k_limit;
-              });
-            }
-          } else {
-            cut = last_of(n, m, w, [&](int, unsigned long long before) { return before < limit; });
+          Cut cut = list_cut(!by_k, Bin{0ull, limit, 0u, 0u}, n);
+          if (by_k && by_p) {
+            const Cut c = list_cut(true, Bin{0ull, p_limit(cut.mass), 0u, 0u}, n);
+            if (c.key > cut.key || (c.key == cut.key && c.id < cut.id)) cut = c;
           }
           found = true;
           cut_key = cut.key;
