@@ -1,10 +1,17 @@
-// Attention of a chunk of new tokens over a paged cache.
+// Attention of a chunk of new tokens over a paged cache, fp32.
 //
 //   out[t, h] = sum_j softmax_j(scale q.k_j) v_j  over slots j <= p(t)
 //
-// One warp per (token, query head) on CUDA cores: lanes split the head, eight
-// keys are in flight per online-softmax update, fp32 throughout.
-#include <cuda_bf16.h>
+// CUDA cores, fp32 throughout.  A row (token, query head) belongs to S warps
+// of a block, which take its keys eight at a time in turn and merge their
+// maxima, sums and outputs through shared memory; S is as large as leaves the
+// machine's warps enough rows (a 128-token prompt of four heads is 512 rows:
+// one warp each would leave nine tenths of the machine idle; 27 us against
+// 8).  Of a step's eight keys the lanes split the head; the eight
+// products are summed over the warp by halving (9 exchanges for 8 sums), so
+// that each lane ends with one key's score and computes one exponential.
+// Bound by latency at the sizes this path is for; K and V rows are read from
+// L2 once per query row.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -17,116 +24,174 @@ namespace medusa {
 
 namespace {
 
-__device__ __forceinline__ float ld(const __nv_bfloat16* x) { return __bfloat162float(*x); }
-__device__ __forceinline__ float ld(const float* x) { return *x; }
-__device__ __forceinline__ void st(__nv_bfloat16* d, float x) { *d = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void st(float* d, float x) { *d = x; }
+constexpr int kWarps = 8;
 
-template <typename T, int PER>
-__global__ void __launch_bounds__(256) chunk_attn_row_kernel(ChunkParams p) {
+template <int PER>
+__global__ void __launch_bounds__(kWarps * 32) chunk_attn_f32_kernel(ChunkParams p, int S) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int DH = PER * 32;
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)p.T * p.Hq;
-  for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < rows;
-       w += (long long)gridDim.x * 8) {
-    const int t = static_cast<int>(w / p.Hq), hq = static_cast<int>(w - (long long)t * p.Hq);
-    int n = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = kWarps / S;  // of a block
+  const int split = warp % S;
+  __shared__ float s_ml[kWarps][2];
+  __shared__ float s_acc[kWarps][DH];
+  const long long row = (long long)blockIdx.x * rows + warp / S;
+  int visible = 0, n = 0, t = 0, hq = 0;
+  bool live = row < (long long)p.T * p.Hq;
+  if (live) {
+    t = static_cast<int>(row / p.Hq);
+    hq = static_cast<int>(row - (long long)t * p.Hq);
     for (int b = lane; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
     n = __reduce_add_sync(0xffffffffu, n);
-    if (n >= p.B) continue;  // behind the last sequence
-    const int first = p.cu_q[n], len = p.cu_q[n + 1] - first, kv = p.kv_len[n];
-    if (first < 0 || t < first || first + len > p.T || kv < 0 || kv > (long long)p.max_pages * p.page_size) {
-      if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-      continue;
-    }
-    const int visible = max(0, kv - len + (t - first) + 1);
-    const T* qp = static_cast<const T*>(p.q) + t * p.q_stride + (size_t)hq * DH + lane * PER;
-    float qv[PER], acc[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      qv[e] = ld(qp + e) * p.scale;
-      acc[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j0 = 0; j0 < visible;) {
-      const int pg = j0 / p.page_size, r0 = j0 - pg * p.page_size;
-      const int id = p.table[(size_t)n * p.max_pages + pg];
-      const int end = min(visible, j0 - r0 + p.page_size);
-      if (id < 0 || id >= p.n_pages) {
-        if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-        j0 = end;
-        continue;
-      }
-      const size_t row = ((size_t)id * p.Hkv + hq / p.G) * p.page_size + r0;
-      const T* kp = static_cast<const T*>(p.K) + row * DH + lane * PER;
-      const T* vp = static_cast<const T*>(p.V) + row * DH + lane * PER;
-      for (; j0 < end; j0 += 8) {
-        const int nk = min(8, end - j0);
-        float s[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          float d = 0.f;
-          if (x < nk) {
-#pragma unroll
-            for (int e = 0; e < PER; ++e) d += qv[e] * ld(kp + (size_t)x * DH + e);
-          }
-          s[x] = d;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
-        float mn = m;
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (x < nk) mn = fmaxf(mn, s[x]);
-        const float corr = expf(m - mn);
-        l *= corr;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] *= corr;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          if (x < nk) {
-            const float pw = expf(s[x] - mn);
-            l += pw;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += pw * ld(vp + (size_t)x * DH + e);
-          }
-        }
-        m = mn;
-        kp += 8 * DH;
-        vp += 8 * DH;
-      }
-      j0 = end;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    T* o = static_cast<T*>(p.out) + (size_t)w * DH + lane * PER;
-    bool finite = true;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const float y = acc[e] * inv;
-      finite = finite && isfinite(y);
-      st(o + e, y);
-    }
-    if (!finite) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    live = n < p.B;  // not behind the last sequence
   }
+  if (live) {
+    const int first = p.cu_q[n], len = p.cu_q[n + 1] - first, kv = p.kv_len[n];
+    if (first < 0 || t < first || first + len > p.T || kv < 0 ||
+        kv > (long long)p.max_pages * p.page_size) {
+      if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      live = false;
+    } else {
+      visible = max(0, kv - len + (t - first) + 1);
+    }
+  }
+  float qv[PER], acc[PER], m = -INFINITY, l = 0.f;
+  const float* qp = static_cast<const float*>(p.q) + t * p.q_stride + (size_t)hq * DH + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    qv[e] = live ? qp[e] * p.scale : 0.f;
+    acc[e] = 0.f;
+  }
+  const float* Kp = static_cast<const float*>(p.K) + lane * PER;
+  const float* Vp = static_cast<const float*>(p.V) + lane * PER;
+  const int mine = (lane >> 2) & 7;  // the key whose score this lane ends with
+  for (int j0 = split * 8; j0 < visible; j0 += S * 8) {
+    const int nk = min(8, visible - j0);
+    size_t at[8];  // element offset of each key's row
+    unsigned int have = (1u << nk) - 1u;
+    const int pg0 = j0 / p.page_size, r0 = j0 - pg0 * p.page_size;
+    if (r0 + nk <= p.page_size) {  // the eight lie in one page
+      const int id = p.table[(size_t)n * p.max_pages + pg0];
+      if (id < 0 || id >= p.n_pages) have = 0u;
+      const size_t first =
+          (((size_t)max(id, 0) * p.Hkv + hq / p.G) * p.page_size + r0) * DH;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) at[x] = first + (size_t)x * DH;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int j = min(j0 + x, visible - 1), pg = j / p.page_size;
+        const int id = p.table[(size_t)n * p.max_pages + pg];
+        at[x] = 0;
+        if (id >= 0 && id < p.n_pages)
+          at[x] = (((size_t)id * p.Hkv + hq / p.G) * p.page_size + (j - pg * p.page_size)) * DH;
+        else
+          have &= ~(1u << x);
+      }
+    }
+    if (have != (1u << nk) - 1u && lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    float d[8], v[8][PER];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      d[x] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) v[x][e] = 0.f;
+      if ((have >> x) & 1u) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) d[x] += qv[e] * Kp[at[x] + e];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[x][e] = Vp[at[x] + e];
+      }
+    }
+    // lanes with bit 4 set keep keys 4-7, with bit 3 the upper two of those, ...
+#pragma unroll
+    for (int o = 16, w = 4; o >= 4; o >>= 1, w >>= 1) {
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (x >= w) break;
+        const float send = up ? d[x] : d[x + w], keep = up ? d[x + w] : d[x];
+        d[x] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    }
+    float s = d[0];
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    if (!((have >> mine) & 1u)) s = -INFINITY;
+    float mn = s;
+#pragma unroll
+    for (int o = 16; o >= 4; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(mn, m);
+    // a NaN score stays NaN; a step without a page adds nothing
+    const float w = mn == -INFINITY && s == -INFINITY ? 0.f : expf(s - mn);
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o >= 4; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float corr = m == -INFINITY ? 0.f : expf(m - mn);
+    l = l * corr + sum;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= corr;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float wx = __shfl_sync(0xffffffffu, w, x * 4);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] += wx * v[x][e];
+    }
+    m = mn;
+  }
+  if (S > 1) {
+    if (lane == 0) {
+      s_ml[warp][0] = m;
+      s_ml[warp][1] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) s_acc[warp][lane * PER + e] = acc[e];
+    __syncthreads();
+    if (split != 0) return;
+    float M = m;
+    for (int x = 1; x < S; ++x) M = fmaxf(M, s_ml[warp + x][0]);
+    const float c0 = m == -INFINITY ? 0.f : expf(m - M);
+    l *= c0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= c0;
+    for (int x = 1; x < S; ++x) {
+      if (s_ml[warp + x][0] == -INFINITY) continue;  // no key
+      const float c = expf(s_ml[warp + x][0] - M);
+      l += c * s_ml[warp + x][1];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] += c * s_acc[warp + x][lane * PER + e];
+    }
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float* o = static_cast<float*>(p.out) + (size_t)row * DH + lane * PER;
+  bool finite = true;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const float y = acc[e] * inv;
+    finite = finite && isfinite(y);
+    o[e] = y;
+  }
+  if (!finite) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
 }
 
-template <typename T>
-medusa_status_t launch_rows(const ChunkParams& p, int dh, cudaStream_t stream) {
-  const long long blocks = ((long long)p.T * p.Hq + 7) / 8;
-  const int grid = (int)(blocks < 148 * 64 ? blocks : 148 * 64);
+medusa_status_t launch_f32(const ChunkParams& p, int dh, cudaStream_t stream) {
+  const long long rows = (long long)p.T * p.Hq;
+  int S = kWarps;
+  while (S > 1 && rows * S > (long long)device_sm_count() * 48) S >>= 1;
+  const long long blocks = (rows * S + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffffLL) return fail(MEDUSA_ERR_SHAPE, "chunk_attention: T * Hq too large");
+  const int grid = static_cast<int>(blocks), threads = kWarps * 32;
   switch (dh / 32) {
-    case 1: launch(chunk_attn_row_kernel<T, 1>, grid, 256, 0, stream, p); break;
-    case 2: launch(chunk_attn_row_kernel<T, 2>, grid, 256, 0, stream, p); break;
-    case 3: launch(chunk_attn_row_kernel<T, 3>, grid, 256, 0, stream, p); break;
-    case 4: launch(chunk_attn_row_kernel<T, 4>, grid, 256, 0, stream, p); break;
-    case 5: launch(chunk_attn_row_kernel<T, 5>, grid, 256, 0, stream, p); break;
-    case 6: launch(chunk_attn_row_kernel<T, 6>, grid, 256, 0, stream, p); break;
-    case 7: launch(chunk_attn_row_kernel<T, 7>, grid, 256, 0, stream, p); break;
-    default: launch(chunk_attn_row_kernel<T, 8>, grid, 256, 0, stream, p); break;
+    case 1: launch(chunk_attn_f32_kernel<1>, grid, threads, 0, stream, p, S); break;
+    case 2: launch(chunk_attn_f32_kernel<2>, grid, threads, 0, stream, p, S); break;
+    case 3: launch(chunk_attn_f32_kernel<3>, grid, threads, 0, stream, p, S); break;
+    case 4: launch(chunk_attn_f32_kernel<4>, grid, threads, 0, stream, p, S); break;
+    case 5: launch(chunk_attn_f32_kernel<5>, grid, threads, 0, stream, p, S); break;
+    case 6: launch(chunk_attn_f32_kernel<6>, grid, threads, 0, stream, p, S); break;
+    case 7: launch(chunk_attn_f32_kernel<7>, grid, threads, 0, stream, p, S); break;
+    default: launch(chunk_attn_f32_kernel<8>, grid, threads, 0, stream, p, S); break;
   }
   return check_launch("chunk_attention");
 }
@@ -146,7 +211,7 @@ medusa_status_t chunk_attention(const void* q, long long q_stride, const medusa_
   ChunkParams p{q, q_stride, pages.K, pages.V, pages.table, cu_q, kv_len, pages.n_pages,
                 pages.page_size, pages.max_pages, B, T, Hq, Hkv, Hq / Hkv, scale, out, status};
   if (dt == MEDUSA_BF16) return chunk_attention_tc(p, dh, ws, stream);
-  return launch_rows<float>(p, dh, stream);
+  return launch_f32(p, dh, stream);
 }
 
 }  // namespace medusa
