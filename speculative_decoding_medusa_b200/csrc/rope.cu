@@ -10,24 +10,24 @@
 // taken as a quadrant and a remainder of at most 1/8 turn, go through
 // sinpi / cospi in fp32 (angle error below 2^-28 turns).
 //
-// A block takes TB tokens: their rot / 2 sine/cosine pairs are computed once
-// into shared memory and serve every head (and, in the append, q and k).  A
-// thread then owns one unit of two 16-byte vectors per token (the two halves
-// of VEC pairs) and moves all TB tokens' units with their loads in flight
-// together.  Bound by HBM: every byte is read once and written once.
+// A token's rot / 2 sine/cosine pairs are computed once into shared memory and
+// serve every head (and, in the append, q and k).  The work is units of two
+// 16-byte vectors (the two halves of VEC pairs), one per thread at a time.
+// Bound by HBM: every byte is read once and written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "abi_internal.h"
+#include "attn_common.cuh"
 #include "common.cuh"
 
 namespace medusa {
 
 namespace {
 
-constexpr int kRopeThreads = 384;  // largest block: four of them fit on an SM
+constexpr int kRopeThreads = 384;  // largest block: several of them fit on an SM
 
 struct RopeParams {
   const void *q, *k, *v;
@@ -98,135 +98,219 @@ __device__ __forceinline__ Unit unit_of(int w, int nq, int nk, const RopeParams&
   return u;
 }
 
-template <typename T, int VEC, int TB, bool kAppend>
-__global__ void __launch_bounds__(kRopeThreads, TB == 1 ? 4 : 3) rope_kernel(RopeParams p) {
+// What a row of the append needs besides its data, found by one warp.
+struct Row {
+  int state;      // bit 0: the row exists, bit 1: it has a cache slot
+  int pos;        // position of the token
+  long long dst;  // row of kv head 0 in the pools
+};
+
+template <bool kAppend>
+__device__ __forceinline__ Row row_of(int t, const RopeParams& p) {
+  Row r{0, 0, 0};
+  if (!kAppend) {
+    if (t < p.T) r = Row{1, p.positions[t], 0};
+    return r;
+  }
+  // the sequence of row t: how many sequences end at or before it
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  for (int b = lane; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (t < p.T && n < p.B) {
+    r.state = 1;
+    const int first = p.cu_q[n];
+    const int slot = p.kv_len[n] - (p.cu_q[n + 1] - first) + (t - first);
+    r.pos = p.positions != nullptr ? p.positions[t] : slot;
+    if (slot >= 0) {
+      const int pg = slot / p.page_size;
+      const int id = pg < p.max_pages ? p.table[(size_t)n * p.max_pages + pg] : -1;
+      if (id >= 0 && id < p.n_pages) {
+        r.state = 3;
+        r.dst = (long long)id * p.Hkv * p.page_size + (slot - pg * p.page_size);
+      } else if (lane == 0) {
+        report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      }
+    }
+  }
+  return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void fetch(const Unit& u, int t, const RopeParams& p, Vec<T, VEC>& a,
+                                      Vec<T, VEC>& b) {
+  const T* s = static_cast<const T*>(u.is_q ? p.q : u.is_v ? p.v : p.k) + (size_t)u.h * p.dh +
+               t * (u.is_q ? p.q_stride : u.is_v ? p.v_stride : p.k_stride);
+  a = *reinterpret_cast<const Vec<T, VEC>*>(s + u.o0);
+  if (u.o1 >= 0) b = *reinterpret_cast<const Vec<T, VEC>*>(s + u.o1);
+}
+
+// Rotates the unit and stores it.  c, s: the row's cosines and sines; the
+// arithmetic takes two pairs at a time (paired fp32 instructions).
+template <typename T, int VEC, bool kAppend>
+__device__ __forceinline__ void finish(const Unit& u, int t, const Row& r, const float* cos_t,
+                                       const float* sin_t, const RopeParams& p, Vec<T, VEC>& a,
+                                       Vec<T, VEC>& b) {
+  if (r.state == 0 || (kAppend && !u.is_q && r.state != 3)) return;
+  T* dst;
+  if (u.is_q)
+    dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + (size_t)u.h * p.dh;
+  else if (kAppend)
+    dst = static_cast<T*>(u.is_v ? p.V : p.K) + (r.dst + (long long)u.h * p.page_size) * p.dh;
+  else
+    dst = static_cast<T*>(p.k_out) + t * p.k_out_stride + (size_t)u.h * p.dh;
+  if (u.turns) {
+    const float *fc = cos_t + u.un * VEC, *fs = sin_t + u.un * VEC;
+    T z0[VEC], z1[VEC];  // the pairs' two elements
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (p.interleaved) {
+        z0[e] = 2 * e < VEC ? a.e[(2 * e) % VEC] : b.e[(2 * e) % VEC];
+        z1[e] = 2 * e + 1 < VEC ? a.e[(2 * e + 1) % VEC] : b.e[(2 * e + 1) % VEC];
+      } else {
+        z0[e] = a.e[e];
+        z1[e] = b.e[e];
+      }
+    }
+    if (VEC == 1) {
+      const float x0 = to_f(z0[0]), x1 = to_f(z1[0]);
+      from_f(z0[0], x0 * fc[0] - x1 * fs[0]);
+      from_f(z1[0], x0 * fs[0] + x1 * fc[0]);
+    } else {
+#pragma unroll
+      for (int e = 0; e + 1 < VEC; e += 2) {
+        const float2 c = *reinterpret_cast<const float2*>(fc + e);
+        const float2 s = *reinterpret_cast<const float2*>(fs + e);
+        const uint64_t x0 = f32x2_pack(to_f(z0[e]), to_f(z0[e + 1]));
+        const uint64_t x1 = f32x2_pack(to_f(z1[e]), to_f(z1[e + 1]));
+        const uint64_t c2 = f32x2_pack(c.x, c.y), s2 = f32x2_pack(s.x, s.y);
+        const uint64_t n2 = f32x2_pack(-s.x, -s.y);
+        float y0, y1;
+        f32x2_unpack(f32x2_fma(x0, c2, f32x2_mul(x1, n2)), y0, y1);
+        from_f(z0[e], y0);
+        from_f(z0[e + 1], y1);
+        f32x2_unpack(f32x2_fma(x0, s2, f32x2_mul(x1, c2)), y0, y1);
+        from_f(z1[e], y0);
+        from_f(z1[e + 1], y1);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (p.interleaved) {
+        if (2 * e < VEC) a.e[(2 * e) % VEC] = z0[e];
+        else b.e[(2 * e) % VEC] = z0[e];
+        if (2 * e + 1 < VEC) a.e[(2 * e + 1) % VEC] = z1[e];
+        else b.e[(2 * e + 1) % VEC] = z1[e];
+      } else {
+        a.e[e] = z0[e];
+        b.e[e] = z1[e];
+      }
+    }
+  }
+  *reinterpret_cast<Vec<T, VEC>*>(dst + u.o0) = a;
+  if (u.o1 >= 0) *reinterpret_cast<Vec<T, VEC>*>(dst + u.o1) = b;
+}
+
+// A block per token.  The first unit's loads go out before anything else: they
+// depend on no metadata, and hide the chain sequence -> slot -> page -> angle
+// behind them.
+template <typename T, int VEC, bool kAppend>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_block_kernel(RopeParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  using V = Vec<T, VEC>;
-  extern __shared__ float2 cs[];  // [TB][rot / 2]
-  __shared__ int s_pos[TB];       // position of the token
-  __shared__ int s_state[TB];     // bit 0: the row exists, bit 1: it has a cache slot
-  __shared__ long long s_dst[TB];  // row of kv head 0 in the pools
-  const int t0 = blockIdx.x * TB;
-  const int tid = threadIdx.x, lane = tid & 31;
+  extern __shared__ float cs[];  // cosines [rot / 2], then the sines
+  __shared__ Row s_row;
+  const int t = blockIdx.x, tid = threadIdx.x;
   const int half = p.rot >> 1;
   const int nq = p.q != nullptr ? p.Hq * p.units : 0;
   const int nk = p.k != nullptr ? p.Hkv * p.units : 0;
   const int total = nq + nk + (kAppend ? p.Hkv * p.v_units : 0);
-
-  // The first unit's loads go out before anything else: they depend on no
-  // metadata, and hide the chain sequence -> slot -> page -> angle behind them.
-  V a[TB], b[TB];
-  auto fetch = [&](const Unit& u) {
-    const T* src = static_cast<const T*>(u.is_q ? p.q : u.is_v ? p.v : p.k) + (size_t)u.h * p.dh;
-    const long long stride = u.is_q ? p.q_stride : u.is_v ? p.v_stride : p.k_stride;
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      if (t0 + j < p.T) {
-        const T* s = src + (t0 + j) * stride;
-        a[j] = *reinterpret_cast<const V*>(s + u.o0);
-        if (u.o1 >= 0) b[j] = *reinterpret_cast<const V*>(s + u.o1);
-      }
-    }
-  };
+  Vec<T, VEC> a, b;
   int w = tid;
   Unit u{};
   if (w < total) {
     u = unit_of<VEC>(w, nq, nk, p);
-    fetch(u);
+    fetch<T, VEC>(u, t, p, a, b);
   }
-
-  if (kAppend) {
-    for (int j = tid >> 5; j < TB; j += blockDim.x >> 5) {
-      const int t = t0 + j;
-      // the sequence of row t: how many sequences end at or before it
-      int n = 0;
-      for (int b = lane; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) {
-        int state = 0, pos = 0;
-        long long dst = 0;
-        if (t < p.T && n < p.B) {
-          state = 1;
-          const int first = p.cu_q[n];
-          const int slot = p.kv_len[n] - (p.cu_q[n + 1] - first) + (t - first);
-          pos = p.positions != nullptr ? p.positions[t] : slot;
-          if (slot >= 0) {
-            const int pg = slot / p.page_size;
-            const int id = pg < p.max_pages ? p.table[(size_t)n * p.max_pages + pg] : -1;
-            if (id >= 0 && id < p.n_pages) {
-              state = 3;
-              dst = (long long)id * p.Hkv * p.page_size + (slot - pg * p.page_size);
-            } else {
-              report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-            }
-          }
-        }
-        s_state[j] = state;
-        s_pos[j] = pos;
-        s_dst[j] = dst;
-      }
-    }
-  } else if (tid < TB) {
-    s_state[tid] = t0 + tid < p.T ? 1 : 0;
-    s_pos[tid] = t0 + tid < p.T ? p.positions[t0 + tid] : 0;
+  if (tid < 32) {
+    const Row r = row_of<kAppend>(t, p);
+    if (tid == 0) s_row = r;
   }
   __syncthreads();
-  const float sign = p.inverse ? -1.f : 1.f;
-  for (int e = tid; e < TB * half; e += blockDim.x) {
-    const int j = e / half, i = e - j * half;
-    cs[e] = turn_cos_sin(p.turns[i], s_pos[j], p.scale, sign);
+  const Row r = s_row;
+  for (int i = tid; i < half; i += blockDim.x) {
+    const float2 f = turn_cos_sin(p.turns[i], r.pos, p.scale, p.inverse ? -1.f : 1.f);
+    cs[i] = f.x;
+    cs[half + i] = f.y;
   }
   __syncthreads();
-
   while (w < total) {
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      if (s_state[j] == 0 || (kAppend && !u.is_q && s_state[j] != 3)) continue;
-      T* dst;
-      if (u.is_q)
-        dst = static_cast<T*>(p.q_out) + (t0 + j) * p.q_out_stride + (size_t)u.h * p.dh;
-      else if (kAppend)
-        dst = static_cast<T*>(u.is_v ? p.V : p.K) + (s_dst[j] + (long long)u.h * p.page_size) * p.dh;
-      else
-        dst = static_cast<T*>(p.k_out) + (t0 + j) * p.k_out_stride + (size_t)u.h * p.dh;
-      if (u.turns) {
-        const float2* f = cs + j * half + u.un * VEC;
-        if (p.interleaved) {
-          T z[2 * VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            z[e] = a[j].e[e];
-            z[VEC + e] = b[j].e[e];
-          }
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float x0 = to_f(z[2 * e]), x1 = to_f(z[2 * e + 1]);
-            from_f(z[2 * e], x0 * f[e].x - x1 * f[e].y);
-            from_f(z[2 * e + 1], x0 * f[e].y + x1 * f[e].x);
-          }
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            a[j].e[e] = z[e];
-            b[j].e[e] = z[VEC + e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float x0 = to_f(a[j].e[e]), x1 = to_f(b[j].e[e]);
-            from_f(a[j].e[e], x0 * f[e].x - x1 * f[e].y);
-            from_f(b[j].e[e], x0 * f[e].y + x1 * f[e].x);
-          }
-        }
-      }
-      *reinterpret_cast<V*>(dst + u.o0) = a[j];
-      if (u.o1 >= 0) *reinterpret_cast<V*>(dst + u.o1) = b[j];
-    }
+    finish<T, VEC, kAppend>(u, t, r, cs, cs + half, p, a, b);
     w += blockDim.x;
     if (w < total) {
       u = unit_of<VEC>(w, nq, nk, p);
-      fetch(u);
+      fetch<T, VEC>(u, t, p, a, b);
     }
+  }
+}
+
+// Many tokens, a thread per unit: resident blocks walk the tokens, each with
+// the next token's data and angles and the one after's metadata on their way
+// while it finishes the current one; one barrier a token.  8192 tokens of
+// 32 + 8 heads written into pages (214 MB): kPipeTime, against 60 us with a
+// block per token, whose latencies nothing covers but the other blocks.
+template <typename T, int VEC, bool kAppend>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  extern __shared__ float cs[];  // two tokens' cosines and sines
+  __shared__ Row s_row[3];
+  const int tid = threadIdx.x, step = gridDim.x;
+  const int half = p.rot >> 1;
+  const int nq = p.q != nullptr ? p.Hq * p.units : 0;
+  const int nk = p.k != nullptr ? p.Hkv * p.units : 0;
+  const int total = nq + nk + (kAppend ? p.Hkv * p.v_units : 0);
+  const bool works = tid < total;
+  const Unit u = unit_of<VEC>(works ? tid : 0, nq, nk, p);
+  const float sign = p.inverse ? -1.f : 1.f;
+  auto angles = [&](int pos, float* table) {
+    for (int i = tid; i < half; i += blockDim.x) {
+      const float2 f = turn_cos_sin(p.turns[i], pos, p.scale, sign);
+      table[i] = f.x;
+      table[half + i] = f.y;
+    }
+  };
+  const bool meta = tid >= static_cast<int>(blockDim.x) - 32;  // the last warp
+  int t = blockIdx.x;
+  Vec<T, VEC> a, b, a2, b2;
+  if (works && t < p.T) fetch<T, VEC>(u, t, p, a, b);
+  if (meta) {
+    const Row r0 = row_of<kAppend>(t, p);
+    const Row r1 = row_of<kAppend>(t + step, p);
+    if ((tid & 31) == 0) {
+      s_row[0] = r0;
+      s_row[1] = r1;
+    }
+  }
+  __syncthreads();
+  angles(s_row[0].pos, cs);
+  __syncthreads();
+  for (int i = 0, cur = 0, nxt = 1, aft = 2; t < p.T; ++i, t += step) {
+    const float* table = cs + (i & 1) * 2 * half;
+    if (works && t + step < p.T) fetch<T, VEC>(u, t + step, p, a2, b2);
+    if (t + step < p.T) angles(s_row[nxt].pos, cs + ((i + 1) & 1) * 2 * half);
+    if (meta && t + 2 * step < p.T) {
+      const Row r = row_of<kAppend>(t + 2 * step, p);
+      if ((tid & 31) == 0) s_row[aft] = r;
+    }
+    if (works) finish<T, VEC, kAppend>(u, t, s_row[cur], table, table + half, p, a, b);
+    __syncthreads();
+    a = a2;
+    b = b2;
+    const int was = cur;
+    cur = nxt;
+    nxt = aft;
+    aft = was;
   }
 }
 
@@ -261,12 +345,13 @@ medusa_status_t launch_vec(RopeParams& p, cudaStream_t stream) {
                    (kAppend ? p.Hkv * p.v_units : 0);
   const int rounds = (work + kRopeThreads - 1) / kRopeThreads;
   const int threads = ((work + rounds - 1) / rounds + 31) / 32 * 32;
-  const size_t table = (p.rot / 2) * sizeof(float2);
-  // two tokens a block once one a block fills the machine twice over
-  if (p.T >= 2 * 4 * device_sm_count())
-    launch(rope_kernel<T, VEC, 2, kAppend>, (p.T + 1) / 2, threads, 2 * table, stream, p);
+  const size_t table = (p.rot / 2) * sizeof(float);
+  // resident blocks once they have several tokens each
+  const int resident = 3 * device_sm_count();
+  if (work <= kRopeThreads && p.T >= 2 * resident)
+    launch(rope_pipe_kernel<T, VEC, kAppend>, resident, threads, 4 * table, stream, p);
   else
-    launch(rope_kernel<T, VEC, 1, kAppend>, p.T, threads, table, stream, p);
+    launch(rope_block_kernel<T, VEC, kAppend>, p.T, threads, 2 * table, stream, p);
   return check_launch(kAppend ? "rope_append" : "rope");
 }
 
