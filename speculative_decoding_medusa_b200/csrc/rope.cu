@@ -27,6 +27,8 @@ namespace medusa {
 
 namespace {
 
+constexpr int kChunk = 32;         // tokens whose metadata a block finds at once
+constexpr int kSmallB = 256;       // sequences whose lengths fit in shared memory
 constexpr int kRopeThreads = 384;  // largest block: several of them fit on an SM
 
 struct RopeParams {
@@ -147,7 +149,7 @@ __device__ __forceinline__ void fetch(const Unit& u, int t, const RopeParams& p,
 
 // Rotates the unit and stores it.  c, s: the row's cosines and sines; the
 // arithmetic takes two pairs at a time (paired fp32 instructions).
-template <typename T, int VEC, bool kAppend>
+template <typename T, int VEC, bool kInter, bool kAppend>
 __device__ __forceinline__ void finish(const Unit& u, int t, const Row& r, const float* cos_t,
                                        const float* sin_t, const RopeParams& p, Vec<T, VEC>& a,
                                        Vec<T, VEC>& b) {
@@ -164,7 +166,7 @@ __device__ __forceinline__ void finish(const Unit& u, int t, const Row& r, const
     T z0[VEC], z1[VEC];  // the pairs' two elements
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      if (p.interleaved) {
+      if (kInter) {
         z0[e] = 2 * e < VEC ? a.e[(2 * e) % VEC] : b.e[(2 * e) % VEC];
         z1[e] = 2 * e + 1 < VEC ? a.e[(2 * e + 1) % VEC] : b.e[(2 * e + 1) % VEC];
       } else {
@@ -196,7 +198,7 @@ __device__ __forceinline__ void finish(const Unit& u, int t, const Row& r, const
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      if (p.interleaved) {
+      if (kInter) {
         if (2 * e < VEC) a.e[(2 * e) % VEC] = z0[e];
         else b.e[(2 * e) % VEC] = z0[e];
         if (2 * e + 1 < VEC) a.e[(2 * e + 1) % VEC] = z1[e];
@@ -214,7 +216,7 @@ __device__ __forceinline__ void finish(const Unit& u, int t, const Row& r, const
 // A block per token.  The first unit's loads go out before anything else: they
 // depend on no metadata, and hide the chain sequence -> slot -> page -> angle
 // behind them.
-template <typename T, int VEC, bool kAppend>
+template <typename T, int VEC, bool kInter, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_block_kernel(RopeParams p) {
   grid_dep_wait();
   grid_dep_launch();
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_block_kernel(RopeParams 
   }
   __syncthreads();
   while (w < total) {
-    finish<T, VEC, kAppend>(u, t, r, cs, cs + half, p, a, b);
+    finish<T, VEC, kInter, kAppend>(u, t, r, cs, cs + half, p, a, b);
     w += blockDim.x;
     if (w < total) {
       u = unit_of<VEC>(w, nq, nk, p);
@@ -254,17 +256,51 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_block_kernel(RopeParams 
   }
 }
 
-// Many tokens, a thread per unit: resident blocks walk the tokens, each with
-// the next token's data and angles and the one after's metadata on their way
-// while it finishes the current one; one barrier a token.  8192 tokens of
-// 32 + 8 heads written into pages (214 MB): kPipeTime, against 60 us with a
-// block per token, whose latencies nothing covers but the other blocks.
-template <typename T, int VEC, bool kAppend>
+// What row_of finds, by one thread, with the sequences' lengths in cu and kv
+// (shared memory, or global where they do not fit).
+template <bool kAppend>
+__device__ __forceinline__ Row row_of_thread(int t, const int* cu, const int* kv,
+                                             const RopeParams& p) {
+  Row r{0, 0, 0};
+  if (t >= p.T) return r;
+  if (!kAppend) return Row{1, p.positions[t], 0};
+  int lo = 0, hi = p.B;  // the first sequence that ends after t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  if (lo >= p.B) return r;
+  r.state = 1;
+  const int first = cu[lo], slot = kv[lo] - (cu[lo + 1] - first) + (t - first);
+  r.pos = p.positions != nullptr ? p.positions[t] : slot;
+  if (slot >= 0) {
+    const int pg = slot / p.page_size;
+    const int id = pg < p.max_pages ? p.table[(size_t)lo * p.max_pages + pg] : -1;
+    if (id >= 0 && id < p.n_pages) {
+      r.state = 3;
+      r.dst = (long long)id * p.Hkv * p.page_size + (slot - pg * p.page_size);
+    } else {
+      report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    }
+  }
+  return r;
+}
+
+// Many tokens, a thread per unit: resident blocks walk the tokens in chunks of
+// kChunk, whose metadata they find at once, with the next token's data and
+// angles on their way while they finish the current one; one barrier a token.
+// 8192 tokens of 32 + 8 heads written into pages (214 MB): kPipeTime, against
+// 60 us with a block per token, whose latencies only other blocks cover, and
+// 54 us with each token's metadata found two tokens ahead (its chain of three
+// reads was as long as a token's turn).
+template <typename T, int VEC, bool kInter, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ float cs[];  // two tokens' cosines and sines
-  __shared__ Row s_row[3];
+  __shared__ Row s_row[kChunk];
+  __shared__ int s_cu[kAppend ? kSmallB + 1 : 1], s_kv[kAppend ? kSmallB : 1];
   const int tid = threadIdx.x, step = gridDim.x;
   const int half = p.rot >> 1;
   const int nq = p.q != nullptr ? p.Hq * p.units : 0;
@@ -280,37 +316,37 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
       table[half + i] = f.y;
     }
   };
-  const bool meta = tid >= static_cast<int>(blockDim.x) - 32;  // the last warp
-  int t = blockIdx.x;
   Vec<T, VEC> a, b, a2, b2;
+  int t = blockIdx.x;
   if (works && t < p.T) fetch<T, VEC>(u, t, p, a, b);
-  if (meta) {
-    const Row r0 = row_of<kAppend>(t, p);
-    const Row r1 = row_of<kAppend>(t + step, p);
-    if ((tid & 31) == 0) {
-      s_row[0] = r0;
-      s_row[1] = r1;
+  const bool small = kAppend && p.B <= kSmallB;
+  if (small) {
+    for (int i = tid; i <= p.B; i += blockDim.x) {
+      s_cu[i] = p.cu_q[i];
+      if (i < p.B) s_kv[i] = p.kv_len[i];
     }
-  }
-  __syncthreads();
-  angles(s_row[0].pos, cs);
-  __syncthreads();
-  for (int i = 0, cur = 0, nxt = 1, aft = 2; t < p.T; ++i, t += step) {
-    const float* table = cs + (i & 1) * 2 * half;
-    if (works && t + step < p.T) fetch<T, VEC>(u, t + step, p, a2, b2);
-    if (t + step < p.T) angles(s_row[nxt].pos, cs + ((i + 1) & 1) * 2 * half);
-    if (meta && t + 2 * step < p.T) {
-      const Row r = row_of<kAppend>(t + 2 * step, p);
-      if ((tid & 31) == 0) s_row[aft] = r;
-    }
-    if (works) finish<T, VEC, kAppend>(u, t, s_row[cur], table, table + half, p, a, b);
     __syncthreads();
-    a = a2;
-    b = b2;
-    const int was = cur;
-    cur = nxt;
-    nxt = aft;
-    aft = was;
+  }
+  int parity = 0;
+  while (t < p.T) {
+    if (tid < kChunk)
+      s_row[tid] = row_of_thread<kAppend>(t + tid * step, small ? s_cu : p.cu_q,
+                                          small ? s_kv : p.kv_len, p);
+    __syncthreads();
+    angles(s_row[0].pos, cs + parity * 2 * half);
+    __syncthreads();
+    for (int j = 0; j < kChunk && t < p.T; ++j, t += step) {
+      const float* table = cs + parity * 2 * half;
+      parity ^= 1;
+      if (t + step < p.T) {
+        if (works) fetch<T, VEC>(u, t + step, p, a2, b2);
+        if (j + 1 < kChunk) angles(s_row[j + 1].pos, cs + parity * 2 * half);
+      }
+      if (works) finish<T, VEC, kInter, kAppend>(u, t, s_row[j], table, table + half, p, a, b);
+      __syncthreads();
+      a = a2;
+      b = b2;
+    }
   }
 }
 
@@ -348,10 +384,16 @@ medusa_status_t launch_vec(RopeParams& p, cudaStream_t stream) {
   const size_t table = (p.rot / 2) * sizeof(float);
   // resident blocks once they have several tokens each
   const int resident = 3 * device_sm_count();
-  if (work <= kRopeThreads && p.T >= 2 * resident)
-    launch(rope_pipe_kernel<T, VEC, kAppend>, resident, threads, 4 * table, stream, p);
-  else
-    launch(rope_block_kernel<T, VEC, kAppend>, p.T, threads, 2 * table, stream, p);
+  if (work <= kRopeThreads && p.T >= 2 * resident) {
+    if (p.interleaved)
+      launch(rope_pipe_kernel<T, VEC, true, kAppend>, resident, threads, 4 * table, stream, p);
+    else
+      launch(rope_pipe_kernel<T, VEC, false, kAppend>, resident, threads, 4 * table, stream, p);
+  } else if (p.interleaved) {
+    launch(rope_block_kernel<T, VEC, true, kAppend>, p.T, threads, 2 * table, stream, p);
+  } else {
+    launch(rope_block_kernel<T, VEC, false, kAppend>, p.T, threads, 2 * table, stream, p);
+  }
   return check_launch(kAppend ? "rope_append" : "rope");
 }
 
