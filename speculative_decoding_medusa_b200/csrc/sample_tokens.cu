@@ -50,8 +50,9 @@ constexpr int kMaxCluster = 8;
 // Top tokens looked for when only top_p bounds a row; a row whose top_k is at
 // most kTopWanted, or whose mass they reach, needs no histogram of its tokens.
 constexpr int kTopWanted = 256;
-constexpr int kRankBelow = 256;  // lists up to here are ranked by counting, not sorted
+constexpr int kRank = 128;  // tokens of a list that are ranked against one another
 constexpr size_t kManyBytes = 65536;  // of a row in a block when there are many rows
+constexpr int kValues = 4096;  // bins of bf16 logits: 16 octaves of magnitude and a sign
 constexpr int kExpTable = 256;
 constexpr float kMaxTemperature = 1e30f;  // 32 T must stay finite
 constexpr uint32_t kLowestKey = 0x00800000u;  // key of the lowest finite float
@@ -75,6 +76,11 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// the largest float below those of key k (-0 has the key of +0)
+__device__ __forceinline__ float value_below(uint32_t k) {
+  return value_of(k == 0x80000000u ? k - 2u : k - 1u);
+}
+
 // A finite float as a double by its bits; zero and subnormals become values
 // of that size (below 2^-126), which no logit difference notices.
 __device__ __forceinline__ double widen(float z) {
@@ -82,49 +88,53 @@ __device__ __forceinline__ double widen(float z) {
   return __hiloint2double(((b >> 3) & static_cast<int>(0x8fffffffu)) + 0x38000000, b << 29);
 }
 
+// NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The row is handled four tokens at a time: a Quad is what holds them.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
-  static constexpr int kVec = 4;
-  __device__ static void unpack(uint4 r, float (&z)[4]) {
+  using Quad = uint4;
+  static constexpr uint32_t kNegInf = 0xff800000u;  // filler word
+  __device__ static void unpack(Quad r, float (&z)[4]) {
     z[0] = __uint_as_float(r.x);
     z[1] = __uint_as_float(r.y);
     z[2] = __uint_as_float(r.z);
     z[3] = __uint_as_float(r.w);
   }
-  static constexpr uint32_t kNegInf = 0xff800000u;  // filler word
-  // NaN if any is
-  __device__ static float max2(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
+  __device__ static float max_of(Quad r) {
+    return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
+                   max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
-  __device__ static float max_of(uint4 r) {
-    return max2(max2(__uint_as_float(r.x), __uint_as_float(r.y)),
-                max2(__uint_as_float(r.z), __uint_as_float(r.w)));
-  }
+  __device__ static float max_of16(uint4 r) { return max_of(r); }
 };
 template <>
 struct Elem<__nv_bfloat16> {
-  static constexpr int kVec = 8;
-  __device__ static void unpack(uint4 r, float (&z)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[2 * i] = __uint_as_float(w[i] << 16);
-      z[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
+  using Quad = uint2;
   static constexpr uint32_t kNegInf = 0xff80ff80u;
+  __device__ static void unpack(Quad r, float (&z)[4]) {
+    z[0] = __uint_as_float(r.x << 16);
+    z[1] = __uint_as_float(r.x & 0xffff0000u);
+    z[2] = __uint_as_float(r.y << 16);
+    z[3] = __uint_as_float(r.y & 0xffff0000u);
+  }
   __device__ static uint32_t max2(uint32_t a, uint32_t b) {  // pairs
     uint32_t d;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
   }
-  __device__ static float max_of(uint4 r) {
-    const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
-    return Elem<float>::max2(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  __device__ static float max_of_pair(uint32_t m) {
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ static float max_of(Quad r) { return max_of_pair(max2(r.x, r.y)); }
+  __device__ static float max_of16(uint4 r) {
+    return max_of_pair(max2(max2(r.x, r.y), max2(r.z, r.w)));
   }
 };
 
@@ -178,36 +188,51 @@ struct Cut {
   int id;
 };
 
+// the cut among bf16 values
+struct ValueCut {
+  unsigned long long mass;  // of the tokens that stay
+  unsigned int count;       // of them
+  uint32_t bin;             // of the last
+  unsigned int ties;        // tokens of that value that stay,
+  unsigned int before;      // ... of them in the blocks before owner, whose tokens
+  int owner;                // of that value are the first that do not all stay
+};
+
 struct Shared {
   float hi[kMaxCluster];    // largest logit (NaN: there is one)
   float edge[kMaxCluster];  // a bound below the block's share of the top tokens
   Sums part[kMaxCluster];
   unsigned long long list_mass[kMaxCluster];  // weights of every token of the block
-  unsigned int list_n[kMaxCluster];
+  unsigned int list_n[kMaxCluster];  // tokens the block lists; bit 31: it filled its bins too
   uint32_t kmin[kMaxCluster], kmax[kMaxCluster];
   double table[kExpTable];
+  unsigned long long word[kRank], word_w[kRank];  // the last words of a list, their weights
+  uint32_t cnt[256], lo[256], high[256];          // narrowing a list
   Bin bin;
   Cut cut;
+  ValueCut value_cut;
+  unsigned long long tiny;  // bf16: weights of the tokens near zero
+  unsigned int far;         // finite tokens without weight or bin
   unsigned int n_local;
-  int cut_id;
+  int cut_id, n_th;
   unsigned long long red64[kWarps], red64b[kWarps];
   unsigned int red32[kWarps], red32b[kWarps];
-  float redf[kWarps];
+  float redf[kWarps], redg[kWarps];
 };
 
 // dynamic shared memory after the slice: histogram (counts, low and high words
-// of the mass; the sorted list lies over the mass words), short lists and
-// group sums of every block
+// of the mass), short lists and group sums of every block
 __host__ __device__ constexpr size_t sample_extra_smem(int C) {
+  static_assert(3 * kBins * 4 + kList * 8 >= 2 * kValues * 4, "weights of bf16 values");
   return 3 * kBins * 4 + kList * 8 + (size_t)C * kGroups * sizeof(Sums);
 }
-static_assert(kList * 8 <= 2 * kBins * 4, "sorted list over the mass words");
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int VE = Elem<T>::kVec;
+  constexpr int VE = 16 / sizeof(T);  // tokens of a 16-byte vector
+  using Quad = typename Elem<T>::Quad;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
@@ -216,12 +241,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 
   extern __shared__ __align__(16) uint8_t dyn[];
   uint4* slice = reinterpret_cast<uint4*>(dyn);
-  const int n_vec = p.slice / VE;
+  const Quad* quads = reinterpret_cast<const Quad*>(dyn);
+  const int n_vec = p.slice / VE, n_quad = p.slice / 4;
   // this block's histogram of its slice: counts, low and high words of the mass
   uint32_t* h_cnt = reinterpret_cast<uint32_t*>(dyn + (size_t)n_vec * 16);
   uint32_t* h_lo = h_cnt + kBins;
   uint32_t* h_hi = h_lo + kBins;
-  unsigned long long* sorted = reinterpret_cast<unsigned long long*>(h_lo);
   // the short lists: words of key and complemented id, cap from each block
   unsigned long long* list = reinterpret_cast<unsigned long long*>(h_hi + kBins);
   Sums* group = reinterpret_cast<Sums*>(list + kList);
@@ -281,14 +306,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         const int v = v0 + f * kThreads;
         if (v >= n_vec) break;
         slice[v] = raw[f];
-        hi = Elem<float>::max2(hi, Elem<T>::max_of(raw[f]));
+        hi = max_nan(hi, Elem<T>::max_of16(raw[f]));
       }
     }
   }
   if (tid >= n_vec && tid < kExpTable) sh.table[tid] = exp2((double)tid / kExpTable);
   const float own_hi = hi;  // the largest of this thread's tokens
   for (int o = 16; o > 0; o >>= 1)
-    hi = Elem<float>::max2(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   if (lane == 0) sh.redf[warp] = hi;
   __syncthreads();
   // The share-th largest of the block's threads' largest, to its top 16 bits
@@ -296,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // lie at or above the least of them, and not many more.
   const bool by_k = top_k > 1 && top_k < p.V;
   const bool by_p = top_p < 1.f;
-  const bool top_list = by_k ? top_k <= kTopWanted : by_p;
+  const bool top_list = sizeof(T) == 4 && (by_k ? top_k <= kTopWanted : by_p);
   float edge = -INFINITY;
   if (top_list) {
     const int want = by_k ? top_k : kTopWanted / 2;
@@ -310,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   }
   if (tid < C) {
     hi = sh.redf[0];
-    for (int w = 1; w < kWarps; ++w) hi = Elem<float>::max2(hi, sh.redf[w]);
+    for (int w = 1; w < kWarps; ++w) hi = max_nan(hi, sh.redf[w]);
     *cluster.map_shared_rank(&sh.hi[rank], tid) = hi;
     *cluster.map_shared_rank(&sh.edge[rank], tid) = edge;
   }
@@ -318,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   hi = sh.hi[0];
   edge = sh.edge[0];
   for (int c = 1; c < C; ++c) {
-    hi = Elem<float>::max2(hi, sh.hi[c]);
+    hi = max_nan(hi, sh.hi[c]);
     edge = fminf(edge, sh.edge[c]);
   }
   if (!(hi > -INFINITY && hi < INFINITY)) bad = true;  // NaN, +inf, or no finite logit
@@ -333,14 +358,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   if (temp == 0.f || top_k == 1) {
     // the lowest id of the largest
     int first = 0x7fffffff;
-    for (int v = tid; v < n_vec; v += kThreads) {
-      const uint4 raw = slice[v];
+    for (int v = tid; v < n_quad; v += kThreads) {
+      const Quad raw = quads[v];
       if (Elem<T>::max_of(raw) < hi) continue;
-      float z[VE];
+      float z[4];
       Elem<T>::unpack(raw, z);
 #pragma unroll
-      for (int i = VE - 1; i >= 0; --i)
-        if (z[i] == hi) first = min(first, base + v * VE + i);
+      for (int i = 3; i >= 0; --i)
+        if (z[i] == hi) first = min(first, base + v * 4 + i);
     }
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) sh.red32[warp] = static_cast<unsigned int>(first);
@@ -362,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // far below the distance to the next float under the largest counts as a
   // 64th of it (every other weight is zero either way).  With the lowest
   // float for the largest, T means nothing.
-  const float next = value_of(key_of(hi) - 1u);
+  const float next = value_below(key_of(hi));
   const double zmax = widen(hi);
   const double t_eff =
       fmax(key_of(hi) == kLowestKey ? 1.0 : (double)temp, (zmax - widen(next)) / 64.0);
@@ -376,131 +401,600 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return __float_as_uint(fminf((hi - z) * bin_scale, (float)(kBins - 1)) + 8388608.f) -
            0x4b000000u;
   };
-  auto clear_bins = [&]() {
-    for (int i = tid; i < kBins; i += kThreads) {
-      h_cnt[i] = 0u;
-      h_lo[i] = 0u;
-      h_hi[i] = 0u;
-    }
-    __syncthreads();
-  };
-  // weights to their bins: two 32-bit words with a carry (64-bit shared-memory
-  // additions measured 1.5 times slower)
-  auto add_mass4 = [&](const uint32_t (&bin)[4], const unsigned long long (&w)[4]) {
-    uint32_t old[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      old[i] = w[i] != 0ull ? atomicAdd(&h_lo[bin[i]], static_cast<uint32_t>(w[i])) : 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t wl = static_cast<uint32_t>(w[i]);
-      const uint32_t wh = static_cast<uint32_t>(w[i] >> 32) + (old[i] + wl < wl ? 1u : 0u);
-      if (wh != 0u) atomicAdd(&h_hi[bin[i]], wh);
-    }
-  };
-  // the sums of every group of 32 bins to every block
-  auto publish = [&]() {
-    __syncthreads();
-    for (int g = warp; g < kGroups; g += kWarps) {
-      const int bin = g * 32 + lane;
-      const unsigned int n = __reduce_add_sync(0xffffffffu, h_cnt[bin]);
-      unsigned long long m = (static_cast<unsigned long long>(h_hi[bin]) << 32) + h_lo[bin];
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (lane < C) *cluster.map_shared_rank(&group[rank * kGroups + g], lane) = Sums{m, n, 0};
-    }
-    cluster.sync();
-  };
-  // One histogram over the cluster: `pick(z, bin)` says whether a finite
-  // logit counts and in which bin.  Afterwards every block holds every
-  // block's sums of each group of 32 bins, and the blocks' own bins stay in
-  // place for find().
-  auto histogram = [&](bool counts, bool masses, auto pick) {
-    clear_bins();
-    for (int v = tid; v < n_vec; v += kThreads) {
-      float z[VE];
-      Elem<T>::unpack(slice[v], z);
-      // four independent weights at a time, then their additions
-#pragma unroll
-      for (int i0 = 0; i0 < VE; i0 += 4) {
-        uint32_t bin[4];
-        bool in[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) in[i] = z[i0 + i] > -INFINITY && pick(z[i0 + i], bin[i]);
-        if (masses) {
-          unsigned long long w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = in[i] ? weight(z[i0 + i]) : 0ull;
-          add_mass4(bin, w);
-        }
-        if (counts) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (in[i]) atomicAdd(&h_cnt[bin[i]], 1u);
-        }
-      }
-    }
-    publish();
+  // The tokens that a bound keeps end in a stretch of the order that is
+  // narrowed step by step: all of the row (kTop lists its top tokens, kRow puts
+  // them in bins), a bin (kIn lists it), and for a bin too full to be listed a
+  // finer histogram of its keys (kRange), until a list holds the stretch.
+  enum Stage { kTop, kRow, kIn, kRange };
+  int stage = top_list ? kTop : kRow;
+  bool by_mass = !by_k;  // the bound looked for; top_k's first
+  unsigned long long limit = by_k ? (unsigned long long)top_k : 0ull;  // 0: top_p of the row
+  Bin b{0ull, 0ull, 0u, 0u};  // what lies before the stretch
+  float below = edge > -INFINITY ? value_below(key_of(edge)) : edge, top = hi;
+  int only = -1;                  // the bin of level 0, if the stretch is one
+  uint32_t kmin = 0u, kmax = 0u;  // kRange: keys of the stretch, and its bins
+  int shift = 0;
+  auto within = [&](float z) {
+    return z > below && z <= top && (only < 0 || bin0(z) == static_cast<uint32_t>(only));
   };
 
-  // The last bin with tokens before which the count (or the mass) is below
-  // `limit`, given what lies before the histogram's range.  In mass mode
-  // limit 0 stands for top_p of the histogram's own total.
+  // where tokens go by id, warp w takes the quads [w * seg, (w + 1) * seg) of
+  // the slice, 32 at a time
+  const int seg = (n_quad + kWarps * 32 - 1) / (kWarps * 32) * 32;
+  const int v_begin = warp * seg, v_end = min(n_quad, v_begin + seg);
+
   auto p_limit = [&](unsigned long long total) {
     // kept while the mass before is below top_p * total: an integer limit
     return max(1ull, static_cast<unsigned long long>(ceil((double)top_p * (double)total)));
   };
-  auto find = [&](bool by_mass, unsigned long long limit, unsigned int count0,
-                  unsigned long long mass0) -> Bin {
+  // a warp's sum, and the block's from the warps'
+  auto warp_sum = [&](unsigned long long m) {
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    return m;
+  };
+  auto block_sum = [&](const unsigned long long* red) {
+    unsigned long long m = 0ull;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) m += red[w];
+    return m;
+  };
+
+  // inclusive sums over the lanes of a warp
+  auto scan = [&](unsigned long long& m, unsigned int& n) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long a = __shfl_up_sync(0xffffffffu, m, o);
+      const unsigned int c = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) {
+        m += a;
+        n += c;
+      }
+    }
+  };
+
+  // The id of the n-th of this block's tokens with logit z (there are as many).
+  // Ids rise with the quads' index, of which warps take contiguous runs.
+  auto nth_of = [&](float z, unsigned int n) -> int {
+    auto count = [&](int v) {
+      unsigned int c = 0u;  // one bit per token with the logit
+      if (v < v_end) {
+        float x[4];
+        Elem<T>::unpack(quads[v], x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c |= x[i] == z ? 1u << i : 0u;
+      }
+      return c;
+    };
+    unsigned int c = 0u, before = 0u;
+#pragma unroll 2
+    for (int v = v_begin + lane; v < v_end; v += 32) c += __popc(count(v));
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) sh.red32[warp] = c;
+    __syncthreads();
+#pragma unroll 1
+    for (int x = 0; x < warp; ++x) before += sh.red32[x];
+    if (before < n && before + c >= n) {
+#pragma unroll 1
+      for (int vv = v_begin; before < n && vv < v_end; vv += 32) {
+        const unsigned int bits = count(vv + lane), x = __popc(bits);
+        unsigned long long none = 0ull;
+        unsigned int s = x;
+        scan(none, s);
+        const unsigned int at = before + s - x;
+        if (at < n && at + x >= n) {
+          unsigned int left = bits;
+          for (unsigned int y = at + 1; y < n; ++y) left &= left - 1;
+          sh.n_th = base + (vv + lane) * 4 + __ffs(left) - 1;
+        }
+        before += __shfl_sync(0xffffffffu, s, 31);
+      }
+    }
+    __syncthreads();
+    return sh.n_th;
+  };
+
+  // ---- pieces of the draw ----
+  // larger keys stay, and ids up to cut_id of this one
+  uint32_t cut_key = kLowestKey;
+  int cut_id = 0x7fffffff;
+  auto take = [&](const Cut& c) {
+    if (c.key > cut_key || (c.key == cut_key && c.id < cut_id)) {
+      cut_key = c.key;
+      cut_id = c.id;
+    }
+  };
+  // min_p, w >= min_p: a bound on the logit, rounded up to a float
+  auto take_min_p = [&]() {
+    if (!(min_p > 0.f)) return;
+    const float z_min = __double2float_ru((double)hi + log((double)min_p) * (double)temp);
+    if (z_min > -INFINITY && key_of(z_min) > cut_key) {
+      cut_key = key_of(z_min);
+      cut_id = 0x7fffffff;
+    }
+  };
+  auto stays = [&](float z, int id) {
+    const float cut_z = value_of(cut_key);
+    return z > cut_z || (z == cut_z && id <= cut_id);
+  };
+  // this warp's tokens that stay, by a function for their weights
+  auto kept_of = [&](const auto& w_of) -> Sums {
+    unsigned long long mass = 0ull;
+    unsigned int count = 0u;
+    int first = 0x7fffffff;
+#pragma unroll 2
+    for (int v = v_begin + lane; v < v_end; v += 32) {
+      const Quad raw = quads[v];
+      if (Elem<T>::max_of(raw) < value_of(cut_key)) continue;
+      float z[4];
+      Elem<T>::unpack(raw, z);
+      bool in[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
+      if (in[0] || in[1] || in[2] || in[3]) {
+        // four independent weights, then the ones that stay
+        unsigned long long w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = w_of(z[i]);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (in[i]) {
+            mass += w[i];
+            ++count;
+            first = min(first, base + v * 4 + i);
+          }
+        }
+      }
+    }
+    return Sums{warp_sum(mass), __reduce_add_sync(0xffffffffu, count),
+                __reduce_min_sync(0xffffffffu, first)};
+  };
+  // the warps' sums, and with them the block's to every block
+  auto exchange = [&](const Sums& t) {
+    if (lane == 0) {
+      sh.red64[warp] = t.mass;
+      sh.red32[warp] = t.count;
+      sh.red32b[warp] = static_cast<unsigned int>(t.first);
+    }
+    __syncthreads();
+    if (tid < C) {
+      Sums t{0ull, 0u, 0x7fffffff};
+#pragma unroll 4
+      for (int w = 0; w < kWarps; ++w) {
+        t.mass += sh.red64[w];
+        t.count += sh.red32[w];
+        t.first = min(t.first, static_cast<int>(sh.red32b[w]));
+      }
+      *cluster.map_shared_rank(&sh.part[rank], tid) = t;
+    }
+    cluster.sync();
+  };
+  // the row's, and the mass in the blocks before this one
+  auto total_of = [&](unsigned long long& before) -> Sums {
+    Sums t{0ull, 0u, 0x7fffffff};
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) {
+      if (c == rank) before = t.mass;
+      t.mass += sh.part[c].mass;
+      t.count += sh.part[c].count;
+      t.first = min(t.first, sh.part[c].first);
+    }
+    return t;
+  };
+  auto target_of = [&](unsigned long long total) {
+    return min(static_cast<unsigned long long>((double)u * (double)total), total - 1);
+  };
+  // the token that holds the target, if this warp has it: `before` is the mass
+  // in front of the block, sh.red64 the warps'
+  auto pick = [&](const auto& w_of, unsigned long long target, unsigned long long before) {
+#pragma unroll 1
+    for (int w = 0; w < warp; ++w) before += sh.red64[w];
+    if (target < before || target >= before + sh.red64[warp]) return;
+#pragma unroll 1
+    for (int v0 = v_begin; v0 < v_end && target >= before; v0 += 32) {
+      const int v = v0 + lane;
+      unsigned long long w[4] = {0ull, 0ull, 0ull, 0ull};
+      if (v < v_end) {
+        float z[4];
+        Elem<T>::unpack(quads[v], z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = stays(z[i], base + v * 4 + i) ? w_of(z[i]) : 0ull;
+      }
+      const unsigned long long n = (w[0] + w[1]) + (w[2] + w[3]);
+      unsigned long long s = n;
+      unsigned int none = 0u;
+      scan(s, none);
+      unsigned long long at = before + s - n;
+      if (target >= at && target < at + n) {
+        int id = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (id < 0 && target < at + w[i]) id = base + v * 4 + i;
+          at += w[i];
+        }
+        p.tokens[r] = id;
+      }
+      before += __shfl_sync(0xffffffffu, s, 31);
+    }
+  };
+
+  // The group of bins that a bound falls in: the last with tokens before which
+  // the count (or the mass) is below the limit, of the given start.  In mass
+  // mode limit 0 stands for top_p of the histogram's own total.  One warp.
+  auto find_group = [&](bool by_mass, Bin b) -> Bin {
     static_assert(kGroups == 64, "two groups per lane");
-    if (warp == 0) {
-      Sums s[2];
-      for (int x = 0; x < 2; ++x) {
-        s[x] = Sums{0ull, 0u, 0};
+    Sums s[2];
+    for (int x = 0; x < 2; ++x) {
+      s[x] = Sums{0ull, 0u, 0};
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (c >= C) break;
+        const Sums t = group[c * kGroups + 2 * lane + x];
+        s[x].mass += t.mass;
+        s[x].count += t.count;
+      }
+    }
+    // exclusive prefix over the lanes
+    unsigned long long m = s[0].mass + s[1].mass;
+    unsigned int n = s[0].count + s[1].count;
+    const unsigned long long own_m = m;
+    const unsigned int own_n = n;
+    scan(m, n);
+    if (b.limit == 0ull) b.limit = p_limit(__shfl_sync(0xffffffffu, m, 31));
+    m += b.mass - own_m;
+    n += b.count - own_n;
+    // this lane's later qualifying group, if any
+    Bin g{0ull, b.limit, 0u, 0u};
+    bool some = false;
+    for (int x = 0; x < 2; ++x) {
+      if ((by_mass ? s[x].mass > 0ull : s[x].count > 0u) &&
+          (by_mass ? m : (unsigned long long)n) < b.limit) {
+        some = true;
+        g = Bin{m, b.limit, n, static_cast<uint32_t>(2 * lane + x)};
+      }
+      m += s[x].mass;
+      n += s[x].count;
+    }
+    const unsigned int votes = __ballot_sync(0xffffffffu, some);
+    const int from = 31 - __clz(votes);  // the first group of all always qualifies
+    return Bin{__shfl_sync(0xffffffffu, g.mass, from), b.limit,
+               __shfl_sync(0xffffffffu, g.count, from), __shfl_sync(0xffffffffu, g.bin, from)};
+  };
+
+  // ---- bf16: tokens counted by value ----
+  // Few values occur more than once each, so nothing is weighted token by
+  // token: a histogram counts every value of the 16 octaves up to the largest
+  // magnitude that has weight, in falling order (magnitudes below share one
+  // bin, with the sum of their weights), and 4096 weights serve the row.  The
+  // cut is then a value and how many of its tokens stay.  Where it falls among
+  // the magnitudes below, the row is cut as one in fp32 is.
+  if constexpr (sizeof(T) == 2) {
+    const int e = min(254, (__float_as_int(fmaxf(fabsf(hi), fabsf(weight.floor))) >> 23) & 255);
+    const int least = max(0, e - 15) << 7;  // magnitude bits of the shared bin's largest
+    constexpr int kHalf = kValues / 2, kTiny = kHalf - 1;
+    auto value = [&](int bin) {
+      const int sign = bin >> 11;
+      return __uint_as_float(static_cast<uint32_t>((bin ^ (kTiny + sign)) + least) << 16 |
+                             static_cast<uint32_t>(sign) << 31);
+    };
+    uint32_t* cnt = h_cnt;
+#pragma unroll
+    for (int i = 0; i < kValues / kThreads; ++i) cnt[i * kThreads + tid] = 0u;
+    if (tid == 0) {
+      sh.tiny = 0ull;
+      sh.far = 0u;
+    }
+    __syncthreads();
+    {
+      unsigned long long tiny = 0ull;
+      unsigned int n_tiny = 0u, far = 0u;
+#pragma unroll 2
+      for (int v = tid; v < n_vec; v += kThreads) {
+        const uint4 raw = slice[v];
+        const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t bits = i & 1 ? word[i / 2] >> 16 : word[i / 2] & 0xffffu;
+          const int mag = static_cast<int>(bits & 0x7fffu) - least;
+          if (mag > 0 && mag < kHalf) {
+            atomicAdd(&cnt[mag ^ (kTiny + (bits >> 15))], 1u);
+          } else if (mag <= 0) {
+            ++n_tiny;
+            tiny += weight(__uint_as_float(bits << 16));
+          } else if (bits != 0xff80u) {
+            ++far;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, n_tiny > 0u)) {
+        tiny = warp_sum(tiny);
+        n_tiny = __reduce_add_sync(0xffffffffu, n_tiny);
+        if (lane == 0) {
+          atomicAdd(&cnt[kTiny], n_tiny);
+          atomicAdd(&sh.tiny, tiny);
+        }
+      }
+      if (far > 0u) atomicAdd(&sh.far, far);
+    }
+    __syncthreads();
+    // the sums of every group of 64 bins to every block
+    auto mass_of = [&](int bin, uint32_t n) {
+      return bin == kTiny ? sh.tiny : n > 0u ? n * weight(value(bin)) : 0ull;
+    };
+#pragma unroll 2
+    for (int g = warp; g < kGroups; g += kWarps) {
+      const int bin = g * 64 + 2 * lane;
+      const uint2 n = *reinterpret_cast<const uint2*>(&cnt[bin]);
+      const unsigned long long m = warp_sum(mass_of(bin, n.x) + mass_of(bin + 1, n.y));
+      const unsigned int k = __reduce_add_sync(0xffffffffu, n.x + n.y);
+      if (lane < C) *cluster.map_shared_rank(&group[rank * kGroups + g], lane) = Sums{m, k, 0};
+    }
+    if (tid < C) {
+      *cluster.map_shared_rank(&sh.list_mass[rank], tid) = sh.tiny;
+      *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.far;
+    }
+    cluster.sync();
+    unsigned long long mass = 0ull;
+    unsigned int counted = 0u, far = 0u;
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) far += sh.list_n[c];
+#pragma unroll 1
+    for (int i = lane; i < C * kGroups; i += 32) {
+      mass += group[i].mass;
+      counted += group[i].count;
+    }
+    ValueCut cut{warp_sum(mass), __reduce_add_sync(0xffffffffu, counted) + far, kValues, 0u, 0u, C};
+    counted = cut.count - far;
+    bool exact = u > 0.f;
+    // the value and the tokens of it that a bound leaves
+    auto cut_at = [&](bool by_mass, unsigned long long limit) {
+      if (warp == 0) {
+        const Bin g = find_group(by_mass, Bin{0ull, limit, 0u, 0u});
+        const int bin = g.bin * 64 + 2 * lane;
+        uint2 n[kMaxCluster];  // all reads in flight
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          n[c] = c < C ? *reinterpret_cast<const uint2*>(&cluster.map_shared_rank(cnt, c)[bin])
+                       : make_uint2(0u, 0u);
+        unsigned long long tiny = 0ull;
+        uint2 s = make_uint2(0u, 0u);
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
-          if (c >= C) break;
-          const Sums t = group[c * kGroups + 2 * lane + x];
-          s[x].mass += t.mass;
-          s[x].count += t.count;
+          s.x += n[c].x;
+          s.y += n[c].y;
+        }
+        if (bin + 1 == kTiny) {
+#pragma unroll 1
+          for (int c = 0; c < C; ++c) tiny += sh.list_mass[c];
+        }
+        unsigned long long w[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) w[x] = weight(value(bin + x));
+        const unsigned long long m0 = s.x * w[0], m1 = bin + 1 == kTiny ? tiny : s.y * w[1];
+        unsigned long long m = m0 + m1;
+        unsigned int k = s.x + s.y;
+        scan(m, k);
+        m += g.mass - (m0 + m1);
+        k += g.count - (s.x + s.y);
+        const bool first = (by_mass ? m0 > 0ull : s.x > 0u) &&
+                           (by_mass ? m : (unsigned long long)k) < g.limit;
+        const bool second = (by_mass ? m1 > 0ull : s.y > 0u) &&
+                            (by_mass ? m + m0 : (unsigned long long)(k + s.x)) < g.limit;
+        const unsigned int votes = __ballot_sync(0xffffffffu, first || second);
+        if (lane == 31 - __clz(votes)) {
+          ValueCut c{};
+          c.bin = bin + (second ? 1 : 0);
+          const unsigned long long one = second ? w[1] : w[0];
+          if (second) {
+            m += m0;
+            k += s.x;
+          }
+          const unsigned int here = second ? s.y : s.x;
+          const unsigned long long room = g.limit - (by_mass ? m : (unsigned long long)k);
+          c.ties = static_cast<unsigned int>(
+              min((unsigned long long)here, by_mass && one > 0ull ? (room + one - 1) / one : room));
+          c.mass = m + c.ties * one;
+          c.count = k + c.ties;
+          c.owner = C;
+          bool found = false;
+#pragma unroll
+          for (int b = 0; b < kMaxCluster; ++b) {
+            const unsigned int y = second ? n[b].y : n[b].x;
+            if (!found && b < C && c.before + y > c.ties) {
+              found = true;
+              c.owner = b;
+            }
+            if (!found) c.before += y;
+          }
+          sh.value_cut = c;
         }
       }
-      // exclusive prefix over the lanes
-      unsigned long long m = s[0].mass + s[1].mass;
-      unsigned int n = s[0].count + s[1].count;
-      const unsigned long long own_m = m;
-      const unsigned int own_n = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long a = __shfl_up_sync(0xffffffffu, m, o);
-        const unsigned int b = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) {
-          m += a;
-          n += b;
+      __syncthreads();
+      const ValueCut c = sh.value_cut;
+      __syncthreads();
+      // (in the shared bin tokens are not alike)
+      exact = exact && c.bin != kTiny;
+      if (c.bin < cut.bin || (c.bin == cut.bin && c.ties < cut.ties)) cut = c;
+    };
+    if (exact && by_k) {
+      if ((unsigned int)top_k <= counted) cut_at(false, top_k);
+      else if (far > 0u) exact = false;  // a cut among tokens without weight
+    }
+    if (exact && by_p) cut_at(true, p_limit(cut.mass));
+    if (exact) {
+      if (cut.bin < kValues) cut_key = key_of(value(cut.bin));
+      take_min_p();
+      // whether all of the shared bin or nothing of it stays
+      const float z_tiny = __uint_as_float(static_cast<uint32_t>(least) << 16);
+      exact = !(fabsf(value_of(cut_key)) <= z_tiny);
+      // (a min_p below every weight that counts)
+      if (far > 0u && cut_key > kLowestKey && value_of(cut_key) < value(kValues - 1)) exact = false;
+    }
+    if (exact) {
+      const float cut_z = value_of(cut_key);
+      const bool split = cut.bin < kValues && key_of(value(cut.bin)) == cut_key;
+      if (split) cut_id = rank < cut.owner ? 0x7fffffff : -1;
+      // this block's tokens that stay
+      unsigned long long m = 0ull;
+      unsigned int k = 0u;
+#pragma unroll 2
+      for (int i = 0; i < kValues / kThreads; ++i) {
+        const int bin = i * kThreads + tid;
+        const float z = value(bin);
+        unsigned int n = cnt[bin];
+        if (split && z == cut_z)
+          n = rank < cut.owner ? n : rank == cut.owner ? cut.ties - cut.before : 0u;
+        else if (z < cut_z)
+          n = 0u;
+        if (n > 0u) {
+          m += mass_of(bin, n);
+          k += n;
         }
       }
-      if (limit == 0ull) limit = p_limit(__shfl_sync(0xffffffffu, m, 31));
-      m += mass0 - own_m;
-      n += count0 - own_n;
-      // this lane's later qualifying group, if any
-      int g = -1;
-      unsigned long long gm = 0ull;
-      unsigned int gn = 0u;
-      for (int x = 0; x < 2; ++x) {
-        const bool some = by_mass ? s[x].mass > 0ull : s[x].count > 0u;
-        if (some && (by_mass ? m : (unsigned long long)n) < limit) {
-          g = 2 * lane + x;
-          gm = m;
-          gn = n;
-        }
-        m += s[x].mass;
-        n += s[x].count;
+      exchange(Sums{warp_sum(m), __reduce_add_sync(0xffffffffu, k), 0});
+      unsigned long long before = 0ull;
+      const Sums all = total_of(before);
+      if (rank == 0 && tid == 0 && p.kept != nullptr)
+        p.kept[r] = static_cast<int>(all.count + (cut_key == kLowestKey ? far : 0u));
+      const unsigned long long target = target_of(all.mass);
+      if (target < before || target >= before + sh.part[rank].mass) return;
+      // This block draws.  Its counts make way for weights, which no other
+      // block reads any more.
+      uint32_t* w_lo = cnt;
+      uint32_t* w_hi = cnt + kValues;
+      if (split && rank == cut.owner)
+        cut_id = cut.ties > cut.before ? nth_of(cut_z, cut.ties - cut.before) : -1;
+#pragma unroll 2
+      for (int i = 0; i < kValues / kThreads; ++i) {
+        const int bin = i * kThreads + tid;
+        const unsigned long long w = cnt[bin] > 0u ? weight(value(bin)) : 0ull;
+        w_lo[bin] = static_cast<uint32_t>(w);
+        w_hi[bin] = static_cast<uint32_t>(w >> 32);
       }
-      const unsigned int votes = __ballot_sync(0xffffffffu, g >= 0);
-      const int from = 31 - __clz(votes);  // the first bin of all always qualifies
-      g = __shfl_sync(0xffffffffu, g, from);
-      gm = __shfl_sync(0xffffffffu, gm, from);
-      gn = __shfl_sync(0xffffffffu, gn, from);
+      __syncthreads();
+      auto looked_up = [&](float z) -> unsigned long long {
+        const uint32_t bits = __float_as_uint(z) >> 16;
+        const int mag = static_cast<int>(bits & 0x7fffu) - least;
+        if (mag <= 0) return weight(z);
+        if (mag >= kHalf) return 0ull;
+        const int bin = mag ^ (kTiny + (bits >> 15));
+        return static_cast<unsigned long long>(w_hi[bin]) << 32 | w_lo[bin];
+      };
+      const Sums own = kept_of(looked_up);
+      if (lane == 0) sh.red64[warp] = own.mass;
+      __syncthreads();
+      pick(looked_up, target, before);
+      return;
+    }
+    cut_key = kLowestKey;
+    cut_id = 0x7fffffff;
+    cluster.sync();  // bins and sums will be written again
+  }
+
+  // One pass over the slice: the tokens of the stretch onto the list of
+  // every block, weights (summed) and counts of tokens into their bins.
+  auto pass = [&](bool to_list, bool sum, bool mass_bins, bool count_bins) {
+    unsigned long long* mine = list + rank * cap;
+    const bool bins = mass_bins || count_bins, weights = sum || mass_bins;
+    if (tid == 0) sh.n_local = 0u;
+    if (bins) {
+#pragma unroll 1
+      for (int i = tid; i < 3 * kBins; i += kThreads) h_cnt[i] = 0u;
+    }
+    __syncthreads();
+    unsigned long long m = 0ull;
+#pragma unroll 1
+    for (int v = tid; v < n_quad; v += kThreads) {
+      const Quad raw = quads[v];
+      const bool listed = to_list && Elem<T>::max_of(raw) > below;
+      if (!listed && !weights && !bins) continue;
+      float z[4];
+      Elem<T>::unpack(raw, z);
+      uint32_t bin[4];
+      bool in[4];
+      if (bins) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bin[i] = bin0(z[i]);
+          in[i] = z[i] > -INFINITY;
+          if (stage == kRange) {
+            const uint32_t k = key_of(z[i]);
+            in[i] = k >= kmin && k <= kmax;
+            bin[i] = (kmax - k) >> shift;
+          }
+          if (count_bins && in[i]) atomicAdd(&h_cnt[bin[i]], 1u);
+        }
+      }
+      if (weights) {
+        // four independent weights, then their additions: two 32-bit words
+        // with a carry (64-bit shared-memory additions measured 1.5 times
+        // slower)
+        unsigned long long w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = weight(z[i]);
+        m += (w[0] + w[1]) + (w[2] + w[3]);
+        if (mass_bins) {
+          uint32_t old[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!in[i]) w[i] = 0ull;
+            old[i] = w[i] != 0ull ? atomicAdd(&h_lo[bin[i]], static_cast<uint32_t>(w[i])) : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t wl = static_cast<uint32_t>(w[i]);
+            const uint32_t wh = static_cast<uint32_t>(w[i] >> 32) + (old[i] + wl < wl ? 1u : 0u);
+            if (wh != 0u) atomicAdd(&h_hi[bin[i]], wh);
+          }
+        }
+      }
+      if (listed) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (within(z[i])) {
+            const unsigned int at = atomicAdd(&sh.n_local, 1u);
+            if (at < (unsigned int)cap)
+              mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
+                         (0xffffffffu - static_cast<uint32_t>(base + v * 4 + i));
+          }
+      }
+    }
+    if (sum) {
+      m = warp_sum(m);
+      if (lane == 0) sh.red64[warp] = m;
+    }
+    __syncthreads();
+    if (tid < C && to_list) {
+      *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local | (bins ? 0x80000000u : 0u);
+      *cluster.map_shared_rank(&sh.list_mass[rank], tid) = sum ? block_sum(sh.red64) : 0ull;
+    }
+    if (to_list) {
+      const int n_mine = static_cast<int>(min(sh.n_local, (unsigned int)cap));
+      // thread e: entry e / C for block e % C
+#pragma unroll 1
+      for (int e = tid; e < n_mine * C; e += kThreads)
+        if (e % C != rank) *cluster.map_shared_rank(&mine[e / C], e % C) = mine[e / C];
+    }
+    if (bins) {
+      // the sums of every group of 32 bins to every block
+#pragma unroll 1
+      for (int g = warp; g < kGroups; g += kWarps) {
+        const int bin = g * 32 + lane;
+        const unsigned int n = __reduce_add_sync(0xffffffffu, h_cnt[bin]);
+        const unsigned long long s =
+            warp_sum((static_cast<unsigned long long>(h_hi[bin]) << 32) + h_lo[bin]);
+        if (lane < C) *cluster.map_shared_rank(&group[rank * kGroups + g], lane) = Sums{s, n, 0};
+      }
+    }
+    cluster.sync();
+  };
+
+  // the bin that a bound falls in, likewise
+  auto find = [&](bool by_mass, Bin before) -> Bin {
+    if (warp == 0) {
+      const Bin g = find_group(by_mass, before);
       // its 32 bins over the cluster
-      const int bin = g * 32 + lane;
+      const int bin = g.bin * 32 + lane;
       uint32_t rn[kMaxCluster], rl[kMaxCluster], rh[kMaxCluster];  // all reads in flight
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
@@ -508,8 +1002,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         rl[c] = c < C ? cluster.map_shared_rank(h_lo, c)[bin] : 0u;
         rh[c] = c < C ? cluster.map_shared_rank(h_hi, c)[bin] : 0u;
       }
-      m = 0ull;
-      n = 0u;
+      unsigned long long m = 0ull;
+      unsigned int n = 0u;
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
         m += (static_cast<unsigned long long>(rh[c]) << 32) + rl[c];
@@ -518,19 +1012,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       const bool some = by_mass ? m > 0ull : n > 0u;
       const unsigned long long bm = m;
       const unsigned int bn = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long a = __shfl_up_sync(0xffffffffu, m, o);
-        const unsigned int b = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) {
-          m += a;
-          n += b;
-        }
-      }
-      m += gm - bm;
-      n += gn - bn;
-      const bool in = some && (by_mass ? m : (unsigned long long)n) < limit;
+      scan(m, n);
+      m += g.mass - bm;
+      n += g.count - bn;
+      const bool in = some && (by_mass ? m : (unsigned long long)n) < g.limit;
       const unsigned int bins = __ballot_sync(0xffffffffu, in);
-      if (lane == 31 - __clz(bins)) sh.bin = Bin{m, limit, n, static_cast<uint32_t>(bin)};
+      if (lane == 31 - __clz(bins)) sh.bin = Bin{m, g.limit, n, static_cast<uint32_t>(bin)};
     }
     __syncthreads();
     const Bin b = sh.bin;
@@ -538,669 +1025,361 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return b;
   };
 
-  // tokens of one key, n of them with weight w each, that stay
-  auto ties_kept = [&](bool by_mass, unsigned long long limit, unsigned int count,
-                       unsigned long long mass, unsigned int n, unsigned long long w) {
-    if (!by_mass) return static_cast<unsigned int>(min((unsigned long long)n, limit - count));
-    if (w == 0ull) return n;
-    return static_cast<unsigned int>(min((unsigned long long)n, (limit - mass + w - 1) / w));
-  };
 
-  // The tokens for which in(z) holds onto the short list of every block
-  // (none(m): no token of a vector whose largest is m); with `masses` also the
-  // weights of all tokens, with `bins` these into their bins.  False when a
-  // block has too many; n: their number.
-  auto gather = [&](auto in, auto none, bool masses, bool bins, unsigned int& n,
-                    unsigned long long& mass) -> bool {
-    unsigned long long* mine = list + rank * cap;
-    if (tid == 0) sh.n_local = 0u;
-    if (bins) clear_bins();
-    __syncthreads();
-    unsigned long long m = 0ull;
-    for (int v = tid; v < n_vec; v += kThreads) {
-      const uint4 raw = slice[v];
-      const bool skip = none(Elem<T>::max_of(raw));
-      if (skip && !masses) continue;
-      float z[VE];
-      Elem<T>::unpack(raw, z);
-      if (masses) {
-#pragma unroll
-        for (int i0 = 0; i0 < VE; i0 += 4) {
-          unsigned long long w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
-          m += (w[0] + w[1]) + (w[2] + w[3]);
-          if (bins) {
-            const uint32_t bin[4] = {bin0(z[i0]), bin0(z[i0 + 1]), bin0(z[i0 + 2]),
-                                     bin0(z[i0 + 3])};
-            add_mass4(bin, w);
-          }
-        }
-      }
-      if (!skip) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (in(z[i])) {
-            const unsigned int at = atomicAdd(&sh.n_local, 1u);
-            if (at < (unsigned int)cap)
-              mine[at] = (static_cast<unsigned long long>(key_of(z[i])) << 32) |
-                         (0xffffffffu - static_cast<uint32_t>(base + v * VE + i));
-          }
-      }
-    }
-    if (masses) {
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (lane == 0) sh.red64[warp] = m;
-    }
-    __syncthreads();
-    if (tid < C) {
-      *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local;
-      m = 0ull;
-      if (masses)
-        for (int w = 0; w < kWarps; ++w) m += sh.red64[w];
-      *cluster.map_shared_rank(&sh.list_mass[rank], tid) = m;
-    }
-    const int n_mine = static_cast<int>(min(sh.n_local, (unsigned int)cap));
-    for (int e = tid; e < n_mine * C; e += kThreads) {
-      const int c = e / n_mine, i = e - c * n_mine;
-      if (c != rank) *cluster.map_shared_rank(&mine[i], c) = mine[i];
-    }
-    cluster.sync();
-    bool fits = true;
-    n = 0u;
-    mass = 0ull;
-    for (int c = 0; c < C; ++c) {
-      fits = fits && sh.list_n[c] <= (unsigned int)cap;
-      n += sh.list_n[c];
-      mass += sh.list_mass[c];
-    }
-    return fits;
-  };
-
-  // The lists as one array in the order of the tokens, largest first, and the
-  // mass before the thread's two words 2 tid and 2 tid + 1 in it (given what
-  // lies before the list).  A long list goes through a bitonic network: thread
-  // t holds word t (and t + kThreads when there are more), exchanged by
-  // shuffles, and through shared memory for distances of a warp or more.
-  bool dirty = false;  // the histogram has been written over
-  // the thread's words of the lists and their places in one array (-1: none)
-  auto list_words = [&](unsigned long long (&e)[2], int (&at)[2]) {
+  // The cut among the n listed tokens, which lie after b.count tokens of mass
+  // b.mass: the last before which the count (or the mass) is below b.limit.
+  // A thread holds up to two of the list's words (key and complemented id, so
+  // that larger words come first).  While more than kRank are left, those of
+  // the 256th of their range that holds the cut; the rest rank by counting the
+  // larger ones and adding up their weights.
+  auto list_cut = [&](Bin b, unsigned int n) -> Cut {
+    unsigned long long e[2], w[2];
+    bool alive[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int c = (tid + x * kThreads) / cap, i = (tid + x * kThreads) - c * cap;
-      at[x] = -1;
-      e[x] = 0ull;
-      if (c < C && i < (int)sh.list_n[c]) {
-        at[x] = i;
-        for (int o = 0; o < c; ++o) at[x] += sh.list_n[o];
-        e[x] = list[tid + x * kThreads];
-      }
+      alive[x] = c < C && i < (int)(sh.list_n[c] & 0x7fffffffu);
+      e[x] = alive[x] ? list[tid + x * kThreads] : 0ull;
     }
-  };
-  // Of the listed n tokens of bin b (which lie after b.count tokens of mass
-  // b.mass), those of the 256th of their key range that holds the cut, into
-  // the array, unsorted: n and what lies before them are updated.
-  auto narrow = [&](bool by_mass, Bin& b, unsigned int& n) {
-    dirty = true;
-    uint32_t* cnt = reinterpret_cast<uint32_t*>(sorted + kList);  // beside the array
-    uint32_t *lo = cnt + 256, *high = lo + 256;
-    unsigned long long e[2];
-    int at[2];
-    list_words(e, at);
-    uint32_t kmin = 0xffffffffu, kmax = 0u;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (at[x] >= 0) {
-        kmin = min(kmin, static_cast<uint32_t>(e[x] >> 32));
-        kmax = max(kmax, static_cast<uint32_t>(e[x] >> 32));
-      }
-    kmin = __reduce_min_sync(0xffffffffu, kmin);
-    kmax = __reduce_max_sync(0xffffffffu, kmax);
-    if (lane == 0) {
-      sh.red32[warp] = kmin;
-      sh.red32b[warp] = kmax;
-    }
-    for (int i = tid; i < 3 * 256; i += kThreads) cnt[i] = 0u;
-    if (tid == 0) sh.n_local = 0u;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      kmin = min(kmin, sh.red32[w]);
-      kmax = max(kmax, sh.red32b[w]);
-    }
-    int shift = 0;
-    while (((kmax - kmin) >> shift) >= 256u) ++shift;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (at[x] >= 0) {
-        const uint32_t key = static_cast<uint32_t>(e[x] >> 32), bin = (kmax - key) >> shift;
-        atomicAdd(&cnt[bin], 1u);
-        if (by_p) {
-          const unsigned long long w = weight(value_of(key));
-          const uint32_t wl = static_cast<uint32_t>(w);
-          const uint32_t wh =
-              static_cast<uint32_t>(w >> 32) + (atomicAdd(&lo[bin], wl) + wl < wl ? 1u : 0u);
-          if (wh != 0u) atomicAdd(&high[bin], wh);
-        }
-      }
-    __syncthreads();
-    if (warp == 0) {
-      // eight bins a lane
-      unsigned int c = 0u;
-      unsigned long long m = 0ull;
-      for (int i = 8 * lane; i < 8 * lane + 8; ++i) {
-        c += cnt[i];
-        m += (static_cast<unsigned long long>(high[i]) << 32) + lo[i];
-      }
-      unsigned int sc = c;
-      unsigned long long sm = m;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned int a = __shfl_up_sync(0xffffffffu, sc, o);
-        const unsigned long long d = __shfl_up_sync(0xffffffffu, sm, o);
-        if (lane >= o) {
-          sc += a;
-          sm += d;
-        }
-      }
-      sc += b.count - c;
-      sm += b.mass - m;
-      Bin f{};
-      bool some = false;
-      for (int i = 8 * lane; i < 8 * lane + 8; ++i) {
-        if (cnt[i] > 0u && (by_mass ? sm : (unsigned long long)sc) < b.limit) {
-          some = true;
-          f = Bin{sm, b.limit, sc, static_cast<uint32_t>(i)};
-        }
-        sc += cnt[i];
-        sm += (static_cast<unsigned long long>(high[i]) << 32) + lo[i];
-      }
-      const unsigned int votes = __ballot_sync(0xffffffffu, some);
-      if (lane == 31 - __clz(votes)) sh.bin = f;
-    }
-    __syncthreads();
-    b = sh.bin;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (at[x] >= 0 && (kmax - static_cast<uint32_t>(e[x] >> 32)) >> shift == b.bin)
-        sorted[atomicAdd(&sh.n_local, 1u)] = e[x];
-    __syncthreads();
-    n = sh.n_local;
-  };
-  // listed: the words are the lists' (otherwise the array's first n)
-  auto sort_list = [&](bool listed, unsigned int n, unsigned long long mass0, bool masses,
-                       unsigned long long (&w)[2]) -> unsigned long long {
-    dirty = true;
-    unsigned long long e[2];
-    int at[2];
-    if (listed) {
-      list_words(e, at);
+    w[0] = w[1] = 0ull;
+    if (by_p) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        if (at[x] >= 0) sorted[at[x]] = e[x];
-    } else {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        at[x] = tid + x * kThreads < (int)n ? tid + x * kThreads : -1;
-        e[x] = at[x] >= 0 ? sorted[at[x]] : 0ull;
-      }
+        if (alive[x]) w[x] = weight(value_of(static_cast<uint32_t>(e[x] >> 32)));
     }
-    if (n <= kRankBelow) {
-      // short: every word's rank by counting the larger ones
-      __syncthreads();
-      int rk[2] = {0, 0};
-      if (__any_sync(0xffffffffu, at[0] >= 0 || at[1] >= 0)) {
-#pragma unroll 4
-        for (int i = 0; i < (int)n; ++i) {
-          const unsigned long long o = sorted[i];
-          rk[0] += o > e[0] ? 1 : 0;
-          rk[1] += o > e[1] ? 1 : 0;
-        }
-      }
-      __syncthreads();
+#pragma unroll 1
+    while (n > (unsigned int)kRank) {
+      unsigned long long least = ~0ull, most = 0ull;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        if (at[x] >= 0) sorted[rk[x]] = e[x];
+        if (alive[x]) {
+          least = min(least, e[x]);
+          most = max(most, e[x]);
+        }
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) {
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      }
+      if (lane == 0) {
+        sh.red64[warp] = least;
+        sh.red64b[warp] = most;
+      }
+      if (tid < 256) sh.cnt[tid] = sh.lo[tid] = sh.high[tid] = 0u;
       __syncthreads();
-    } else {
-      int size = 32;
-      while (size < (int)n) size <<= 1;
-      for (int i = n + tid; i < size; i += kThreads) sorted[i] = 0ull;
+#pragma unroll 1
+      for (int x = 0; x < kWarps; ++x) {
+        least = min(least, sh.red64[x]);
+        most = max(most, sh.red64b[x]);
+      }
+      // words are distinct: the range is above zero and shrinks 128-fold a turn
+      const int sh_r = max(0, 64 - __clzll(static_cast<long long>(most - least)) - 8);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (alive[x]) {
+          const uint32_t bin = static_cast<uint32_t>((most - e[x]) >> sh_r);
+          atomicAdd(&sh.cnt[bin], 1u);
+          const uint32_t wl = static_cast<uint32_t>(w[x]);
+          uint32_t wh = static_cast<uint32_t>(w[x] >> 32);
+          if (wl != 0u && atomicAdd(&sh.lo[bin], wl) + wl < wl) ++wh;
+          if (wh != 0u) atomicAdd(&sh.high[bin], wh);
+        }
       __syncthreads();
-      const bool wide = size > kThreads;
-      const bool act = warp * 32 < size;
-      unsigned long long e0 = act ? sorted[tid] : 0ull;
-      unsigned long long e1 = wide ? sorted[tid + kThreads] : 0ull;
-      auto keep = [&](unsigned long long mine, unsigned long long other, int x, int k, int j) {
-        const bool larger = ((x & j) == 0) == ((x & k) == 0);
-        return (mine > other) == larger ? mine : other;
-      };
-      for (int k = 2; k <= size; k <<= 1) {
-        for (int j = k >> 1; j > 0; j >>= 1) {
-          if (j == kThreads) {  // the thread's own two words
-            const unsigned long long a = keep(e0, e1, tid, k, j);
-            e1 = keep(e1, e0, tid + kThreads, k, j);
-            e0 = a;
-          } else if (j >= 32) {
-            __syncthreads();
-            if (act) sorted[tid] = e0;
-            if (wide) sorted[tid + kThreads] = e1;
-            __syncthreads();
-            if (act) e0 = keep(e0, sorted[tid ^ j], tid, k, j);
-            if (wide) e1 = keep(e1, sorted[(tid + kThreads) ^ j], tid + kThreads, k, j);
-          } else if (act) {
-            e0 = keep(e0, __shfl_xor_sync(0xffffffffu, e0, j), tid, k, j);
-            if (wide) e1 = keep(e1, __shfl_xor_sync(0xffffffffu, e1, j), tid + kThreads, k, j);
+      if (warp == 0) {
+        // eight bins a lane
+        unsigned int c = 0u;
+        unsigned long long m = 0ull;
+#pragma unroll 1
+        for (int i = 8 * lane; i < 8 * lane + 8; ++i) {
+          c += sh.cnt[i];
+          m += (static_cast<unsigned long long>(sh.high[i]) << 32) + sh.lo[i];
+        }
+        unsigned int sc = c;
+        unsigned long long sm = m;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned int y = __shfl_up_sync(0xffffffffu, sc, o);
+          const unsigned long long d = __shfl_up_sync(0xffffffffu, sm, o);
+          if (lane >= o) {
+            sc += y;
+            sm += d;
           }
         }
+        sc += b.count - c;
+        sm += b.mass - m;
+        Bin f{};
+        bool some = false;
+#pragma unroll 1
+        for (int i = 8 * lane; i < 8 * lane + 8; ++i) {
+          if (sh.cnt[i] > 0u && (by_mass ? sm : (unsigned long long)sc) < b.limit) {
+            some = true;
+            f = Bin{sm, b.limit, sc, static_cast<uint32_t>(i)};
+          }
+          sc += sh.cnt[i];
+          sm += (static_cast<unsigned long long>(sh.high[i]) << 32) + sh.lo[i];
+        }
+        const unsigned int votes = __ballot_sync(0xffffffffu, some);
+        if (lane == 31 - __clz(votes)) sh.bin = f;
       }
       __syncthreads();
-      if (act) sorted[tid] = e0;
-      if (wide) sorted[tid + kThreads] = e1;
+      b = sh.bin;
+      n = sh.cnt[b.bin];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        alive[x] = alive[x] && static_cast<uint32_t>((most - e[x]) >> sh_r) == b.bin;
       __syncthreads();
     }
+    if (tid == 0) {
+      sh.n_local = 0u;
+      sh.red32[0] = 0u;
+    }
+    __syncthreads();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-      w[x] = masses && 2 * tid + x < (int)n
-                 ? weight(value_of(static_cast<uint32_t>(sorted[2 * tid + x] >> 32)))
-                 : 0ull;
-    unsigned long long m = w[0] + w[1];
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, m, o);
-      if (lane >= o) m += y;
-    }
-    if (lane == 31) sh.red64[warp] = m;
-    __syncthreads();
-    m += mass0 - w[0] - w[1];
-    for (int x = 0; x < warp; ++x) m += sh.red64[x];
-    return m;
-  };
-  // the last of the sorted words for which stay(i, mass before) holds
-  auto last_of = [&](unsigned int n, unsigned long long before,
-                     const unsigned long long (&w)[2], auto stay) -> Cut {
-    int last = -1;
-    unsigned long long mass = 0ull;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int i = 2 * tid + x;
-      if (i < (int)n && stay(i, before)) {
-        last = i;
-        mass = before + w[x];
+      if (alive[x]) {
+        const unsigned int at = atomicAdd(&sh.n_local, 1u);
+        sh.word[at] = e[x];
+        sh.word_w[at] = w[x];
       }
-      before += w[x];
-    }
-    const unsigned int votes = __ballot_sync(0xffffffffu, last >= 0);
-    if (votes != 0u && lane == 31 - __clz(votes)) sh.red32[warp] = last + 1;
-    if (votes == 0u && lane == 0) sh.red32[warp] = 0u;
     __syncthreads();
-    unsigned int best = 0u;
-    for (int x = 0; x < kWarps; ++x) best = max(best, sh.red32[x]);
-    if (last >= 0 && (unsigned int)last + 1u == best) {
-      const unsigned long long e = sorted[last];
-      sh.cut = Cut{mass, static_cast<uint32_t>(e >> 32),
-                   static_cast<int>(0xffffffffu - static_cast<uint32_t>(e))};
+    // four threads to a word, each over a quarter of the others
+    static_assert(4 * kRank <= kThreads, "");
+    const int at = tid / 4;
+    unsigned int rk = 0u;
+    unsigned long long m = 0ull;
+    bool stays = false;
+    const unsigned long long own = at < (int)n ? sh.word[at] : 0ull;
+    if (warp * 8 < (int)n) {
+#pragma unroll 4
+      for (int i = tid % 4; i < (int)n; i += 4)
+        if (sh.word[i] > own) {
+          ++rk;
+          m += sh.word_w[i];
+        }
+      for (int o = 1; o < 4; o *= 2) {
+        rk += __shfl_xor_sync(0xffffffffu, rk, o);
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+      }
+      m += b.mass;
+      stays = at < (int)n && (by_mass ? m : (unsigned long long)b.count + rk) < b.limit;
+      if (stays) atomicMax(&sh.red32[0], rk + 1u);
     }
+    __syncthreads();
+    if (stays && sh.red32[0] == rk + 1u)
+      sh.cut = Cut{m + sh.word_w[at], static_cast<uint32_t>(own >> 32),
+                   static_cast<int>(0xffffffffu - static_cast<uint32_t>(own))};
     __syncthreads();
     const Cut cut = sh.cut;
     __syncthreads();
     return cut;
   };
 
-  // The cut among the n listed tokens, which lie after b.count tokens of mass
-  // b.mass: the last before which the count (or the mass) is below b.limit.
-  auto list_cut = [&](bool by_mass, Bin b, unsigned int n) -> Cut {
-    const bool many = n > kRankBelow / 4;
-    if (many) narrow(by_mass, b, n);
-    unsigned long long w[2];
-    const unsigned long long m = sort_list(!many, n, b.mass, by_p, w);
-    return last_of(n, m, w, [&](int i, unsigned long long before) {
-      return (by_mass ? before : (unsigned long long)b.count + i) < b.limit;
-    });
-  };
-
-  // The exact cut inside bin b of the current histogram.
-  auto resolve = [&](bool by_mass, Bin b, bool again) -> Cut {
-    const unsigned long long limit = b.limit;
-    bool level0 = true;
-    float below = 0.f, top = 0.f;  // the bin's tokens: below < z <= top (levels >= 1)
-    for (;;) {
-      auto in_bin = [&](float z) {
-        if (level0) return z > -INFINITY && bin0(z) == b.bin;
-        return z > below && z <= top;
-      };
-      auto none = [&](float m) { return level0 ? bin0(m) > b.bin : !(m > below); };
-      unsigned int n;
-      unsigned long long unused;
-      if (gather(in_bin, none, false, false, n, unused)) {
-        const Cut cut = list_cut(by_mass, b, n);
-        if (again) cluster.sync();  // the lists will be written again
-        return cut;
+  // ---- the cut ----
+#pragma unroll 1
+  while (by_k || by_p) {
+    bool sum = false, mass_bins = false;
+    if (stage == kTop && !by_k) {
+      // Whether the top tokens reach top_p is guessed from the block's threads'
+      // largest: when those above the edge are short of top_p of all, the
+      // weights go into their bins in the same pass.
+      sum = true;
+      const float w = own_hi > -INFINITY ? exp2f((own_hi - hi) * (float)(weight.c / kExpTable)) : 0.f;
+      float some = own_hi > below ? w : 0.f, whole = w;
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) {
+        some += __shfl_xor_sync(0xffffffffu, some, o);
+        whole += __shfl_xor_sync(0xffffffffu, whole, o);
       }
-      // a crowded bin: its key range
-      uint32_t kmin = 0xffffffffu, kmax = 0u;
-      for (int v = tid; v < n_vec; v += kThreads) {
-        float z[VE];
-        Elem<T>::unpack(slice[v], z);
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (in_bin(z[i])) {
-            const uint32_t k = key_of(z[i]);
-            kmin = min(kmin, k);
-            kmax = max(kmax, k);
-          }
-      }
-      kmin = __reduce_min_sync(0xffffffffu, kmin);
-      kmax = __reduce_max_sync(0xffffffffu, kmax);
       if (lane == 0) {
-        sh.red32[warp] = kmin;
-        sh.red32b[warp] = kmax;
+        sh.redf[warp] = some;
+        sh.redg[warp] = whole;
       }
       __syncthreads();
-      if (tid < C) {
-        for (int w = 0; w < kWarps; ++w) {
-          kmin = min(kmin, sh.red32[w]);
-          kmax = max(kmax, sh.red32b[w]);
-        }
-        *cluster.map_shared_rank(&sh.kmin[rank], tid) = kmin;
-        *cluster.map_shared_rank(&sh.kmax[rank], tid) = kmax;
+      some = whole = 0.f;
+#pragma unroll 1
+      for (int x = 0; x < kWarps; ++x) {
+        some += sh.redf[x];
+        whole += sh.redg[x];
       }
-      cluster.sync();
-      kmin = 0xffffffffu;
-      kmax = 0u;
+      mass_bins = some < top_p * whole;
+    } else if (stage == kRow || stage == kRange) {
+      mass_bins = by_p;
+    }
+    const bool to_list = stage == kTop || stage == kIn;
+    pass(to_list, sum, mass_bins, stage == kRange || (stage == kRow && by_k));
+
+    bool in_bins = !to_list;  // the stretch's tokens are in bins: find the one
+    if (to_list) {
+      unsigned int n = 0u;
+      unsigned long long total = 0ull;
+      bool fits = true, binned = true;
+#pragma unroll 1
       for (int c = 0; c < C; ++c) {
-        kmin = min(kmin, sh.kmin[c]);
-        kmax = max(kmax, sh.kmax[c]);
+        const unsigned int k = sh.list_n[c] & 0x7fffffffu;
+        fits = fits && k <= (unsigned int)cap;
+        binned = binned && sh.list_n[c] != k;
+        n += k;
+        total += sh.list_mass[c];
       }
-      if (kmin == kmax) {
-        // one key: the id of the last of its tokens that stay, by counting
+      if (stage == kTop && !by_k) {
+        limit = p_limit(total);
+        if (fits) {
+          // the list serves if its mass reaches the limit
+          unsigned long long m = 0ull;
+#pragma unroll 1
+          for (int e = tid; e < kList; e += kThreads)
+            if (e % cap < (int)(sh.list_n[e / cap] & 0x7fffffffu))
+              m += weight(value_of(static_cast<uint32_t>(list[e] >> 32)));
+          m = warp_sum(m);
+          if (lane == 0) sh.red64[warp] = m;
+          __syncthreads();
+          fits = block_sum(sh.red64) >= limit;
+          __syncthreads();
+        }
+      }
+      Cut cut{};
+      bool done = fits;
+      if (fits) {
+        b.limit = limit;
+        cut = list_cut(b, n);
+        if (stage == kTop && by_k && by_p) {
+          // the same list again for top_p of what top_k leaves
+          take(cut);
+          by_mass = true;
+          b.limit = limit = p_limit(cut.mass);
+          cut = list_cut(b, n);
+        }
+      } else if (stage == kTop) {
+        if (by_k || !binned) stage = kRow;
+        else in_bins = true;  // every block has filled its bins
+        b = Bin{0ull, 0ull, 0u, 0u};
+        cluster.sync();  // lists and bins will be written again
+        if (!in_bins) continue;
+        stage = kRow;
+      } else {
+        // a crowded bin: its key range
+        kmin = 0xffffffffu;
+        kmax = 0u;
+#pragma unroll 1
+        for (int v = tid; v < n_quad; v += kThreads) {
+          float z[4];
+          Elem<T>::unpack(quads[v], z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (within(z[i])) {
+              const uint32_t k = key_of(z[i]);
+              kmin = min(kmin, k);
+              kmax = max(kmax, k);
+            }
+        }
+        kmin = __reduce_min_sync(0xffffffffu, kmin);
+        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        if (lane == 0) {
+          sh.red32[warp] = kmin;
+          sh.red32b[warp] = kmax;
+        }
+        __syncthreads();
+        if (tid < C) {
+#pragma unroll 1
+          for (int w = 0; w < kWarps; ++w) {
+            kmin = min(kmin, sh.red32[w]);
+            kmax = max(kmax, sh.red32b[w]);
+          }
+          *cluster.map_shared_rank(&sh.kmin[rank], tid) = kmin;
+          *cluster.map_shared_rank(&sh.kmax[rank], tid) = kmax;
+        }
+        cluster.sync();
+        kmin = 0xffffffffu;
+        kmax = 0u;
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+          kmin = min(kmin, sh.kmin[c]);
+          kmax = max(kmax, sh.kmax[c]);
+        }
+        if (kmin < kmax) {
+          shift = max(0, 32 - __clz(static_cast<int>(kmax - kmin)) - 11);
+          stage = kRange;
+          continue;
+        }
+        // one key: how many of its tokens stay, and the last of them
         const unsigned long long w = weight(value_of(kmin));
-        const unsigned int m = ties_kept(by_mass, limit, b.count, b.mass, n, w);
+        const unsigned long long room = limit - (by_mass ? b.mass : (unsigned long long)b.count);
+        const unsigned int m = static_cast<unsigned int>(
+            min((unsigned long long)n, !by_mass ? room : w == 0ull ? n : (room + w - 1) / w));
         unsigned int before = 0u;
         int owner = 0;
-        for (int c = 0; c < C; ++c) {
-          if (before + sh.list_n[c] >= m) break;
+#pragma unroll 1
+        for (int c = 0; c < C && before + sh.list_n[c] < m; ++c) {
           before += sh.list_n[c];
           ++owner;
         }
         if (rank == owner) {
-          // ids rise with the vector index: warps take contiguous runs of it
-          const int seg = (n_vec + kWarps * 32 - 1) / (kWarps * 32) * 32;
-          const int v0 = warp * seg, v1 = min(n_vec, v0 + seg);
-          auto count = [&](int v, float (&z)[VE]) {
-            unsigned int c = 0u;
-            if (v < v1) {
-              Elem<T>::unpack(slice[v], z);
-#pragma unroll
-              for (int i = 0; i < VE; ++i)
-                c += z[i] > -INFINITY && key_of(z[i]) == kmin ? 1u : 0u;
-            }
-            return c;
-          };
-          float z[VE];
-          unsigned int c = 0u;
-          for (int v = v0 + lane; v < v1; v += 32) c += count(v, z);
-          c = __reduce_add_sync(0xffffffffu, c);
-          if (lane == 0) sh.red32[warp] = c;
-          __syncthreads();
-          for (int w = 0; w < warp; ++w) before += sh.red32[w];
-          if (before < m && before + c >= m) {
-            for (int vv = v0; vv < v1; vv += 32) {
-              const unsigned int x = count(vv + lane, z);
-              unsigned int s = x;
-              for (int o = 1; o < 32; o <<= 1) {
-                const unsigned int a = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += a;
-              }
-              unsigned int at = before + s - x;
-              if (at < m && at + x >= m) {
-#pragma unroll
-                for (int i = 0; i < VE; ++i)
-                  if (z[i] > -INFINITY && key_of(z[i]) == kmin && ++at == m)
-                    for (int c2 = 0; c2 < C; ++c2)
-                      *cluster.map_shared_rank(&sh.cut_id, c2) = base + (vv + lane) * VE + i;
-              }
-              before += __shfl_sync(0xffffffffu, s, 31);
-            }
-          }
+          const int id = nth_of(value_of(kmin), m - before);
+          if (tid < C) *cluster.map_shared_rank(&sh.cut_id, tid) = id;
         }
         cluster.sync();
-        return Cut{b.mass + m * w, kmin, sh.cut_id};
+        cut = Cut{b.mass + m * w, kmin, sh.cut_id};
+        done = true;
       }
-      dirty = true;
-      int shift = 0;
-      while (((kmax - kmin) >> shift) >= (uint32_t)kBins) ++shift;
-      histogram(true, by_p, [&](float z, uint32_t& bin) {
-        const uint32_t k = key_of(z);
-        if (k < kmin || k > kmax) return false;
-        bin = (kmax - k) >> shift;
-        return true;
-      });
-      b = find(by_mass, limit, b.count, b.mass);  // the same limit
-      level0 = false;
-      const uint32_t last = kmax - (b.bin << shift), width = (1u << shift) - 1u;
-      top = value_of(last);
-      below = value_of((last - kmin > width ? last - width : kmin) - 1u);
+      if (done) {
+        take(cut);
+        if (by_mass || !by_p) break;
+        // top_k's cut is found in a bin: the row once more for top_p of the rest
+        by_mass = true;
+        limit = p_limit(cut.mass);
+        stage = kRow;
+        b = Bin{0ull, 0ull, 0u, 0u};
+        cluster.sync();  // lists and bins will be written again
+        continue;
+      }
     }
-  };
-
-  // ---- the cut: larger keys stay, and ids up to cut_id of this one ----
-  uint32_t cut_key = kLowestKey;
-  int cut_id = 0x7fffffff;
-  if (by_k || by_p) {
-    auto all = [&](float z, uint32_t& bin) {
-      bin = bin0(z);
-      return true;
-    };
-    // whether the listed tokens' mass is at least `limit` (before they are sorted)
-    auto list_reaches = [&](unsigned long long limit) {
-      unsigned long long m = 0ull;
-      for (int e = tid; e < C * cap; e += kThreads) {
-        const int c = e / cap;
-        if (e - c * cap < (int)sh.list_n[c])
-          m += weight(value_of(static_cast<uint32_t>(list[e] >> 32)));
-      }
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (lane == 0) sh.red64[warp] = m;
-      __syncthreads();
-      m = 0ull;
-      for (int w = 0; w < kWarps; ++w) m += sh.red64[w];
-      __syncthreads();
-      return m >= limit;
-    };
-    auto group_count = [&]() {
-      unsigned int count = 0u;
-      for (int i = lane; i < C * kGroups; i += 32) count += group[i].count;
-      return __reduce_add_sync(0xffffffffu, count);
-    };
-    // The top tokens first (from `edge` on): they hold the cut of a top_k, and
-    // that of a top_p when they reach it.
-    bool found = false, binned = false;
-    if (top_list) {
-      if (!by_k) {
-        // Whether they will is guessed from the block's threads' largest: when
-        // those above the edge are short of top_p of all, the weights go into
-        // their bins in the same pass.
-        const unsigned long long w = own_hi > -INFINITY ? weight(own_hi) : 0ull;
-        unsigned long long some = own_hi >= edge ? w : 0ull, whole = w;
-        for (int o = 16; o > 0; o >>= 1) {
-          some += __shfl_xor_sync(0xffffffffu, some, o);
-          whole += __shfl_xor_sync(0xffffffffu, whole, o);
-        }
-        if (lane == 0) {
-          sh.red64[warp] = some;
-          sh.red64b[warp] = whole;
-        }
-        __syncthreads();
-        some = whole = 0ull;
-        for (int x = 0; x < kWarps; ++x) {
-          some += sh.red64[x];
-          whole += sh.red64b[x];
-        }
-        binned = (double)some < (double)top_p * (double)whole;
-        __syncthreads();
-      }
-      unsigned int n;
-      unsigned long long total;
-      if (gather([&](float z) { return z >= edge && z > -INFINITY; },
-                 [&](float m) { return m < edge; }, !by_k, binned, n, total)) {
-        const unsigned long long limit = by_k ? (unsigned long long)top_k : p_limit(total);
-        if (by_k || list_reaches(limit)) {
-          Cut cut = list_cut(!by_k, Bin{0ull, limit, 0u, 0u}, n);
-          if (by_k && by_p) {
-            const Cut c = list_cut(true, Bin{0ull, p_limit(cut.mass), 0u, 0u}, n);
-            if (c.key > cut.key || (c.key == cut.key && c.id < cut.id)) cut = c;
-          }
-          found = true;
-          cut_key = cut.key;
-          cut_id = cut.id;
+    if (in_bins) {
+      if (stage == kRow && !by_mass) {
+        unsigned int count = 0u;
+#pragma unroll 1
+        for (int i = lane; i < C * kGroups; i += 32) count += group[i].count;
+        if ((unsigned int)top_k >= __reduce_add_sync(0xffffffffu, count)) {
+          // top_k keeps the whole row
+          if (!by_p) break;
+          by_mass = true;
+          limit = 0ull;
         }
       }
-      if (!found) cluster.sync();  // the lists will be written again
-    }
-    if (!found) {
-      if (binned) publish();
-      else histogram(by_k, by_p, all);
-      dirty = false;
-      unsigned long long limit = 0ull;  // top_p of the whole row
-      bool k_cut = false;
-      if (by_k) {
-        k_cut = (unsigned int)top_k < group_count();
+      b.limit = limit;
+      b = find(by_mass, b);
+      limit = b.limit;
+      if (stage == kRow) {
+        // listed by bin; `below`, half a bin further, leaves out most others
+        only = static_cast<int>(b.bin);
+        const float lo = hi - (float)(only + 1) / bin_scale;
+        below = only == kBins - 1 || !(lo > -INFINITY) ? -INFINITY : value_below(key_of(lo));
+        top = hi;
+      } else {
+        const uint32_t last = kmax - (b.bin << shift), width = (1u << shift) - 1u;
+        only = -1;
+        top = value_of(last);
+        below = value_below(last - kmin > width ? last - width : kmin);
       }
-      if (k_cut) {
-        const Bin b = find(false, (unsigned long long)top_k, 0u, 0ull);
-        const Cut cut = resolve(false, b, by_p);
-        cut_key = cut.key;
-        cut_id = cut.id;
-        if (by_p) {
-          limit = p_limit(cut.mass);
-          if (dirty) histogram(true, true, all);
-        }
-      }
-      if (by_p) {
-        const Bin b = find(true, limit, 0u, 0ull);
-        const Cut cut = resolve(true, b, false);
-        if (cut.key > cut_key || (cut.key == cut_key && cut.id < cut_id)) {
-          cut_key = cut.key;
-          cut_id = cut.id;
-        }
-      }
+      stage = kIn;
     }
   }
-  if (min_p > 0.f) {
-    // w >= min_p: a bound on the logit, rounded up to a float
-    const float z_min = __double2float_ru((double)hi + log((double)min_p) * (double)temp);
-    if (z_min > -INFINITY && key_of(z_min) > cut_key) {
-      cut_key = key_of(z_min);
-      cut_id = 0x7fffffff;
-    }
-  }
+  take_min_p();
 
   // ---- the draw: kept mass in id order ----
-  // warp w takes the vectors [w * seg, (w + 1) * seg) of the slice, 32 at a time
-  const int seg = (n_vec + kWarps * 32 - 1) / (kWarps * 32) * 32;
-  const int v_begin = warp * seg, v_end = min(n_vec, v_begin + seg);
-  const float cut_z = value_of(cut_key);
-  auto stays = [&](float z, int id) { return z > cut_z || (z == cut_z && id <= cut_id); };
-  unsigned long long mass = 0ull;
-  unsigned int count = 0u;
-  int first = 0x7fffffff;
-  for (int v = v_begin + lane; v < v_end; v += 32) {
-    const uint4 raw = slice[v];
-    if (Elem<T>::max_of(raw) < cut_z) continue;
-    float z[VE];
-    Elem<T>::unpack(raw, z);
-#pragma unroll
-    for (int i0 = 0; i0 < VE; i0 += 4) {
-      bool in[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) in[i] = stays(z[i0 + i], base + v * VE + i0 + i);
-      if (in[0] || in[1] || in[2] || in[3]) {
-        // four independent weights, then the ones that stay
-        unsigned long long w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = weight(z[i0 + i]);
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          if (in[i]) {
-            mass += w[i];
-            ++count;
-            first = min(first, base + v * VE + i0 + i);
-          }
-        }
-      }
-    }
-  }
-  for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-  count = __reduce_add_sync(0xffffffffu, count);
-  first = __reduce_min_sync(0xffffffffu, first);
-  if (lane == 0) {
-    sh.red64[warp] = mass;
-    sh.red32[warp] = count;
-    sh.red32b[warp] = static_cast<unsigned int>(first);
-  }
-  __syncthreads();
-  if (tid < C) {
-    Sums t{0ull, 0u, 0x7fffffff};
-    for (int w = 0; w < kWarps; ++w) {
-      t.mass += sh.red64[w];
-      t.count += sh.red32[w];
-      t.first = min(t.first, static_cast<int>(sh.red32b[w]));
-    }
-    *cluster.map_shared_rank(&sh.part[rank], tid) = t;
-  }
-  cluster.sync();
-  unsigned long long total = 0ull, before = 0ull;
-  unsigned int kept = 0u;
-  first = 0x7fffffff;
-  for (int c = 0; c < C; ++c) {
-    if (c == rank) before = total;
-    total += sh.part[c].mass;
-    kept += sh.part[c].count;
-    first = min(first, sh.part[c].first);
-  }
-  if (rank == 0 && tid == 0 && p.kept != nullptr) p.kept[r] = static_cast<int>(kept);
+  exchange(kept_of(weight));
+  unsigned long long before = 0ull;
+  const Sums all = total_of(before);
+  if (rank == 0 && tid == 0 && p.kept != nullptr) p.kept[r] = static_cast<int>(all.count);
   if (u == 0.f) {  // the first token that stays, however small its weight
-    if (rank == 0 && tid == 0) p.tokens[r] = first;
+    if (rank == 0 && tid == 0) p.tokens[r] = all.first;
     return;
   }
-  const unsigned long long target =
-      min(static_cast<unsigned long long>((double)u * (double)total), total - 1);
-  for (int w = 0; w < warp; ++w) before += sh.red64[w];
-  if (target < before || target >= before + mass) return;
-  // this warp holds the drawn token
-  for (int v0 = v_begin; v0 < v_end; v0 += 32) {
-    const int v = v0 + lane;
-    unsigned long long w[VE], n = 0ull;
-    if (v < v_end) {
-      float z[VE];
-      Elem<T>::unpack(slice[v], z);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        w[i] = stays(z[i], base + v * VE + i) ? weight(z[i]) : 0ull;
-        n += w[i];
-      }
-    }
-    unsigned long long s = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long a = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += a;
-    }
-    unsigned long long at = before + s - n;
-    if (target >= at && target < at + n) {
-      int id = -1;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        if (id < 0 && target < at + w[i]) id = base + v * VE + i;
-        at += w[i];
-      }
-      p.tokens[r] = id;
-    }
-    before += __shfl_sync(0xffffffffu, s, 31);
-    if (target < before) break;
-  }
+  pick(weight, target_of(all.mass), before);
 }
 
 template <typename T>
 medusa_status_t launch_sample(SampleParams& p, cudaStream_t stream) {
-  constexpr int VE = Elem<T>::kVec;
+  constexpr int VE = 16 / sizeof(T);
   // A cluster holds the row in shared memory.  Few rows: more blocks for each
   // while a block still has 4096 tokens.  Many: as few as leave two blocks to
   // an SM (a step's barriers cost a block the same whatever its share).

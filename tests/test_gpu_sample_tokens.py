@@ -121,6 +121,44 @@ def test_values_closer_than_a_bin():
     _compare(z, u, top_p=[0.1, 0.5, 0.99, 0.3, 0.7, 0.9], temperature=[20.0] * R, least=0.9)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_zeros_at_the_end_of_a_stretch(dtype):
+    """Zeros (of both signs) as the smallest of the tokens looked at: as the
+    lowest of the top tokens, and of a crowded bin."""
+    V, R = 20000, 4
+    rng = np.random.default_rng(9)
+    z = np.where(rng.random((R, V)) < 0.5, 0.0, -0.0)
+    z[:, ::200] = 1 + rng.random((R, V // 200))  # a hundred positive tokens
+    u = rng.random(R).tolist()
+    _compare(torch.from_numpy(z).to(dtype), u, top_k=[90, 101, 200, 256])
+    _compare(torch.from_numpy(z).to(dtype), u, top_p=[0.01, 0.03, 0.05, 0.5])
+    z[:, ::3] = 1e-3 * rng.random((R, len(z[0, ::3])))  # a third just above zero
+    z[:, 5] = 6.0
+    _compare(torch.from_numpy(z).to(dtype), u, top_k=[300, 6000, 9000, 15000])
+    _compare(torch.from_numpy(z).to(dtype), u, top_p=[0.1, 0.4, 0.6, 0.9])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_magnitudes_far_apart(dtype):
+    """Logits from 1e-6 to 8 of both signs, cuts among the smallest; tokens far
+    below any weight that a count or a tiny min_p still keeps."""
+    V, R = 9000, 6
+    rng = np.random.default_rng(10)
+    z = 10.0 ** rng.uniform(-6, 0.9, (R, V)) * rng.choice([-1.0, 1.0], (R, V))
+    z = torch.from_numpy(z).to(dtype)
+    u = [0.0] + rng.random(R - 1).tolist()
+    _compare(z, u, top_k=[4500, 4400, 4600, 3900, 8000, 1000])
+    _compare(z, u, top_p=[0.9, 0.93, 0.95, 0.97, 0.5, 0.99], temperature=[2.0] * R)
+    _compare(z, u, min_p=[0.02, 0.0183, 0.019, 0.3, 1e-30, 1.0], temperature=[2.0] * R, least=0.6)
+    _compare(z, u, temperature=[200.0] * R, top_p=[0.3, 0.5, 0.6, 0.7, 0.9, 1.0])
+    far = torch.full((R, V), -1000.0).to(dtype)
+    far[:, 7:4000:100] = z[:, :40]
+    far[:, 9::50] = -60.0
+    _compare(far, u, top_k=[20, 40, 41, 100, 2000, 8999])
+    _compare(far, u, top_p=[0.5, 0.9, 0.99, 1.0, 1.0, 1.0], min_p=[0.0, 0.0, 0.0, 0.0, 1e-30, 1e-35],
+             least=0.5)
+
+
 def test_masked_and_extreme_logits():
     """-inf and the types' lowest values: never drawn / no mass; temperatures
     far from one; a single finite logit."""
