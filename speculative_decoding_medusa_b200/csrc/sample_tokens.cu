@@ -203,7 +203,7 @@ struct Shared {
   float edge[kMaxCluster];  // a bound below the block's share of the top tokens
   Sums part[kMaxCluster];
   unsigned long long list_mass[kMaxCluster];  // weights of every token of the block
-  unsigned int list_n[kMaxCluster];  // tokens the block lists; bit 31: it filled its bins too
+  unsigned int list_n[kMaxCluster];           // tokens the block lists
   uint32_t kmin[kMaxCluster], kmax[kMaxCluster];
   double table[kExpTable];
   unsigned long long word[kRank], word_w[kRank];  // the last words of a list, their weights
@@ -217,7 +217,8 @@ struct Shared {
   int cut_id, n_th;
   unsigned long long red64[kWarps], red64b[kWarps];
   unsigned int red32[kWarps], red32b[kWarps];
-  float redf[kWarps], redg[kWarps];
+  float redf[kWarps];
+  float2 share[kWarps], shares[kMaxCluster];  // mass above and below the edge, a guess
 };
 
 // dynamic shared memory after the slice: histogram (counts, low and high words
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   if (lane == 0) sh.redf[warp] = hi;
   __syncthreads();
   // The share-th largest of the block's threads' largest, to its top 16 bits
-  // (found bit by bit): with every block's, at least `want` tokens of the row
-  // lie at or above the least of them, and not many more.
+  // (found bit by bit): with every block's, at least `want` tokens
+  // of the row lie at or above the least of them, and not many more.
   const bool by_k = top_k > 1 && top_k < p.V;
   const bool by_p = top_p < 1.f;
   const bool top_list = sizeof(T) == 4 && (by_k ? top_k <= kTopWanted : by_p);
@@ -326,18 +327,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   if (top_list) {
     const int want = by_k ? top_k : kTopWanted / 2;
     const int share = (want + C - 1) / C;
-    const uint32_t own = own_hi > -INFINITY ? key_of(own_hi) : 0u;
-    uint32_t k = 0u;
+    const bool some = own_hi > -INFINITY;
+    const uint32_t own = some ? key_of(own_hi) : 0u;
+    const uint32_t low = __reduce_min_sync(0xffffffffu, some ? own : 0xffffffffu);
+    const uint32_t high = __reduce_max_sync(0xffffffffu, own);
+    if (lane == 0) {
+      sh.red32[warp] = low;
+      sh.red32b[warp] = high;
+    }
+    const bool enough = __syncthreads_count(some) >= share;
+    const uint32_t k0 = __reduce_min_sync(0xffffffffu, sh.red32[lane % kWarps]);
+    const uint32_t k1 = __reduce_max_sync(0xffffffffu, sh.red32b[lane % kWarps]);
+    // (their common leading bits need no search)
+    uint32_t bit = k0 < k1 ? 0x80000000u >> __clz(static_cast<int>(k0 ^ k1)) : 0u;
+    uint32_t k = bit > 0u ? k0 & ~(2u * bit - 1u) : k0;
 #pragma unroll 1
-    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-      if (__syncthreads_count(own >= (k | bit)) >= share) k |= bit;
-    if (k > 0u) edge = value_of(k);
+    for (; bit >= 0x10000u; bit >>= 1)
+      if (__syncthreads_count(some && own >= (k | bit)) >= share) k |= bit;
+    if (enough) edge = value_of(k);
+    if (!by_k) {
+      // What share of the mass lies above the edge: the threads' largest there
+      // against one of their quads, for all, below it.  (A guess, by which a
+      // flat row's list is not tried.)
+      const float c = 1.442695f / temp;
+      float z[4], above = 0.f, rest = 0.f;
+      const Quad raw = tid < n_quad ? quads[tid] : Quad{};
+      Elem<T>::unpack(raw, z);
+      if (own_hi > edge) above = exp2f((own_hi - hi) * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (tid < n_quad && z[i] > -INFINITY && !(z[i] > edge)) rest += exp2f((z[i] - hi) * c);
+      for (int o = 16; o > 0; o >>= 1) {
+        above += __shfl_xor_sync(0xffffffffu, above, o);
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      }
+      if (lane == 0) sh.share[warp] = make_float2(above, rest * max(1.f, (float)n_quad / kThreads));
+      __syncthreads();
+    }
   }
   if (tid < C) {
     hi = sh.redf[0];
     for (int w = 1; w < kWarps; ++w) hi = max_nan(hi, sh.redf[w]);
     *cluster.map_shared_rank(&sh.hi[rank], tid) = hi;
     *cluster.map_shared_rank(&sh.edge[rank], tid) = edge;
+    if (top_list && !by_k) {
+      float2 t = make_float2(0.f, 0.f);
+      for (int w = 0; w < kWarps; ++w) {
+        if (!(sh.redf[w] > -INFINITY)) continue;
+        const float x = exp2f((sh.redf[w] - hi) * (1.442695f / temp));
+        t.x += x * sh.share[w].x;
+        t.y += x * sh.share[w].y;
+      }
+      *cluster.map_shared_rank(&sh.shares[rank], tid) = t;
+    }
   }
   cluster.sync();
   hi = sh.hi[0];
@@ -407,6 +449,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // finer histogram of its keys (kRange), until a list holds the stretch.
   enum Stage { kTop, kRow, kIn, kRange };
   int stage = top_list ? kTop : kRow;
+  if (top_list && !by_k) {
+    float some = 0.f, rest = 0.f;
+    for (int c = 0; c < C; ++c) {
+      if (!(sh.hi[c] > -INFINITY)) continue;
+      const float x = exp2f((sh.hi[c] - hi) * (1.442695f / temp));
+      some += x * sh.shares[c].x;
+      rest += x * sh.shares[c].y;
+    }
+    if (some < top_p * (some + rest)) stage = kRow;
+  }
   bool by_mass = !by_k;  // the bound looked for; top_k's first
   unsigned long long limit = by_k ? (unsigned long long)top_k : 0ull;  // 0: top_p of the row
   Bin b{0ull, 0ull, 0u, 0u};  // what lies before the stretch
@@ -422,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // the slice, 32 at a time
   const int seg = (n_quad + kWarps * 32 - 1) / (kWarps * 32) * 32;
   const int v_begin = warp * seg, v_end = min(n_quad, v_begin + seg);
+  const int run = (seg / 32 + 31) / 32;  // rows of 32 quads of a warp to a lane
 
   auto p_limit = [&](unsigned long long total) {
     // kept while the mass before is below top_p * total: an integer limit
@@ -466,19 +519,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       }
       return c;
     };
-    unsigned int c = 0u, before = 0u;
+    unsigned int mine = 0u, before = 0u;
+    int turn = 0, lot = 0;
 #pragma unroll 2
-    for (int v = v_begin + lane; v < v_end; v += 32) c += __popc(count(v));
-    c = __reduce_add_sync(0xffffffffu, c);
+    for (int v0 = v_begin; v0 < v_end; v0 += 32) {
+      const unsigned int c = __reduce_add_sync(0xffffffffu, __popc(count(v0 + lane)));
+      if (lane == lot) mine += c;
+      if (++turn == run) {
+        turn = 0;
+        ++lot;
+      }
+    }
+    const unsigned int c = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) sh.red32[warp] = c;
     __syncthreads();
 #pragma unroll 1
     for (int x = 0; x < warp; ++x) before += sh.red32[x];
     if (before < n && before + c >= n) {
+      unsigned long long none = 0ull;
+      unsigned int s = mine;
+      scan(none, s);
+      lot = __ffs(__ballot_sync(0xffffffffu, before + s >= n)) - 1;
+      before += __shfl_sync(0xffffffffu, s - mine, lot);
+      const int from = v_begin + lot * run * 32;
 #pragma unroll 1
-      for (int vv = v_begin; before < n && vv < v_end; vv += 32) {
+      for (int vv = from; before < n && vv < v_end; vv += 32) {
         const unsigned int bits = count(vv + lane), x = __popc(bits);
-        unsigned long long none = 0ull;
         unsigned int s = x;
         scan(none, s);
         const unsigned int at = before + s - x;
@@ -517,36 +583,50 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     const float cut_z = value_of(cut_key);
     return z > cut_z || (z == cut_z && id <= cut_id);
   };
-  // this warp's tokens that stay, by a function for their weights
+  // This warp's tokens that stay, by a function for their weights.  Their mass
+  // goes to `mine` by runs of `run` rows of 32 quads, a lane for each.
+  unsigned long long mine = 0ull;
   auto kept_of = [&](const auto& w_of) -> Sums {
-    unsigned long long mass = 0ull;
+    mine = 0ull;
     unsigned int count = 0u;
     int first = 0x7fffffff;
+    int turn = 0, lot = 0;
 #pragma unroll 2
-    for (int v = v_begin + lane; v < v_end; v += 32) {
-      const Quad raw = quads[v];
-      if (Elem<T>::max_of(raw) < value_of(cut_key)) continue;
-      float z[4];
-      Elem<T>::unpack(raw, z);
-      bool in[4];
+    for (int v0 = v_begin; v0 < v_end; v0 += 32) {
+      const int v = v0 + lane;
+      unsigned long long mass = 0ull;
+      const Quad raw = quads[min(v, n_quad - 1)];
+      if (v < v_end && Elem<T>::max_of(raw) >= value_of(cut_key)) {
+        float z[4];
+        Elem<T>::unpack(raw, z);
+        bool in[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
-      if (in[0] || in[1] || in[2] || in[3]) {
-        // four independent weights, then the ones that stay
-        unsigned long long w[4];
+        for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
+        if (in[0] || in[1] || in[2] || in[3]) {
+          // four independent weights, then the ones that stay
+          unsigned long long w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = w_of(z[i]);
+          for (int i = 0; i < 4; ++i) w[i] = w_of(z[i]);
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          if (in[i]) {
-            mass += w[i];
-            ++count;
-            first = min(first, base + v * 4 + i);
+          for (int i = 3; i >= 0; --i) {
+            if (in[i]) {
+              mass += w[i];
+              ++count;
+              first = min(first, base + v * 4 + i);
+            }
           }
         }
       }
+      // below 2^45 a lane: the sum of 32 by 24 bits
+      const unsigned int lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(mass) & 0xffffffu);
+      const unsigned int up = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(mass >> 24));
+      if (lane == lot) mine += (static_cast<unsigned long long>(up) << 24) + lo;
+      if (++turn == run) {
+        turn = 0;
+        ++lot;
+      }
     }
-    return Sums{warp_sum(mass), __reduce_add_sync(0xffffffffu, count),
+    return Sums{warp_sum(mine), __reduce_add_sync(0xffffffffu, count),
                 __reduce_min_sync(0xffffffffu, first)};
   };
   // the warps' sums, and with them the block's to every block
@@ -590,11 +670,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 #pragma unroll 1
     for (int w = 0; w < warp; ++w) before += sh.red64[w];
     if (target < before || target >= before + sh.red64[warp]) return;
+    // the run that holds it
+    unsigned long long s = mine;
+    unsigned int none = 0u;
+    scan(s, none);
+    const int lot = __ffs(__ballot_sync(0xffffffffu, target < before + s)) - 1;
+    before += __shfl_sync(0xffffffffu, s - mine, lot);
+    const int from = v_begin + lot * run * 32, to = min(v_end, from + run * 32);
 #pragma unroll 1
-    for (int v0 = v_begin; v0 < v_end && target >= before; v0 += 32) {
+    for (int v0 = from; v0 < to && target >= before; v0 += 32) {
       const int v = v0 + lane;
       unsigned long long w[4] = {0ull, 0ull, 0ull, 0ull};
-      if (v < v_end) {
+      if (v < to) {
         float z[4];
         Elem<T>::unpack(quads[v], z);
 #pragma unroll
@@ -602,7 +689,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       }
       const unsigned long long n = (w[0] + w[1]) + (w[2] + w[3]);
       unsigned long long s = n;
-      unsigned int none = 0u;
       scan(s, none);
       unsigned long long at = before + s - n;
       if (target >= at && target < at + n) {
@@ -620,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 
   // The group of bins that a bound falls in: the last with tokens before which
   // the count (or the mass) is below the limit, of the given start.  In mass
-  // mode limit 0 stands for top_p of the histogram's own total.  One warp.
+  // mode limit 0 stands for top_p of the histogram's own total; kGroups if a
+  // count limit is above the total.  One warp.
   auto find_group = [&](bool by_mass, Bin b) -> Bin {
     static_assert(kGroups == 64, "two groups per lane");
     Sums s[2];
@@ -641,6 +728,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     const unsigned int own_n = n;
     scan(m, n);
     if (b.limit == 0ull) b.limit = p_limit(__shfl_sync(0xffffffffu, m, 31));
+    if (!by_mass && b.limit > b.count + __shfl_sync(0xffffffffu, n, 31))
+      return Bin{0ull, b.limit, 0u, kGroups};
     m += b.mass - own_m;
     n += b.count - own_n;
     // this lane's later qualifying group, if any
@@ -721,36 +810,43 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     auto mass_of = [&](int bin, uint32_t n) {
       return bin == kTiny ? sh.tiny : n > 0u ? n * weight(value(bin)) : 0ull;
     };
-#pragma unroll 2
-    for (int g = warp; g < kGroups; g += kWarps) {
-      const int bin = g * 64 + 2 * lane;
-      const uint2 n = *reinterpret_cast<const uint2*>(&cnt[bin]);
-      const unsigned long long m = warp_sum(mass_of(bin, n.x) + mass_of(bin + 1, n.y));
-      const unsigned int k = __reduce_add_sync(0xffffffffu, n.x + n.y);
-      if (lane < C) *cluster.map_shared_rank(&group[rank * kGroups + g], lane) = Sums{m, k, 0};
+    {
+      // eight bins a thread, eight threads a group
+      const uint4 a = reinterpret_cast<const uint4*>(cnt)[2 * tid];
+      const uint4 c = reinterpret_cast<const uint4*>(cnt)[2 * tid + 1];
+      const uint32_t n[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+      unsigned long long m = 0ull;
+      unsigned int k = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m += mass_of(tid * 8 + i, n[i]);
+        k += n[i];
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2) {
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+        k += __shfl_xor_sync(0xffffffffu, k, o);
+      }
+      if (tid % 8 < C)
+        *cluster.map_shared_rank(&group[rank * kGroups + tid / 8], tid % 8) = Sums{m, k, 0};
     }
     if (tid < C) {
       *cluster.map_shared_rank(&sh.list_mass[rank], tid) = sh.tiny;
       *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.far;
     }
     cluster.sync();
-    unsigned long long mass = 0ull;
-    unsigned int counted = 0u, far = 0u;
+    unsigned int far = 0u;
 #pragma unroll 1
     for (int c = 0; c < C; ++c) far += sh.list_n[c];
-#pragma unroll 1
-    for (int i = lane; i < C * kGroups; i += 32) {
-      mass += group[i].mass;
-      counted += group[i].count;
-    }
-    ValueCut cut{warp_sum(mass), __reduce_add_sync(0xffffffffu, counted) + far, kValues, 0u, 0u, C};
-    counted = cut.count - far;
+    ValueCut cut{0ull, 0u, kValues, 0u, 0u, C};
     bool exact = u > 0.f;
     // the value and the tokens of it that a bound leaves
     auto cut_at = [&](bool by_mass, unsigned long long limit) {
       if (warp == 0) {
         const Bin g = find_group(by_mass, Bin{0ull, limit, 0u, 0u});
-        const int bin = g.bin * 64 + 2 * lane;
+        if (lane == 0) sh.value_cut.bin = kValues;
+        __syncwarp();
+        const int bin = min(g.bin, kGroups - 1u) * 64 + 2 * lane;
         uint2 n[kMaxCluster];  // all reads in flight
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
@@ -781,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         const bool second = (by_mass ? m1 > 0ull : s.y > 0u) &&
                             (by_mass ? m + m0 : (unsigned long long)(k + s.x)) < g.limit;
         const unsigned int votes = __ballot_sync(0xffffffffu, first || second);
-        if (lane == 31 - __clz(votes)) {
+        if (g.bin < kGroups && lane == 31 - __clz(votes)) {
           ValueCut c{};
           c.bin = bin + (second ? 1 : 0);
           const unsigned long long one = second ? w[1] : w[0];
@@ -814,13 +910,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       __syncthreads();
       // (in the shared bin tokens are not alike)
       exact = exact && c.bin != kTiny;
-      if (c.bin < cut.bin || (c.bin == cut.bin && c.ties < cut.ties)) cut = c;
+      if (c.bin == kValues)  // all that are counted stay
+        exact = exact && far == 0u;
+      else if (c.bin < cut.bin || (c.bin == cut.bin && c.ties < cut.ties)) cut = c;
     };
-    if (exact && by_k) {
-      if ((unsigned int)top_k <= counted) cut_at(false, top_k);
-      else if (far > 0u) exact = false;  // a cut among tokens without weight
-    }
-    if (exact && by_p) cut_at(true, p_limit(cut.mass));
+    if (exact && by_k) cut_at(false, top_k);
+    if (exact && by_p) cut_at(true, cut.bin < kValues ? p_limit(cut.mass) : 0ull);
     if (exact) {
       if (cut.bin < kValues) cut_key = key_of(value(cut.bin));
       take_min_p();
@@ -860,25 +955,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       if (target < before || target >= before + sh.part[rank].mass) return;
       // This block draws.  Its counts make way for weights, which no other
       // block reads any more.
-      uint32_t* w_lo = cnt;
-      uint32_t* w_hi = cnt + kValues;
+      unsigned long long* table = reinterpret_cast<unsigned long long*>(cnt);
       if (split && rank == cut.owner)
         cut_id = cut.ties > cut.before ? nth_of(cut_z, cut.ties - cut.before) : -1;
-#pragma unroll 2
-      for (int i = 0; i < kValues / kThreads; ++i) {
-        const int bin = i * kThreads + tid;
-        const unsigned long long w = cnt[bin] > 0u ? weight(value(bin)) : 0ull;
-        w_lo[bin] = static_cast<uint32_t>(w);
-        w_hi[bin] = static_cast<uint32_t>(w >> 32);
-      }
+      const uint4 a = reinterpret_cast<const uint4*>(cnt)[2 * tid];
+      const uint4 c = reinterpret_cast<const uint4*>(cnt)[2 * tid + 1];
+      const uint32_t n[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n[i] > 0u) table[tid * 8 + i] = weight(value(tid * 8 + i));
       __syncthreads();
       auto looked_up = [&](float z) -> unsigned long long {
+        if (z < cut_z) return 0ull;
         const uint32_t bits = __float_as_uint(z) >> 16;
         const int mag = static_cast<int>(bits & 0x7fffu) - least;
         if (mag <= 0) return weight(z);
-        if (mag >= kHalf) return 0ull;
-        const int bin = mag ^ (kTiny + (bits >> 15));
-        return static_cast<unsigned long long>(w_hi[bin]) << 32 | w_lo[bin];
+        return mag < kHalf ? table[mag ^ (kTiny + (bits >> 15))] : 0ull;
       };
       const Sums own = kept_of(looked_up);
       if (lane == 0) sh.red64[warp] = own.mass;
@@ -965,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     }
     __syncthreads();
     if (tid < C && to_list) {
-      *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local | (bins ? 0x80000000u : 0u);
+      *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.n_local;
       *cluster.map_shared_rank(&sh.list_mass[rank], tid) = sum ? block_sum(sh.red64) : 0ull;
     }
     if (to_list) {
@@ -994,6 +1087,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     if (warp == 0) {
       const Bin g = find_group(by_mass, before);
       // its 32 bins over the cluster
+      if (g.bin == kGroups) {
+        if (lane == 0) sh.bin = Bin{0ull, g.limit, 0u, kBins};
+      } else {
       const int bin = g.bin * 32 + lane;
       uint32_t rn[kMaxCluster], rl[kMaxCluster], rh[kMaxCluster];  // all reads in flight
 #pragma unroll
@@ -1018,6 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       const bool in = some && (by_mass ? m : (unsigned long long)n) < g.limit;
       const unsigned int bins = __ballot_sync(0xffffffffu, in);
       if (lane == 31 - __clz(bins)) sh.bin = Bin{m, g.limit, n, static_cast<uint32_t>(bin)};
+      }
     }
     __syncthreads();
     const Bin b = sh.bin;
@@ -1032,13 +1129,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // that larger words come first).  While more than kRank are left, those of
   // the 256th of their range that holds the cut; the rest rank by counting the
   // larger ones and adding up their weights.
-  auto list_cut = [&](Bin b, unsigned int n) -> Cut {
+  auto list_cut = [&](Bin b, unsigned int n, bool& then_p) -> Cut {
     unsigned long long e[2], w[2];
     bool alive[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int c = (tid + x * kThreads) / cap, i = (tid + x * kThreads) - c * cap;
-      alive[x] = c < C && i < (int)(sh.list_n[c] & 0x7fffffffu);
+      alive[x] = c < C && i < (int)sh.list_n[c];
       e[x] = alive[x] ? list[tid + x * kThreads] : 0ull;
     }
     w[0] = w[1] = 0ull;
@@ -1049,6 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     }
 #pragma unroll 1
     while (n > (unsigned int)kRank) {
+      then_p = false;
       unsigned long long least = ~0ull, most = 0ull;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -1131,7 +1229,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     }
     if (tid == 0) {
       sh.n_local = 0u;
-      sh.red32[0] = 0u;
+      sh.red32[0] = sh.red32[1] = 0u;
     }
     __syncthreads();
 #pragma unroll
@@ -1169,6 +1267,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       sh.cut = Cut{m + sh.word_w[at], static_cast<uint32_t>(own >> 32),
                    static_cast<int>(0xffffffffu - static_cast<uint32_t>(own))};
     __syncthreads();
+    if (then_p) {
+      stays = stays && m < p_limit(sh.cut.mass);
+      if (stays) atomicMax(&sh.red32[1], rk + 1u);
+      __syncthreads();
+      if (stays && sh.red32[1] == rk + 1u)
+        sh.cut = Cut{m + sh.word_w[at], static_cast<uint32_t>(own >> 32),
+                     static_cast<int>(0xffffffffu - static_cast<uint32_t>(own))};
+      __syncthreads();
+    }
     const Cut cut = sh.cut;
     __syncthreads();
     return cut;
@@ -1177,48 +1284,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // ---- the cut ----
 #pragma unroll 1
   while (by_k || by_p) {
-    bool sum = false, mass_bins = false;
-    if (stage == kTop && !by_k) {
-      // Whether the top tokens reach top_p is guessed from the block's threads'
-      // largest: when those above the edge are short of top_p of all, the
-      // weights go into their bins in the same pass.
-      sum = true;
-      const float w = own_hi > -INFINITY ? exp2f((own_hi - hi) * (float)(weight.c / kExpTable)) : 0.f;
-      float some = own_hi > below ? w : 0.f, whole = w;
-#pragma unroll 1
-      for (int o = 16; o > 0; o >>= 1) {
-        some += __shfl_xor_sync(0xffffffffu, some, o);
-        whole += __shfl_xor_sync(0xffffffffu, whole, o);
-      }
-      if (lane == 0) {
-        sh.redf[warp] = some;
-        sh.redg[warp] = whole;
-      }
-      __syncthreads();
-      some = whole = 0.f;
-#pragma unroll 1
-      for (int x = 0; x < kWarps; ++x) {
-        some += sh.redf[x];
-        whole += sh.redg[x];
-      }
-      mass_bins = some < top_p * whole;
-    } else if (stage == kRow || stage == kRange) {
-      mass_bins = by_p;
-    }
     const bool to_list = stage == kTop || stage == kIn;
-    pass(to_list, sum, mass_bins, stage == kRange || (stage == kRow && by_k));
+    pass(to_list, stage == kTop && !by_k, !to_list && by_p,
+         stage == kRange || (stage == kRow && by_k));
 
-    bool in_bins = !to_list;  // the stretch's tokens are in bins: find the one
     if (to_list) {
       unsigned int n = 0u;
       unsigned long long total = 0ull;
-      bool fits = true, binned = true;
+      bool fits = true;
 #pragma unroll 1
       for (int c = 0; c < C; ++c) {
-        const unsigned int k = sh.list_n[c] & 0x7fffffffu;
-        fits = fits && k <= (unsigned int)cap;
-        binned = binned && sh.list_n[c] != k;
-        n += k;
+        fits = fits && sh.list_n[c] <= (unsigned int)cap;
+        n += sh.list_n[c];
         total += sh.list_mass[c];
       }
       if (stage == kTop && !by_k) {
@@ -1228,7 +1305,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
           unsigned long long m = 0ull;
 #pragma unroll 1
           for (int e = tid; e < kList; e += kThreads)
-            if (e % cap < (int)(sh.list_n[e / cap] & 0x7fffffffu))
+            if (e % cap < (int)sh.list_n[e / cap])
               m += weight(value_of(static_cast<uint32_t>(list[e] >> 32)));
           m = warp_sum(m);
           if (lane == 0) sh.red64[warp] = m;
@@ -1241,21 +1318,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       bool done = fits;
       if (fits) {
         b.limit = limit;
-        cut = list_cut(b, n);
-        if (stage == kTop && by_k && by_p) {
-          // the same list again for top_p of what top_k leaves
-          take(cut);
+        // both bounds at once if the list is short enough to be ranked whole
+        bool then_p = stage == kTop && by_k && by_p;
+        const bool both = then_p;
+        cut = list_cut(b, n, then_p);
+        if (both) {
           by_mass = true;
-          b.limit = limit = p_limit(cut.mass);
-          cut = list_cut(b, n);
+          if (!then_p) {
+            take(cut);
+            b.limit = limit = p_limit(cut.mass);
+            cut = list_cut(b, n, then_p);
+          }
         }
       } else if (stage == kTop) {
-        if (by_k || !binned) stage = kRow;
-        else in_bins = true;  // every block has filled its bins
-        b = Bin{0ull, 0ull, 0u, 0u};
-        cluster.sync();  // lists and bins will be written again
-        if (!in_bins) continue;
         stage = kRow;
+        b = Bin{0ull, 0ull, 0u, 0u};
+        cluster.sync();  // the lists will be written again
+        continue;
       } else {
         // a crowded bin: its key range
         kmin = 0xffffffffu;
@@ -1333,20 +1412,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         continue;
       }
     }
-    if (in_bins) {
-      if (stage == kRow && !by_mass) {
-        unsigned int count = 0u;
-#pragma unroll 1
-        for (int i = lane; i < C * kGroups; i += 32) count += group[i].count;
-        if ((unsigned int)top_k >= __reduce_add_sync(0xffffffffu, count)) {
-          // top_k keeps the whole row
-          if (!by_p) break;
-          by_mass = true;
-          limit = 0ull;
-        }
-      }
+    if (!to_list) {
       b.limit = limit;
       b = find(by_mass, b);
+      if (b.bin == kBins) {
+        // top_k keeps the whole row
+        if (!by_p) break;
+        by_mass = true;
+        b = find(by_mass, Bin{0ull, 0ull, 0u, 0u});
+      }
       limit = b.limit;
       if (stage == kRow) {
         // listed by bin; `below`, half a bin further, leaves out most others
