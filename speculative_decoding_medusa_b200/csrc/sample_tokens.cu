@@ -520,31 +520,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       return c;
     };
     unsigned int mine = 0u, before = 0u;
-    int turn = 0, lot = 0;
-#pragma unroll 2
-    for (int v0 = v_begin; v0 < v_end; v0 += 32) {
-      const unsigned int c = __reduce_add_sync(0xffffffffu, __popc(count(v0 + lane)));
-      if (lane == lot) mine += c;
-      if (++turn == run) {
-        turn = 0;
-        ++lot;
-      }
-    }
+#pragma unroll 4
+    for (int v = v_begin + lane; v < v_end; v += 32) mine += __popc(count(v));
     const unsigned int c = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) sh.red32[warp] = c;
     __syncthreads();
 #pragma unroll 1
     for (int x = 0; x < warp; ++x) before += sh.red32[x];
     if (before < n && before + c >= n) {
-      unsigned long long none = 0ull;
-      unsigned int s = mine;
-      scan(none, s);
-      lot = __ffs(__ballot_sync(0xffffffffu, before + s >= n)) - 1;
-      before += __shfl_sync(0xffffffffu, s - mine, lot);
-      const int from = v_begin + lot * run * 32;
 #pragma unroll 1
-      for (int vv = from; before < n && vv < v_end; vv += 32) {
+      for (int vv = v_begin; before < n && vv < v_end; vv += 32) {
         const unsigned int bits = count(vv + lane), x = __popc(bits);
+        const unsigned int all = __reduce_add_sync(0xffffffffu, x);
+        if (before + all < n) {
+          before += all;
+          continue;
+        }
+        unsigned long long none = 0ull;
         unsigned int s = x;
         scan(none, s);
         const unsigned int at = before + s - x;
@@ -553,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
           for (unsigned int y = at + 1; y < n; ++y) left &= left - 1;
           sh.n_th = base + (vv + lane) * 4 + __ffs(left) - 1;
         }
-        before += __shfl_sync(0xffffffffu, s, 31);
+        before += all;
       }
     }
     __syncthreads();
@@ -603,14 +595,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
 #pragma unroll
         for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
         if (in[0] || in[1] || in[2] || in[3]) {
-          // four independent weights, then the ones that stay
           unsigned long long w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = w_of(z[i]);
+          w_of(z, in, w);
+          mass = (w[0] + w[1]) + (w[2] + w[3]);
 #pragma unroll
           for (int i = 3; i >= 0; --i) {
             if (in[i]) {
-              mass += w[i];
               ++count;
               first = min(first, base + v * 4 + i);
             }
@@ -683,9 +673,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       unsigned long long w[4] = {0ull, 0ull, 0ull, 0ull};
       if (v < to) {
         float z[4];
+        bool in[4];
         Elem<T>::unpack(quads[v], z);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = stays(z[i], base + v * 4 + i) ? w_of(z[i]) : 0ull;
+        for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
+        w_of(z, in, w);
       }
       const unsigned long long n = (w[0] + w[1]) + (w[2] + w[3]);
       unsigned long long s = n;
@@ -766,6 +758,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       return __uint_as_float(static_cast<uint32_t>((bin ^ (kTiny + sign)) + least) << 16 |
                              static_cast<uint32_t>(sign) << 31);
     };
+    const float z_tiny = __uint_as_float(static_cast<uint32_t>(least) << 16);
     uint32_t* cnt = h_cnt;
 #pragma unroll
     for (int i = 0; i < kValues / kThreads; ++i) cnt[i * kThreads + tid] = 0u;
@@ -920,7 +913,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       if (cut.bin < kValues) cut_key = key_of(value(cut.bin));
       take_min_p();
       // whether all of the shared bin or nothing of it stays
-      const float z_tiny = __uint_as_float(static_cast<uint32_t>(least) << 16);
       exact = !(fabsf(value_of(cut_key)) <= z_tiny);
       // (a min_p below every weight that counts)
       if (far > 0u && cut_key > kLowestKey && value_of(cut_key) < value(kValues - 1)) exact = false;
@@ -966,12 +958,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       for (int i = 0; i < 8; ++i)
         if (n[i] > 0u) table[tid * 8 + i] = weight(value(tid * 8 + i));
       __syncthreads();
-      auto looked_up = [&](float z) -> unsigned long long {
-        if (z < cut_z) return 0ull;
-        const uint32_t bits = __float_as_uint(z) >> 16;
-        const int mag = static_cast<int>(bits & 0x7fffu) - least;
-        if (mag <= 0) return weight(z);
-        return mag < kHalf ? table[mag ^ (kTiny + (bits >> 15))] : 0ull;
+      auto looked_up = [&](const float (&z)[4], const bool (&in)[4], unsigned long long (&w)[4]) {
+        bool near = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t bits = __float_as_uint(z[i]) >> 16;
+          const int mag = static_cast<int>(bits & 0x7fffu) - least;
+          near = near || (in[i] && mag <= 0);
+          w[i] = 0ull;
+          if (in[i] && mag > 0 && mag < kHalf) w[i] = table[mag ^ (kTiny + (bits >> 15))];
+        }
+        if (near) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (in[i] && fabsf(z[i]) <= z_tiny) w[i] = weight(z[i]);
+        }
       };
       const Sums own = kept_of(looked_up);
       if (lane == 0) sh.red64[warp] = own.mass;
@@ -1440,7 +1441,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   take_min_p();
 
   // ---- the draw: kept mass in id order ----
-  exchange(kept_of(weight));
+  // four independent weights, then the ones that stay
+  auto weights = [&](const float (&z)[4], const bool (&in)[4], unsigned long long (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = weight(z[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = in[i] ? w[i] : 0ull;
+  };
+  exchange(kept_of(weights));
   unsigned long long before = 0ull;
   const Sums all = total_of(before);
   if (rank == 0 && tid == 0 && p.kept != nullptr) p.kept[r] = static_cast<int>(all.count);
@@ -1448,7 +1456,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     if (rank == 0 && tid == 0) p.tokens[r] = all.first;
     return;
   }
-  pick(weight, target_of(all.mass), before);
+  pick(weights, target_of(all.mass), before);
 }
 
 template <typename T>
