@@ -6,8 +6,8 @@
 // of a block, which take its keys eight at a time in turn and merge their
 // maxima, sums and outputs through shared memory; S is as large as leaves the
 // machine's warps enough rows (a 128-token prompt of four heads is 512 rows:
-// one warp each would leave nine tenths of the machine idle; 27 us against
-// 8).  Of a step's eight keys the lanes split the head; the eight
+// one warp each would leave nine tenths of the machine idle: 27 us against
+// 9, most of which is the call).  Of a step's eight keys the lanes split the head; the eight
 // products are summed over the warp by halving (9 exchanges for 8 sums), so
 // that each lane ends with one key's score and computes one exponential.
 // Bound by latency at the sizes this path is for; K and V rows are read from

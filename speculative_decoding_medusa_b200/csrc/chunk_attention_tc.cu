@@ -6,29 +6,55 @@
 // One online-softmax pass over the keys.  A segment is one (sequence, kv head,
 // group of query tokens): two M tiles of 128 rows, each floor(128 / G) tokens
 // times their G query heads, against the key tiles its last token can see.
-// All segments are laid end to end and every CTA takes an equal contiguous
-// range of their tiles, so prompts, single tokens and anything between fill
-// the machine alike; where a range cuts a segment, its pieces are merged by
-// log-sum-exp weights inside the kernel by the last piece to arrive.  A range
-// has at most two such pieces (its first and its last), so the workspace
-// depends on the number of CTAs alone.
+// All segments are laid end to end on an axis of cost (a tile by its M tiles,
+// a segment's start and end) and every CTA takes an equal contiguous range of
+// it, so prompts, single tokens and anything between fill the machine alike;
+// where a range cuts a segment, its pieces are merged by log-sum-exp weights
+// inside the kernel by the last piece to arrive.  A range has at most two such
+// pieces (its first and its last), so the workspace depends on the number of
+// CTAs alone.
 //
 // Roles (384 threads):
-//   warp 0      TMA producer.  Key tiles are 128 slots: part of a page of 128
+//   warp 0      TMA producer of Q and K.  Key tiles are 128 slots: part of a page of 128
 //               or more, or as many whole smaller pages as fit (their boxes
 //               land one after another in the tile; page sizes are multiples
 //               of the 8-row swizzle atom, any other size takes one page per
 //               tile).  Lanes fetch the page table entries and issue one
-//               box each.  K and V share one ring of 32 KB slots (dh = 128:
-//               5), K's freed after its scores, V's after its product.
+//               box each.
+//   warp 2      the same of V.  K and V share one ring of 32 KB slots (dh =
+//               128: 5), K's freed after its scores, V's after its product.
 //   warp 1      MMA issuer: S = Q K^T into TMEM, then O += P V with P as bf16
-//               in TMEM over the scores' columns.
+//               in TMEM over the scores' columns.  The whole warp walks the
+//               tiles and one elected lane issues; a product waits for its P
+//               in a queue while the next scores are issued.
 //   warps 4-11  two softmax warpgroups, one query row per thread, each with a
 //               score buffer and an O of its own.  A segment of two M tiles
 //               gives one to each.  A segment of one M tile (single tokens,
 //               short chunks) gives its key tiles to them in turn, two
 //               independent chains instead of one; the first warpgroup adds
 //               the second's O to its own where the piece ends.
+//
+// Roundings to fewer bits than fp32: P to bf16, the product's operand type
+// (relative 2^-8 of each probability, while the sum l is of the fp32 values);
+// O to bf16 once, at the end.  Scores, maxima, sums, O and the pieces are fp32.
+//
+// What bounds it, with what it measured (one B200; 6.55 TB/s copy and 1.66
+// PFLOP/s bf16 products in a burst, 1.36 sustained):
+//   prompts         the chain scores -> maximum -> exponentials -> P of a tile
+//                   and, in long runs, the power limit.  8192 tokens, 32 + 8
+//                   heads of 128: 480 us, 1.14 PFLOP/s.
+//   short chunks    the same, with M tiles partly empty and segments of a few
+//                   tiles: 12 sequences of 1 to 600 tokens that end at 601 to
+//                   6000 slots, pages of 16: 163 to 177 us.
+//   single tokens   HBM: 32 sequences of 30001 to 32768 slots 597 us, 6.9
+//                   TB/s; eight of 4096 to 8192 47 us, of which the prologue,
+//                   the merge and the launch are a third.
+// Tried and slower: tiles of 64 keys with two score buffers a warpgroup (848 us
+// where tiles of 128 took 565); some of the exponentials as a polynomial on the
+// FMA units (every fourth pair: prompt 498 us, every eighth: 490, none: 480);
+// rescaling O at every new maximum (prompt 519); a producer's and an issuer's
+// single lane in divergent code (a third slower); one producer for K and V (a V
+// waits behind the next K's slot).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -56,7 +82,9 @@ constexpr float kLazy = 8.f;   // rescale O only when the maximum grows by 2^8
 constexpr uint32_t kTmemCols = 512;
 // What a CTA's range is measured in: the cost of a tile of two M tiles, of a
 // tile of one, and of a segment's start and end (its Q, its first scores, its
-// output).
+// output).  With 2, 3 and 4 for a tile of one, short chunks took 280, 193 and
+// 185 us and the prompt of 8192 tokens 499, 501 and 519; with 4, 8 and 16 for a
+// segment 191, 173, 188 and 534, 501, 511.
 constexpr int kTwoCost = 4, kOneCost = 3;
 constexpr int kSegCost = 8;
 constexpr int kMinCost = 8;    // smallest range a CTA takes
@@ -86,33 +114,6 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(r));
   return r != 0;
-}
-
-constexpr int kPolyEvery = 4;  // one pair of exponentials in kPolyEvery by polynomial
-
-// 2^x of a pair by fp32 arithmetic: x = n + f, |f| <= 1/2, a minimax
-// polynomial of degree 5 for 2^f (relative error 2^-22) and n added to the
-// exponent; x below -126 counts as -126.  It takes some of the exponentials
-// off the special-function unit, which alone would bound the softmax.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-  float x0, x1;
-  f32x2_unpack(x2, x0, x1);
-  const uint64_t x = f32x2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const uint64_t t = f32x2_add(x, f32x2_pack(kMagic, kMagic));
-  const uint64_t nf = f32x2_add(t, f32x2_pack(-kMagic, -kMagic));
-  const uint64_t f = f32x2_fma(nf, f32x2_pack(-1.f, -1.f), x);
-  auto both = [](float c) { return f32x2_pack(c, c); };
-  uint64_t q = f32x2_fma(both(0.0013276472454890609f), f, both(0.009675540961325169f));
-  q = f32x2_fma(q, f, both(0.05550713092088699f));
-  q = f32x2_fma(q, f, both(0.24022120237350464f));
-  q = f32x2_fma(q, f, both(0.6931469440460205f));
-  q = f32x2_fma(q, f, both(1.0000001192092896f));
-  float t0, t1, q0, q1;
-  f32x2_unpack(t, t0, t1);
-  f32x2_unpack(q, q0, q1);
-  return f32x2_pack(__int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23)),
-                    __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23)));
 }
 
 template <int DH>
@@ -952,14 +953,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int c = h * 64 + 2 * e;
           const uint64_t x2 = f32x2_fma(f32x2_pack(sv[c], sv[c + 1]), scale2, nbase2);
-          uint64_t a2;
-          if (kFull && e % kPolyEvery == kPolyEvery - 1) {
-            a2 = exp2_poly2(x2);
-          } else {
-            float x0, x1;
-            f32x2_unpack(x2, x0, x1);
-            a2 = f32x2_pack(ex2_approx(x0), ex2_approx(x1));
-          }
+          float x0, x1;
+          f32x2_unpack(x2, x0, x1);
+          const uint64_t a2 = f32x2_pack(ex2_approx(x0), ex2_approx(x1));
           part[e & 3] = f32x2_add(part[e & 3], a2);
           float a0, a1;
           f32x2_unpack(a2, a0, a1);

@@ -290,7 +290,8 @@ __device__ __forceinline__ Row row_of_thread(int t, const int* cu, const int* kv
 // Many tokens, a thread per unit: resident blocks walk the tokens in chunks of
 // kChunk, whose metadata they find at once, with the next token's data and
 // angles on their way while they finish the current one; one barrier a token.
-// 8192 tokens of 32 + 8 heads written into pages (214 MB): kPipeTime, against
+// 8192 tokens of 32 + 8 heads written into pages (214 MB): 46.5 us
+// (4.6 TB/s of the 6.55 that a copy reaches; 33 us at that), against
 // 60 us with a block per token, whose latencies only other blocks cover, and
 // 54 us with each token's metadata found two tokens ahead (its chain of three
 // reads was as long as a token's turn).
