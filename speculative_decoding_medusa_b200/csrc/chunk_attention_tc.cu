@@ -97,6 +97,7 @@ struct TcParams {
   int ppt;  // pages per tile (0: pages of 128 or more, tpp tiles each)
   int tpp, kt;  // kt: slots of a full tile
   int B, T, Hq, Hkv, G, tpt;  // tpt: tokens per M tile
+  int q_box;                  // tokens per copy of Q
   float scale_log2;
   __nv_bfloat16* out;
   float* o_part;             // [2 * grid] pieces of [8] warps' rows: groups of 4 columns
@@ -632,12 +633,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int t1 = start[8], per = start[9];
-  // Rows that no copy ever writes are cleared once: of the Q tiles past their
-  // tokens, of the key tiles past a full tile's slots (their weights are zero,
-  // but 0 * NaN is not).
-  if (p.G * p.tpt < kMT || (p.ppt > 0 && p.kt < kBN)) {
+  // Rows that no copy writes are cleared once: of the key tiles past a full
+  // tile's slots (their weights are zero, but 0 * NaN is not); of the Q tiles
+  // past a short chunk's tokens, because products of zeros draw less power
+  // (32 single tokens of 32768 slots hold the card at its limit).
+  {
+    const int n = p.ppt > 0 && p.kt < kBN ? L::kBarOff : 2 * L::kQBytes;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < L::kBarOff / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = z;
+    for (int i = tid; i < n / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = z;
     fence_proxy_async_smem();
     __syncthreads();
   }
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int next_id = page_id(cur);
       const int panel_rows = p.ppt > 0 ? p.page : kBN;
       const uint32_t box_bytes = static_cast<uint32_t>(panel_rows) * 128u * L::kPanels;
-      const uint32_t q_bytes = static_cast<uint32_t>(p.G * p.tpt) * 128u * L::kPanels;
+      const uint32_t q_rows = static_cast<uint32_t>(p.G * p.q_box);
       int slot = is_v ? 1 : 0;
       uint32_t phase = 0, n_pieces = 0;
       uint32_t q_loads0 = 0, q_loads1 = 0;
@@ -709,24 +712,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         id, pol);
         }
         if (!is_v && cur.first) {
-          // the piece's Q tiles, once the last piece's scores are done
-          if (lane == 0) {
-            if (n_pieces > 0)
-              ok = mbar_wait_bounded(q_empty, (n_pieces - 1) & 1, abort_flag, p.status);
-            if (ok) {
-              for (int m = 0; m < cur.n_mt; ++m) {
-                mbar_arrive_expect_tx(&q_full[m], q_bytes);
+          // the piece's Q tiles, once the last piece's scores are done: as many
+          // boxes as have tokens
+          if (lane == 0 && n_pieces > 0)
+            ok = mbar_wait_bounded(q_empty, (n_pieces - 1) & 1, abort_flag, p.status);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          for (int m = 0; ok && m < cur.n_mt; ++m) {
+            const int t0 = (cur.qg * 2 + m) * p.tpt;  // of the sequence's new tokens
+            const int boxes = (min(p.tpt, cur.qlen - t0) + p.q_box - 1) / p.q_box;
+            if (lane == 0) mbar_arrive_expect_tx(&q_full[m], boxes * q_rows * 128u * L::kPanels);
+            __syncwarp();
+            if (lane < boxes) {
+              uint8_t* dst = smem + L::kQOff + m * L::kQBytes + lane * q_rows * 128;
 #pragma unroll
-                for (int pn = 0; pn < L::kPanels; ++pn)
-                  tma_load_4d(smem + L::kQOff + m * L::kQBytes + pn * (kMT * 128), &tmQ, &q_full[m],
-                              pn * 64, 0, cur.kvh, cur.q0 + (cur.qg * 2 + m) * p.tpt, pass);
-                if (m == 0) ++q_loads0;
-                else ++q_loads1;
-              }
+              for (int pn = 0; pn < L::kPanels; ++pn)
+                tma_load_4d(dst + pn * (kMT * 128), &tmQ, &q_full[m], pn * 64, 0, cur.kvh,
+                            cur.q0 + t0 + lane * p.q_box, pass);
             }
+            if (m == 0) ++q_loads0;
+            else ++q_loads1;
           }
           ++n_pieces;
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         slot += 2;
         if (slot >= L::kRing) {
@@ -1184,6 +1190,10 @@ medusa_status_t launch_tc(const ChunkParams& c, void* ws, cudaStream_t stream) {
   p.Hkv = c.Hkv;
   p.G = c.G;
   p.tpt = kMT / c.G;
+  // copies of Q start on whole swizzle atoms of 8 rows
+  p.q_box = c.G % 8 == 0 ? 1 : c.G % 4 == 0 ? 2 : c.G % 2 == 0 ? 4 : 8;
+  if (p.q_box > p.tpt) p.q_box = p.tpt;  // one copy
+  else p.tpt -= p.tpt % p.q_box;
   p.scale_log2 = c.scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(c.out);
   p.status = c.status;
@@ -1195,11 +1205,11 @@ medusa_status_t launch_tc(const ChunkParams& c, void* ws, cudaStream_t stream) {
   p.piece_count = reinterpret_cast<unsigned int*>(w8 + o_bytes + l_bytes);
 
   CUtensorMap mQ, mK, mV;
-  // queries as [T][Hkv][G][DH]: boxes of 64 columns x G heads x tpt tokens
+  // queries as [T][Hkv][G][DH]: boxes of 64 columns x G heads x q_box tokens
   const uint64_t dq[4] = {DH, (uint64_t)c.G, (uint64_t)c.Hkv, (uint64_t)c.T};
   const uint64_t sq[3] = {DH * 2, (uint64_t)c.G * DH * 2,
                           (uint64_t)(c.T > 1 ? c.q_stride : (long long)c.Hq * DH) * 2};
-  const uint32_t bq[4] = {64, (uint32_t)c.G, 1, (uint32_t)p.tpt};
+  const uint32_t bq[4] = {64, (uint32_t)c.G, 1, (uint32_t)p.q_box};
   // pools [n_pages][Hkv][page][DH]: boxes of 64 columns x (a page or 128 rows)
   const uint64_t dk[4] = {DH, (uint64_t)c.page_size, (uint64_t)c.Hkv, (uint64_t)c.n_pages};
   const uint64_t sk[3] = {DH * 2, (uint64_t)c.page_size * DH * 2,
