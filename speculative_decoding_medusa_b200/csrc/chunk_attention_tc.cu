@@ -294,104 +294,88 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
   const bool valid = (rows >> lane) & 1u;
   bool finite = true;
   if (__popc(rows) <= kFewRows) {
-    // few rows (single tokens): the warp takes four rows together, lanes over
-    // the pieces for the weights, then over the columns; a step's loads of
-    // all four rows are in flight together
+    // Few rows (single tokens): the warp takes four rows together, lanes over
+    // the pieces for the weights, then over the columns, with 16 loads in
+    // flight.  Written to be short: this code runs once a launch, and waiting
+    // for its instructions took longer than waiting for the pieces (17 pieces:
+    // 17k cycles with the weights worked out in every lane, 31k unrolled
+    // twice as far).
     constexpr int kCols = DH / 32;  // columns a lane
-    constexpr int kR = 4, kK = 2;   // rows and pieces of a step
+    constexpr int kR = 4, kK = 4;   // rows and pieces of a step
+    using V = typename std::conditional<kCols == 4, float4, float2>::type;
+#pragma unroll 1
     for (unsigned int left = rows; left != 0u;) {
       int src[kR];
+      float M[kR], sum[kR], acc[kR][kCols];
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
         src[i] = left != 0u ? __ffs(left) - 1 : -1;
         left &= left - 1;
-      }
-      float M[kR], sum[kR], l[kR];
-#pragma unroll
-      for (int i = 0; i < kR; ++i) {
         M[i] = -INFINITY;
         sum[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[i][c] = 0.f;
       }
+#pragma unroll 1
       for (int k0 = 0; k0 < n; k0 += 32) {
         const float* lse = p.lse_part + (size_t)piece_slot(c0 + k0 + lane, per, s0) * kRows + row0;
-        float mx[kR], e[kR];
+        float l[kR], mx[kR], w[kR];  // w: this lane's piece
 #pragma unroll
-        for (int i = 0; i < kR; ++i) {
-          l[i] = k0 + lane < n && src[i] >= 0 ? __ldcg(lse + src[i]) : -INFINITY;
-          mx[i] = l[i];
-        }
-#pragma unroll
+        for (int i = 0; i < kR; ++i)
+          mx[i] = l[i] = k0 + lane < n && src[i] >= 0 ? __ldcg(lse + src[i]) : -INFINITY;
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
           for (int i = 0; i < kR; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
           mx[i] = fmaxf(M[i], mx[i]);
-          e[i] = l[i] == -INFINITY ? 0.f : exp2f(l[i] - mx[i]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < kR; ++i) e[i] += __shfl_xor_sync(0xffffffffu, e[i], o);
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-          sum[i] = (M[i] == -INFINITY ? 0.f : sum[i] * exp2f(M[i] - mx[i])) + e[i];
+          const float corr = M[i] == -INFINITY ? 0.f : ex2_approx(M[i] - mx[i]);
+          w[i] = l[i] == -INFINITY ? 0.f : ex2_approx(l[i] - mx[i]);
           M[i] = mx[i];
+          sum[i] = sum[i] * corr + w[i];
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) acc[i][c] *= corr;
         }
-      }
-      float inv[kR], acc[kR][kCols];
+        const int cnt = min(32, n - k0);
+#pragma unroll 1
+        for (int k = 0; k < cnt; k += kK) {
+          V x[kK][kR];
 #pragma unroll
-      for (int i = 0; i < kR; ++i) {
-        inv[i] = sum[i] > 0.f ? 1.f / sum[i] : sum[i];
+          for (int d = 0; d < kK; ++d) {
+            const size_t slot = piece_slot(c0 + k0 + min(k + d, cnt - 1), per, s0);
+            const float* v = p.o_part + (slot * kRows + row0) * DH + lane * kCols;  // whole rows
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[i][c] = 0.f;
-      }
-      for (int k = 0; k < n; k += kK) {
-        float x[kK][kR][kCols], lk[kK][kR];
+            for (int i = 0; i < kR; ++i)
+              x[d][i] = __ldcg(reinterpret_cast<const V*>(v + max(src[i], 0) * DH));
+          }
 #pragma unroll
-        for (int d = 0; d < kK; ++d) {
-          const size_t slot = piece_slot(c0 + min(k + d, n - 1), per, s0);
-          const float* v = p.o_part + (slot * kRows + row0) * DH + lane * kCols;  // whole rows
-          const float* lse = p.lse_part + slot * kRows + row0;
+          for (int d = 0; d < kK; ++d)
 #pragma unroll
-          for (int i = 0; i < kR; ++i) {
-            const int r = max(src[i], 0);
-            if (kCols == 4) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(v + r * DH));
-              x[d][i][0] = y.x;
-              x[d][i][1] = y.y;
-              x[d][i][kCols - 2] = y.z;
-              x[d][i][kCols - 1] = y.w;
-            } else {
-              const float2 y = __ldcg(reinterpret_cast<const float2*>(v + r * DH));
-              x[d][i][0] = y.x;
-              x[d][i][kCols - 1] = y.y;
+            for (int i = 0; i < kR; ++i) {
+              // a weight of zero adds nothing, whatever the partial holds
+              const float wk = __shfl_sync(0xffffffffu, w[i], k + d);
+              const float* f = reinterpret_cast<const float*>(&x[d][i]);
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) acc[i][c] += wk == 0.f ? 0.f : wk * f[c];
             }
-            lk[d][i] = __ldcg(lse + r);
-          }
         }
-#pragma unroll
-        for (int d = 0; d < kK; ++d)
-#pragma unroll
-          for (int i = 0; i < kR; ++i) {
-            const float w = k + d >= n || src[i] < 0 || lk[d][i] == -INFINITY
-                                ? 0.f
-                                : exp2f(lk[d][i] - M[i]) * inv[i];
-            // a weight of zero adds nothing, whatever the partial holds
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) acc[i][c] += w == 0.f ? 0.f : w * x[d][i][c];
-          }
       }
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < kR; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
+        const float inv = sum[i] > 0.f ? 1.f / sum[i] : sum[i];
         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(
             0xffffffffu, reinterpret_cast<unsigned long long>(out), max(src[i], 0)));
         if (src[i] < 0) continue;
 #pragma unroll
         for (int c = 0; c < kCols; c += 2) {
-          finite = finite && fabsf(acc[i][c]) < INFINITY && fabsf(acc[i][c + 1]) < INFINITY;
-          *reinterpret_cast<__nv_bfloat162*>(dst + lane * kCols + c) =
-              __floats2bfloat162_rn(acc[i][c], acc[i][c + 1]);
+          const float a = acc[i][c] * inv, b = acc[i][c + 1] * inv;
+          finite = finite && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+          *reinterpret_cast<__nv_bfloat162*>(dst + lane * kCols + c) = __floats2bfloat162_rn(a, b);
         }
       }
     }
@@ -472,10 +456,12 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
       const int groups = __shfl_sync(0xffffffffu, n_qg, src);
       long long s = 0;
       for (int g = lane; g < groups; g += 32) s += group_cost(q, k, g, p);
+#pragma unroll 1
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (lane == src) n = s;
     }
     n *= p.Hkv;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const long long a = __shfl_up_sync(0xffffffffu, n, o);
       if (lane >= o) n += a;
@@ -525,6 +511,7 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
     // beyond the last group the costs only have to be positive
     const int n = group_cost(s[6], s[7], g0 + lane, p);
     int c = n;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, c, o);
       if (lane >= o) c += a;
@@ -623,6 +610,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+  } else if (warp > 2) {
+    // No copy writes the Q rows past a short chunk's tokens: cleared once, for
+    // products of zeros draw less power (32 single tokens of 32768 slots hold
+    // the card at its limit).
+    for (int i = tid - 96; i < L::kRingOff / 16; i += kThreads - 96)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
   }
   __syncwarp();
   tc_fence_before();
@@ -633,14 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int t1 = start[8], per = start[9];
-  // Rows that no copy writes are cleared once: of the key tiles past a full
-  // tile's slots (their weights are zero, but 0 * NaN is not); of the Q tiles
-  // past a short chunk's tokens, because products of zeros draw less power
-  // (32 single tokens of 32768 slots hold the card at its limit).
-  {
-    const int n = p.ppt > 0 && p.kt < kBN ? L::kBarOff : 2 * L::kQBytes;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < n / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = z;
+  if (p.ppt > 0 && p.kt < kBN) {
+    // nor any past a full tile's slots (their weights are zero, but 0 * NaN
+    // is not)
+    for (int i = L::kRingOff / 16 + tid; i < L::kBarOff / 16; i += kThreads)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     __syncthreads();
   }
