@@ -667,7 +667,7 @@ MEDUSA_API medusa_status_t medusa_rope_freqs(int rot, double theta,
  * Outputs (device, dtype dt): q_out, k_out, tokens q_out_stride /
  *   k_out_stride apart.  An output may be its input (in place, same stride);
  *   otherwise outputs overlap no input.
- * Precision: angles to 2^-33 turns, products in fp32, one rounding.
+ * Precision: angles to 2^-28 turns, products in fp32, one rounding.
  * Limits: T >= 0 (nothing is launched for 0); rot <= dh <= 1024;
  *   Hq, Hkv >= 1; strides >= heads * dh.  No alignment beyond the type's own.
  * ---------------------------------------------------------------------- */

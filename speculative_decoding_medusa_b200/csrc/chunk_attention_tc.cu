@@ -46,9 +46,10 @@
 //   short chunks    the same, with M tiles partly empty and segments of a few
 //                   tiles: 12 sequences of 1 to 600 tokens that end at 601 to
 //                   6000 slots, pages of 16: 163 to 177 us.
-//   single tokens   HBM: 32 sequences of 30001 to 32768 slots 597 us, 6.9
-//                   TB/s; eight of 4096 to 8192 47 us, of which the prologue,
-//                   the merge and the launch are a third.
+//   single tokens   HBM: 32 sequences of 30001 to 32768 slots 600 us, 6.9
+//                   TB/s (676 in long runs, under the power limit); eight of
+//                   4096 to 8192 45 us, of which the prologue, the merge and
+//                   the launch are a third; one of 6000, all latency, 19 us.
 // Tried and slower: tiles of 64 keys with two score buffers a warpgroup (848 us
 // where tiles of 128 took 565); some of the exponentials as a polynomial on the
 // FMA units (every fourth pair: prompt 498 us, every eighth: 490, none: 480);
@@ -87,7 +88,10 @@ constexpr uint32_t kTmemCols = 512;
 // segment 191, 173, 188 and 534, 501, 511.
 constexpr int kTwoCost = 4, kOneCost = 3;
 constexpr int kSegCost = 8;
-constexpr int kMinCost = 8;    // smallest range a CTA takes
+// Smallest range a CTA takes: with 8, 16, 24 and 32 a token over 1000 slots of 8
+// kv heads took 15.5, 19.5, 20.5 and 16.1 us, a chunk of 100 tokens 25.6, 27.2,
+// 30.4 and 34.3.
+constexpr int kMinCost = 8;
 constexpr int kMaxB = 1024;
 constexpr int kFewRows = 8;    // rows of a warp whose pieces the whole warp merges
 
