@@ -719,8 +719,8 @@ MEDUSA_API medusa_status_t medusa_rope_append(
  *
  * Inputs (device): q [T, Hq, dh] of dtype dt, tokens q_stride elements apart;
  *   pages (dtype dt); cu_q [B + 1], kv_len [B] int32 as above.
- * Output (device): out [T, Hq, dh] of dtype dt, dense; rows from cu_q[B] on
- *   are left as they are.
+ * Output (device): out [T, Hq, dh] of dtype dt, dense, apart from q; rows from
+ *   cu_q[B] on are left as they are.
  * Workspace: medusa_chunk_attention_workspace_size(...) bytes, 256-byte
  *   aligned; the size depends on the current device's multiprocessor count
  *   and on none of the lengths.

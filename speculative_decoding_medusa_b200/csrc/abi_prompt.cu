@@ -21,7 +21,7 @@ medusa_status_t check_rotation(const medusa_rope_t* r, int dh) {
   return MEDUSA_OK;
 }
 
-// one operand [T, H, dh] and, for an output in place, its input
+// one operand [T, H, dh]
 medusa_status_t check_operand(const void* x, long long stride, int T, int H, int dh, size_t eb) {
   if (x == nullptr) return fail(MEDUSA_ERR_INVALID_ARG, "rope: null pointer");
   if (T > 1 && stride < (long long)H * dh)
@@ -30,25 +30,36 @@ medusa_status_t check_operand(const void* x, long long stride, int T, int H, int
   return MEDUSA_OK;
 }
 
+struct Span {
+  const void* p;
+  long long stride;  // elements between tokens
+  int H;
+};
+
+// whether two operands of T tokens share a byte; slices of one buffer with the
+// same stride may interleave
+bool overlap(const Span& x, const Span& y, int T, int dh, size_t eb) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  const uintptr_t wa = (uintptr_t)x.H * dh * eb, wb = (uintptr_t)y.H * dh * eb;
+  const uintptr_t na = (uintptr_t)(T - 1) * x.stride * eb + wa;
+  const uintptr_t nb = (uintptr_t)(T - 1) * y.stride * eb + wb;
+  if (a + na <= b || b + nb <= a) return false;
+  if (T == 1 || x.stride != y.stride) return true;
+  const uintptr_t row = (uintptr_t)x.stride * eb;
+  const uintptr_t d = b >= a ? (b - a) % row : (row - (a - b) % row) % row;  // of y's row in x's
+  return d < wa || d + wb > row;
+}
+
 // an output is its input (same stride) or shares no byte with it
-medusa_status_t check_overlap(const void* in, long long in_stride, const void* out,
-                              long long out_stride, int T, int H, int dh, size_t eb) {
-  if (in == out) {
-    if (T > 1 && in_stride != out_stride)
+medusa_status_t check_in_place(const Span& in, const Span& out, int T, int dh, size_t eb) {
+  if (in.p == out.p) {
+    if (T > 1 && in.stride != out.stride)
       return fail(MEDUSA_ERR_INVALID_ARG, "rope: in place needs equal strides");
     return MEDUSA_OK;
   }
-  // two slices of one buffer with the same stride may interleave
-  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
-  const uintptr_t na = ((uintptr_t)(T - 1) * in_stride + (uintptr_t)H * dh) * eb;
-  const uintptr_t nb = ((uintptr_t)(T - 1) * out_stride + (uintptr_t)H * dh) * eb;
-  if (a + na <= b || b + nb <= a) return MEDUSA_OK;
-  if (T > 1 && in_stride == out_stride) {
-    const uintptr_t row = (uintptr_t)in_stride * eb, used = (uintptr_t)H * dh * eb;
-    const uintptr_t d = (b > a ? b - a : row - (a - b) % row) % row;
-    if (d >= used && d + used <= row) return MEDUSA_OK;
-  }
-  return fail(MEDUSA_ERR_INVALID_ARG, "rope: an output overlaps its input");
+  if (overlap(in, out, T, dh, eb))
+    return fail(MEDUSA_ERR_INVALID_ARG, "rope: an output overlaps its input");
+  return MEDUSA_OK;
 }
 
 medusa_status_t check_pages(const medusa_pages_t* p, size_t align) {
@@ -105,12 +116,15 @@ medusa_status_t medusa_rope(const medusa_rope_t* rope, const void* q, long long 
   const size_t eb = dt == MEDUSA_BF16 ? 2 : 4;
   if ((st = check_operand(q, q_stride, T, Hq, dh, eb)) != MEDUSA_OK) return st;
   if ((st = check_operand(q_out, q_out_stride, T, Hq, dh, eb)) != MEDUSA_OK) return st;
-  if ((st = check_overlap(q, q_stride, q_out, q_out_stride, T, Hq, dh, eb)) != MEDUSA_OK) return st;
+  const Span sq{q, q_stride, Hq}, sqo{q_out, q_out_stride, Hq};
+  if ((st = check_in_place(sq, sqo, T, dh, eb)) != MEDUSA_OK) return st;
   if (k != nullptr) {
     if ((st = check_operand(k, k_stride, T, Hkv, dh, eb)) != MEDUSA_OK) return st;
     if ((st = check_operand(k_out, k_out_stride, T, Hkv, dh, eb)) != MEDUSA_OK) return st;
-    if ((st = check_overlap(k, k_stride, k_out, k_out_stride, T, Hkv, dh, eb)) != MEDUSA_OK)
-      return st;
+    const Span sk{k, k_stride, Hkv}, sko{k_out, k_out_stride, Hkv};
+    if ((st = check_in_place(sk, sko, T, dh, eb)) != MEDUSA_OK) return st;
+    if (overlap(sqo, sk, T, dh, eb) || overlap(sko, sq, T, dh, eb) || overlap(sqo, sko, T, dh, eb))
+      return fail(MEDUSA_ERR_INVALID_ARG, "rope: q's and k's operands overlap");
   }
   return medusa::rope(*rope, q, q_stride, k, k_stride, dt, positions, T, Hq, Hkv, dh,
                       inverse ? 1 : 0, q_out, q_out_stride, k_out, k_out_stride,
@@ -145,8 +159,10 @@ medusa_status_t medusa_rope_append(const medusa_rope_t* rope, const void* q, lon
   if (q != nullptr) {
     if ((st = check_operand(q, q_stride, T, Hq, dh, eb)) != MEDUSA_OK) return st;
     if ((st = check_operand(q_out, q_out_stride, T, Hq, dh, eb)) != MEDUSA_OK) return st;
-    if ((st = check_overlap(q, q_stride, q_out, q_out_stride, T, Hq, dh, eb)) != MEDUSA_OK)
-      return st;
+    const Span sqo{q_out, q_out_stride, Hq};
+    if ((st = check_in_place({q, q_stride, Hq}, sqo, T, dh, eb)) != MEDUSA_OK) return st;
+    if (overlap(sqo, {k, k_stride, Hkv}, T, dh, eb) || overlap(sqo, {v, v_stride, Hkv}, T, dh, eb))
+      return fail(MEDUSA_ERR_INVALID_ARG, "rope_append: q_out overlaps k or v");
   }
   return medusa::rope_append(rope, q, q_stride, k, k_stride, v, v_stride, dt, positions, cu_q,
                              kv_len, B, T, Hq, Hkv, dh, q_out, q_out_stride, *pages, dev_status,
@@ -190,6 +206,8 @@ medusa_status_t medusa_chunk_attention(const void* q, long long q_stride,
   const size_t al = dt == MEDUSA_BF16 ? 16 : eb;
   if (!aligned(q, al) || !aligned(out, al))
     return fail(MEDUSA_ERR_ALIGNMENT, "chunk_attention: q or out misaligned");
+  if (overlap({q, q_stride, Hq}, {out, (long long)Hq * dh, Hq}, T, dh, eb))
+    return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention: out overlaps q");
   const size_t need = medusa::chunk_attention_workspace_size(Hq, Hkv, dh, dt);
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
     return fail(MEDUSA_ERR_WORKSPACE, "chunk_attention: workspace null, misaligned or too small");

@@ -126,7 +126,8 @@ class DecodeVerifyStep:
             stream=None) -> None:
         """Enqueue one step on ``stream``.  Kc/Vc/prefix_len are updated in place
         (tree K/V written, then the kept branch compacted, prefix advanced).
-        With a rotation q and k_new come unrotated.  Each call sits in an NVTX range of its name (for ncu --nvtx filters)."""
+        With a rotation q and k_new come unrotated.  Each call sits in an NVTX
+        range of its name (for ncu --nvtx filters)."""
         with nvtx.range("medusa_heads_topk_tree"):
             M.medusa_heads_topk_tree(h, W1, b1, W2, self.kmax, self.topk_ids, self.topk_vals,
                                      self.tree, root_tok, prefix_len, self.cand_ids, self.pos_ids,

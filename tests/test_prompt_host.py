@@ -61,6 +61,43 @@ def test_rope_refusals(L):
     assert call(qs=512, qo=(1 << 20) + 2 * 200, qos=512) == 1
 
 
+def test_operands_that_share_memory_are_refused(L):
+    """q's and k's operands of one call, among packed slices and apart."""
+    r = _rope()
+    buf = 1 << 20
+
+    def call(q, k, qo, ko, st, sto=None, T=4):
+        sto = sto or st
+        return L.medusa_rope(ctypes.addressof(r), q, st, k, st, 0, 4096, T, 4, 2, 64, 0, qo, sto,
+                             ko, sto, None)
+
+    n = 4 * 64 * 2  # bytes of q's heads of a token
+    # q_out over k, k_out over q, q_out over k_out
+    assert call(buf, 2 * buf, 2 * buf, 3 * buf, 512) == 1
+    assert call(buf, 2 * buf, 3 * buf, buf + n - 64, 512) == 1
+    assert call(buf, 2 * buf, 3 * buf, 3 * buf + 64, 512) == 1
+    assert call(buf, buf + n, buf, buf + n - 128, 512) == 1  # k_out a head early, over q
+    assert call(buf, buf + n, 3 * buf, 3 * buf + n - 2, 512, T=1) == 1
+    assert b"overlap" in L.medusa_last_error()
+    pages = _pages()
+
+    def append(q, k, v, qo, st=1024):
+        return L.medusa_rope_append(ctypes.addressof(r), q, st, k, st, v, st, 0, None, 4096, 4096,
+                                    2, 4, 4, 2, 64, qo, st, ctypes.addressof(pages), None, None)
+
+    assert append(buf, 2 * buf, 3 * buf, 2 * buf + 64) == 1
+    assert append(buf, 2 * buf, 3 * buf, 3 * buf - 64) == 1
+    assert append(buf, buf + n, buf + n + 256, buf + n) == 1  # packed: q's result over k
+
+    def attend(q, qs, out, T=4):
+        return L.medusa_chunk_attention(q, qs, ctypes.addressof(pages), 0, 4096, 4096, 2, T, 4, 2,
+                                        128, 0.1, out, None, 0, None, None)
+
+    assert attend(buf, 512, buf) == 1 and attend(buf, 512, buf + 4 * 1024 - 16) == 1
+    assert attend(buf, 1024, buf + 1024) == 1     # out dense between q's strided rows
+    assert attend(buf, 512, buf + 1008, T=1) == 1
+
+
 def test_rope_append_refusals(L):
     def call(r=0, q=1 << 20, k=1 << 21, ks=128, vv=1 << 24, vs=128, dt=0, cu=4096, kv=4096, B=2,
              T=4, Hq=4, Hkv=2, dh=64, qo=1 << 22, pages=None):
