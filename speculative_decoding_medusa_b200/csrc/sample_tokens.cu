@@ -73,6 +73,7 @@ constexpr int kRank = 128;  // tokens of a list that are ranked against one anot
 // much 251), and two of this size fit on an SM.
 constexpr size_t kManyBytes = 65536;
 constexpr int kValues = 4096;  // bins of bf16 logits: 16 octaves of magnitude and a sign
+constexpr int kSubs = 4;       // parts of a block's tokens, each with its own counts
 constexpr int kExpTable = 256;
 constexpr float kMaxTemperature = 1e30f;  // 32 T must stay finite
 constexpr uint32_t kLowestKey = 0x00800000u;  // key of the lowest finite float
@@ -231,8 +232,10 @@ struct Shared {
   Bin bin;
   Cut cut;
   ValueCut value_cut;
-  unsigned long long tiny;  // bf16: weights of the tokens near zero
-  unsigned int far;         // finite tokens without weight or bin
+  unsigned int tiny[2][kSubs];  // bf16: weights of the tokens near zero (low, high words)
+  unsigned int far;             // finite tokens without weight or bin
+  int tie_sub;                  // the part with the last token of the cut's value that stays
+  unsigned int tie_n;           // how many of its tokens of that value do
   unsigned int n_local;
   int cut_id, n_th;
   unsigned long long red64[kWarps], red64b[kWarps];
@@ -244,7 +247,7 @@ struct Shared {
 // dynamic shared memory after the slice: histogram (counts, low and high words
 // of the mass), short lists and group sums of every block
 __host__ __device__ constexpr size_t sample_extra_smem(int C) {
-  static_assert(3 * kBins * 4 + kList * 8 >= 2 * kValues * 4, "weights of bf16 values");
+  static_assert(3 * kBins * 4 + kList * 8 >= 2 * kValues * 4, "counts of bf16 values");
   return 3 * kBins * 4 + kList * 8 + (size_t)C * kGroups * sizeof(Sums);
 }
 
@@ -490,11 +493,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     return z > below && z <= top && (only < 0 || bin0(z) == static_cast<uint32_t>(only));
   };
 
-  // where tokens go by id, warp w takes the quads [w * seg, (w + 1) * seg) of
-  // the slice, 32 at a time
-  const int seg = (n_quad + kWarps * 32 - 1) / (kWarps * 32) * 32;
-  const int v_begin = warp * seg, v_end = min(n_quad, v_begin + seg);
-  const int run = (seg / 32 + 31) / 32;  // rows of 32 quads of a warp to a lane
+  // where tokens go by id, warps take contiguous runs of the quads [q0, q1),
+  // 32 at a time
+  int v_begin, v_end, run;  // run: rows of 32 quads of a warp to a lane
+  auto span_of = [&](int q0, int q1) {
+    const int seg = (q1 - q0 + kWarps * 32 - 1) / (kWarps * 32) * 32;
+    v_begin = min(q1, q0 + warp * seg);
+    v_end = min(q1, v_begin + seg);
+    run = (seg / 32 + 31) / 32;
+  };
+  span_of(0, n_quad);
 
   auto p_limit = [&](unsigned long long total) {
     // kept while the mass before is below top_p * total: an integer limit
@@ -595,10 +603,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     const float cut_z = value_of(cut_key);
     return z > cut_z || (z == cut_z && id <= cut_id);
   };
-  // This warp's tokens that stay, by a function for their weights.  Their mass
-  // goes to `mine` by runs of `run` rows of 32 quads, a lane for each.
+  // four independent weights, then the ones that stay
+  auto weights = [&](const float (&z)[4], const bool (&in)[4], unsigned long long (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = weight(z[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = in[i] ? w[i] : 0ull;
+  };
+  // This warp's tokens that stay, by their weights.  Their mass goes to `mine`
+  // by runs of `run` rows of 32 quads, a lane for each.
   unsigned long long mine = 0ull;
-  auto kept_of = [&](const auto& w_of) -> Sums {
+  auto kept_of = [&]() -> Sums {
     mine = 0ull;
     unsigned int count = 0u;
     int first = 0x7fffffff;
@@ -616,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
         if (in[0] || in[1] || in[2] || in[3]) {
           unsigned long long w[4];
-          w_of(z, in, w);
+          weights(z, in, w);
           mass = (w[0] + w[1]) + (w[2] + w[3]);
 #pragma unroll
           for (int i = 3; i >= 0; --i) {
@@ -676,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   };
   // the token that holds the target, if this warp has it: `before` is the mass
   // in front of the block, sh.red64 the warps'
-  auto pick = [&](const auto& w_of, unsigned long long target, unsigned long long before) {
+  auto pick = [&](unsigned long long target, unsigned long long before) {
 #pragma unroll 1
     for (int w = 0; w < warp; ++w) before += sh.red64[w];
     if (target < before || target >= before + sh.red64[warp]) return;
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         Elem<T>::unpack(quads[v], z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) in[i] = stays(z[i], base + v * 4 + i);
-        w_of(z, in, w);
+        weights(z, in, w);
       }
       const unsigned long long n = (w[0] + w[1]) + (w[2] + w[3]);
       unsigned long long s = n;
@@ -769,6 +784,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   // bin, with the sum of their weights), and 4096 weights serve the row.  The
   // cut is then a value and how many of its tokens stay.  Where it falls among
   // the magnitudes below, the row is cut as one in fp32 is.
+  // The block's tokens are counted in kSubs parts (16-bit counts, two to a
+  // word): the masses of the parts follow from the counts, and the draw looks
+  // at the tokens of one part alone.
   if constexpr (sizeof(T) == 2) {
     const int e = min(254, (__float_as_int(fmaxf(fabsf(hi), fabsf(weight.floor))) >> 23) & 255);
     const int least = max(0, e - 15) << 7;  // magnitude bits of the shared bin's largest
@@ -779,61 +797,76 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
                              static_cast<uint32_t>(sign) << 31);
     };
     const float z_tiny = __uint_as_float(static_cast<uint32_t>(least) << 16);
+    // parts 2 h and 2 h + 1 of a bin: the halves of cnt[h * kValues + bin]
     uint32_t* cnt = h_cnt;
+    const int part = (n_vec + kSubs - 1) / kSubs;  // vectors of a part
+    static_assert(kSubs == 4, "two words of two counts");
+    auto both = [](uint32_t word) { return (word & 0xffffu) + (word >> 16); };
+    auto tiny_of = [&](int x) {
+      return static_cast<unsigned long long>(sh.tiny[1][x]) << 32 | sh.tiny[0][x];
+    };
 #pragma unroll
-    for (int i = 0; i < kValues / kThreads; ++i) cnt[i * kThreads + tid] = 0u;
-    if (tid == 0) {
-      sh.tiny = 0ull;
-      sh.far = 0u;
-    }
+    for (int i = 0; i < 2 * kValues / 4; i += kThreads)
+      reinterpret_cast<uint4*>(cnt)[i + tid] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 2 * kSubs) sh.tiny[tid / kSubs][tid % kSubs] = 0u;
+    if (tid == 0) sh.far = 0u;
     __syncthreads();
     {
-      unsigned long long tiny = 0ull;
-      unsigned int n_tiny = 0u, far = 0u;
-#pragma unroll 2
+      unsigned int far = 0u;
+#pragma unroll 1
       for (int v = tid; v < n_vec; v += kThreads) {
         const uint4 raw = slice[v];
         const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
+        const int sub = (v >= part) + (v >= 2 * part) + (v >= 3 * part);
+        uint32_t* counts = cnt + (sub >> 1) * kValues;
+        const uint32_t one = sub & 1 ? 0x10000u : 1u;
+        unsigned int near = 0u;  // tokens of the shared bin, a bit each
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t bits = i & 1 ? word[i / 2] >> 16 : word[i / 2] & 0xffffu;
           const int mag = static_cast<int>(bits & 0x7fffu) - least;
           if (mag > 0 && mag < kHalf) {
-            atomicAdd(&cnt[mag ^ (kTiny + (bits >> 15))], 1u);
+            atomicAdd(&counts[mag ^ (kTiny + (bits >> 15))], one);
           } else if (mag <= 0) {
-            ++n_tiny;
-            tiny += weight(__uint_as_float(bits << 16));
+            near |= 1u << i;
           } else if (bits != 0xff80u) {
             ++far;
           }
         }
-      }
-      if (__any_sync(0xffffffffu, n_tiny > 0u)) {
-        tiny = warp_sum(tiny);
-        n_tiny = __reduce_add_sync(0xffffffffu, n_tiny);
-        if (lane == 0) {
-          atomicAdd(&cnt[kTiny], n_tiny);
-          atomicAdd(&sh.tiny, tiny);
+        if (near != 0u) {
+          unsigned long long w = 0ull;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i)
+            if ((near >> i) & 1u)
+              w += weight(__uint_as_float(reinterpret_cast<const uint16_t*>(slice + v)[i] << 16));
+          atomicAdd(&counts[kTiny], __popc(near) * one);
+          const uint32_t lo = static_cast<uint32_t>(w);
+          const uint32_t carry = atomicAdd(&sh.tiny[0][sub], lo) + lo < lo ? 1u : 0u;
+          atomicAdd(&sh.tiny[1][sub], static_cast<uint32_t>(w >> 32) + carry);
         }
       }
       if (far > 0u) atomicAdd(&sh.far, far);
     }
     __syncthreads();
     // the sums of every group of 64 bins to every block
-    auto mass_of = [&](int bin, uint32_t n) {
-      return bin == kTiny ? sh.tiny : n > 0u ? n * weight(value(bin)) : 0ull;
-    };
     {
       // eight bins a thread, eight threads a group
-      const uint4 a = reinterpret_cast<const uint4*>(cnt)[2 * tid];
-      const uint4 c = reinterpret_cast<const uint4*>(cnt)[2 * tid + 1];
-      const uint32_t n[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
       unsigned long long m = 0ull;
       unsigned int k = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m += mass_of(tid * 8 + i, n[i]);
-        k += n[i];
+      for (int i = 0; i < 8; i += 4) {
+        const uint4 a = reinterpret_cast<const uint4*>(cnt)[2 * tid + i / 4];
+        const uint4 c = reinterpret_cast<const uint4*>(cnt + kValues)[2 * tid + i / 4];
+        const uint32_t n[4] = {both(a.x) + both(c.x), both(a.y) + both(c.y), both(a.z) + both(c.z),
+                               both(a.w) + both(c.w)};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int bin = tid * 8 + i + x;
+          if (n[x] > 0u)
+            m += bin == kTiny ? tiny_of(0) + tiny_of(1) + tiny_of(2) + tiny_of(3)
+                              : n[x] * weight(value(bin));
+          k += n[x];
+        }
       }
 #pragma unroll
       for (int o = 1; o < 8; o *= 2) {
@@ -844,7 +877,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         *cluster.map_shared_rank(&group[rank * kGroups + tid / 8], tid % 8) = Sums{m, k, 0};
     }
     if (tid < C) {
-      *cluster.map_shared_rank(&sh.list_mass[rank], tid) = sh.tiny;
+      *cluster.map_shared_rank(&sh.list_mass[rank], tid) =
+          tiny_of(0) + tiny_of(1) + tiny_of(2) + tiny_of(3);
       *cluster.map_shared_rank(&sh.list_n[rank], tid) = sh.far;
     }
     cluster.sync();
@@ -860,18 +894,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         if (lane == 0) sh.value_cut.bin = kValues;
         __syncwarp();
         const int bin = min(g.bin, kGroups - 1u) * 64 + 2 * lane;
-        uint2 n[kMaxCluster];  // all reads in flight
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          n[c] = c < C ? *reinterpret_cast<const uint2*>(&cluster.map_shared_rank(cnt, c)[bin])
-                       : make_uint2(0u, 0u);
-        unsigned long long tiny = 0ull;
         uint2 s = make_uint2(0u, 0u);
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-          s.x += n[c].x;
-          s.y += n[c].y;
+        for (int half = 0; half < 2; ++half) {
+          uint2 n[kMaxCluster];  // reads in flight
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c)
+            n[c] = c < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(cnt, c) +
+                                                           half * kValues + bin)
+                         : make_uint2(0u, 0u);
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c) {
+            s.x += both(n[c].x);
+            s.y += both(n[c].y);
+          }
         }
+        unsigned long long tiny = 0ull;
         if (bin + 1 == kTiny) {
 #pragma unroll 1
           for (int c = 0; c < C; ++c) tiny += sh.list_mass[c];
@@ -890,7 +928,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
         const bool second = (by_mass ? m1 > 0ull : s.y > 0u) &&
                             (by_mass ? m + m0 : (unsigned long long)(k + s.x)) < g.limit;
         const unsigned int votes = __ballot_sync(0xffffffffu, first || second);
-        if (g.bin < kGroups && lane == 31 - __clz(votes)) {
+        if (g.bin < kGroups && votes != 0u) {
+          const int from = 31 - __clz(votes);
           ValueCut c{};
           c.bin = bin + (second ? 1 : 0);
           const unsigned long long one = second ? w[1] : w[0];
@@ -899,23 +938,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
             k += s.x;
           }
           const unsigned int here = second ? s.y : s.x;
-          const unsigned long long room = g.limit - (by_mass ? m : (unsigned long long)k);
-          c.ties = static_cast<unsigned int>(
-              min((unsigned long long)here, by_mass && one > 0ull ? (room + one - 1) / one : room));
+          if (lane == from) {
+            const unsigned long long room = g.limit - (by_mass ? m : (unsigned long long)k);
+            c.ties = static_cast<unsigned int>(
+                min((unsigned long long)here, by_mass && one > 0ull ? (room + one - 1) / one : room));
+          }
           c.mass = m + c.ties * one;
           c.count = k + c.ties;
-          c.owner = C;
-          bool found = false;
-#pragma unroll
-          for (int b = 0; b < kMaxCluster; ++b) {
-            const unsigned int y = second ? n[b].y : n[b].x;
-            if (!found && b < C && c.before + y > c.ties) {
-              found = true;
-              c.owner = b;
-            }
-            if (!found) c.before += y;
+          // the first block whose tokens of the value do not all stay
+          const int cut_bin = __shfl_sync(0xffffffffu, static_cast<int>(c.bin), from);
+          const unsigned int ties = __shfl_sync(0xffffffffu, c.ties, from);
+          unsigned int y = 0u;
+          if (lane < C) {
+            const uint32_t* counts = cluster.map_shared_rank(cnt, lane) + cut_bin;
+            y = both(counts[0]) + both(counts[kValues]);
           }
-          sh.value_cut = c;
+          unsigned long long none = 0ull;
+          unsigned int sum = y;
+          scan(none, sum);
+          const unsigned int over = __ballot_sync(0xffffffffu, sum > ties);
+          c.owner = over != 0u ? __ffs(over) - 1 : C;
+          c.before = __shfl_sync(0xffffffffu, sum - y, over != 0u ? c.owner : 31);
+          if (lane == from) sh.value_cut = c;
         }
       }
       __syncthreads();
@@ -941,63 +985,81 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       const float cut_z = value_of(cut_key);
       const bool split = cut.bin < kValues && key_of(value(cut.bin)) == cut_key;
       if (split) cut_id = rank < cut.owner ? 0x7fffffff : -1;
-      // this block's tokens that stay
-      unsigned long long m = 0ull;
+      // this block's tokens that stay, by part
+      unsigned long long m[kSubs] = {};
       unsigned int k = 0u;
-#pragma unroll 2
+#pragma unroll 1
       for (int i = 0; i < kValues / kThreads; ++i) {
         const int bin = i * kThreads + tid;
         const float z = value(bin);
-        unsigned int n = cnt[bin];
-        if (split && z == cut_z)
-          n = rank < cut.owner ? n : rank == cut.owner ? cut.ties - cut.before : 0u;
-        else if (z < cut_z)
-          n = 0u;
-        if (n > 0u) {
-          m += mass_of(bin, n);
-          k += n;
+        const uint32_t a = cnt[bin], c = cnt[kValues + bin];
+        if (z < cut_z || (a | c) == 0u) continue;
+        uint32_t n[kSubs] = {a & 0xffffu, a >> 16, c & 0xffffu, c >> 16};
+        if (split && z == cut_z) {
+          // the first of its tokens stay
+          uint32_t left = rank < cut.owner ? 0xffffffffu
+                                           : rank == cut.owner ? cut.ties - cut.before : 0u;
+          bool cut_here = true;
+#pragma unroll
+          for (int x = 0; x < kSubs; ++x) {
+            if (left < n[x]) {
+              if (cut_here) {
+                sh.tie_sub = x;
+                sh.tie_n = left;
+                cut_here = false;
+              }
+              n[x] = left;
+            }
+            left -= n[x];
+          }
+        }
+        const unsigned long long w = bin == kTiny ? 0ull : weight(z);
+#pragma unroll
+        for (int x = 0; x < kSubs; ++x) {
+          m[x] += bin == kTiny ? tiny_of(x) : n[x] * w;
+          k += n[x];
         }
       }
-      exchange(Sums{warp_sum(m), __reduce_add_sync(0xffffffffu, k), 0});
+      exchange(Sums{warp_sum((m[0] + m[1]) + (m[2] + m[3])), __reduce_add_sync(0xffffffffu, k), 0});
       unsigned long long before = 0ull;
       const Sums all = total_of(before);
       if (rank == 0 && tid == 0 && p.kept != nullptr)
         p.kept[r] = static_cast<int>(all.count + (cut_key == kLowestKey ? far : 0u));
       const unsigned long long target = target_of(all.mass);
       if (target < before || target >= before + sh.part[rank].mass) return;
-      // This block draws.  Its counts make way for weights, which no other
-      // block reads any more.
-      unsigned long long* table = reinterpret_cast<unsigned long long*>(cnt);
-      if (split && rank == cut.owner)
-        cut_id = cut.ties > cut.before ? nth_of(cut_z, cut.ties - cut.before) : -1;
-      const uint4 a = reinterpret_cast<const uint4*>(cnt)[2 * tid];
-      const uint4 c = reinterpret_cast<const uint4*>(cnt)[2 * tid + 1];
-      const uint32_t n[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+      // This block draws: the part that holds the target, then its token.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int x = 0; x < kSubs - 1; ++x) m[x] += __shfl_xor_sync(0xffffffffu, m[x], o);
+      if (lane == 0) {
+#pragma unroll
+        for (int x = 0; x < kSubs - 1; ++x) sh.word[x * kWarps + warp] = m[x];
+      }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n[i] > 0u) table[tid * 8 + i] = weight(value(tid * 8 + i));
-      __syncthreads();
-      auto looked_up = [&](const float (&z)[4], const bool (&in)[4], unsigned long long (&w)[4]) {
-        bool near = false;
+      for (int x = 0; x < kSubs - 1; ++x) m[x] = sh.word[x * kWarps + lane % kWarps];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t bits = __float_as_uint(z[i]) >> 16;
-          const int mag = static_cast<int>(bits & 0x7fffu) - least;
-          near = near || (in[i] && mag <= 0);
-          w[i] = 0ull;
-          if (in[i] && mag > 0 && mag < kHalf) w[i] = table[mag ^ (kTiny + (bits >> 15))];
-        }
-        if (near) {
+      for (int o = kWarps / 2; o > 0; o >>= 1)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (in[i] && fabsf(z[i]) <= z_tiny) w[i] = weight(z[i]);
+        for (int x = 0; x < kSubs - 1; ++x) m[x] += __shfl_xor_sync(0xffffffffu, m[x], o);
+      int sub = 0;
+#pragma unroll
+      for (int x = 0; x < kSubs - 1; ++x) {
+        if (sub == x && target >= before + m[x]) {
+          before += m[x];
+          ++sub;
         }
-      };
-      const Sums own = kept_of(looked_up);
+      }
+      span_of(min(n_vec, sub * part) * (VE / 4), min(n_vec, (sub + 1) * part) * (VE / 4));
+      if (split && rank == cut.owner) {
+        if (sub < sh.tie_sub) cut_id = 0x7fffffff;
+        else if (sub == sh.tie_sub && sh.tie_n > 0u) cut_id = nth_of(cut_z, sh.tie_n);
+      }
+      const Sums own = kept_of();
       if (lane == 0) sh.red64[warp] = own.mass;
       __syncthreads();
-      pick(looked_up, target, before);
+      pick(target, before);
       return;
     }
     cut_key = kLowestKey;
@@ -1461,14 +1523,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   take_min_p();
 
   // ---- the draw: kept mass in id order ----
-  // four independent weights, then the ones that stay
-  auto weights = [&](const float (&z)[4], const bool (&in)[4], unsigned long long (&w)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = weight(z[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = in[i] ? w[i] : 0ull;
-  };
-  exchange(kept_of(weights));
+  exchange(kept_of());
   unsigned long long before = 0ull;
   const Sums all = total_of(before);
   if (rank == 0 && tid == 0 && p.kept != nullptr) p.kept[r] = static_cast<int>(all.count);
@@ -1476,7 +1531,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     if (rank == 0 && tid == 0) p.tokens[r] = all.first;
     return;
   }
-  pick(weights, target_of(all.mass), before);
+  pick(target_of(all.mass), before);
 }
 
 template <typename T>
