@@ -38,11 +38,12 @@
 //
 // Bound by latency: few rows by the chain of three or four cluster barriers
 // with a pass between them, many rows by the same chain two blocks at a time
-// on an SM (one block's loads and shared-memory atomics run under the other's
-// barriers).  One row of 32000 (fp32, top-k and top-p) 12.4 us; 8 rows of
-// 128256 (bf16, top-p) 20 us; 512 of them with settings of their own 165 us,
-// 0.8 TB/s.  With the weights of all tokens added into bins, as in fp32, the
-// bf16 rows took 44 and 269 us.
+// on an SM and by the shared-memory atomics of the count (about six cycles a
+// warp's; computing the bins with half the instructions changed nothing).  One
+// row of 32000 (fp32, top-k and top-p) 12.4 us; 8 rows of 128256 (bf16, top-p)
+// 17 us; 512 of them with settings of their own 158 us, 0.83 TB/s.  With the
+// weights of all tokens added into bins, as in fp32, the bf16 rows took 44 and
+// 269 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
