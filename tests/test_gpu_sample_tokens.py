@@ -96,6 +96,14 @@ def test_flat_rows_and_ties():
             assert tok == [int(x * n) for x, n in zip(u, kept)]
 
 
+def test_the_longest_row_of_one_value():
+    """Every count of a block in one bin."""
+    for dtype, V in ((torch.bfloat16, 655360), (torch.float32, 327680)):
+        z = torch.full((3, V), 1.5).to(dtype)
+        assert _run(z, [0.5, 0.25, 0.875], top_p=[1.0, 0.5, 0.25]) == (
+            [V // 2, V // 8, 7 * V // 32], [V, V // 2, V // 4])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_few_distinct_values(dtype):
     """Crowded bins: a handful of values over a large vocabulary, cuts inside
