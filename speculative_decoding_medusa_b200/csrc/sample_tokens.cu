@@ -40,8 +40,8 @@
 // with a pass between them, many rows by the same chain two blocks at a time
 // on an SM and by the shared-memory atomics of the count (about six cycles a
 // warp's; computing the bins with half the instructions changed nothing).  One
-// row of 32000 (fp32, top-k and top-p) 12.4 us; 8 rows of 128256 (bf16, top-p)
-// 17 us; 512 of them with settings of their own 158 us, 0.83 TB/s.  With the
+// row of 32000 (fp32, top-k and top-p) 11.9 us; 8 rows of 128256 (bf16, top-p)
+// 16.6 us; 512 of them with settings of their own 158 us, 0.83 TB/s.  With the
 // weights of all tokens added into bins, as in fp32, the bf16 rows took 44 and
 // 269 us.
 #include <cooperative_groups.h>
@@ -254,8 +254,6 @@ __host__ __device__ constexpr size_t sample_extra_smem(int C) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
   constexpr int VE = 16 / sizeof(T);  // tokens of a 16-byte vector
   using Quad = typename Elem<T>::Quad;
   cg::cluster_group cluster = cg::this_cluster();
@@ -277,6 +275,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   Sums* group = reinterpret_cast<Sums*>(list + kList);
   const int cap = kList / C;
   __shared__ Shared sh;
+
+  // the cluster's blocks must all run before one writes to another's memory:
+  // the wait is at the first such write
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // what needs no input, while an earlier kernel ends: the table of powers,
+  // cleared counts
+  if (tid < kExpTable) sh.table[tid] = exp2((double)tid / kExpTable);
+  if constexpr (sizeof(T) == 2) {
+    for (int i = tid; i < 2 * kValues / 4; i += kThreads)
+      reinterpret_cast<uint4*>(h_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 2 * kSubs) sh.tiny[tid / kSubs][tid % kSubs] = 0u;
+    if (tid == 0) sh.far = 0u;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
 
   const float temp = p.temperature != nullptr ? p.temperature[r] : 1.f;
   const float u = p.u[r];
@@ -324,8 +337,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
           }
         }
       }
-      // the table of powers, while the first loads are under way
-      if (v0 < kExpTable) sh.table[v0] = exp2((double)v0 / kExpTable);
 #pragma unroll
       for (int f = 0; f < kFetch; ++f) {
         const int v = v0 + f * kThreads;
@@ -335,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       }
     }
   }
-  if (tid >= n_vec && tid < kExpTable) sh.table[tid] = exp2((double)tid / kExpTable);
   const float own_hi = hi;  // the largest of this thread's tokens
   for (int o = 16; o > 0; o >>= 1)
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
@@ -389,6 +399,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
       __syncthreads();
     }
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (tid < C) {
     hi = sh.redf[0];
     for (int w = 1; w < kWarps; ++w) hi = max_nan(hi, sh.redf[w]);
@@ -806,12 +818,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
     auto tiny_of = [&](int x) {
       return static_cast<unsigned long long>(sh.tiny[1][x]) << 32 | sh.tiny[0][x];
     };
-#pragma unroll
-    for (int i = 0; i < 2 * kValues / 4; i += kThreads)
-      reinterpret_cast<uint4*>(cnt)[i + tid] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < 2 * kSubs) sh.tiny[tid / kSubs][tid % kSubs] = 0u;
-    if (tid == 0) sh.far = 0u;
-    __syncthreads();
     {
       unsigned int far = 0u;
 #pragma unroll 1
