@@ -511,26 +511,33 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
     s[6] = p.cu_q[lo + 1] - s[5];
     s[7] = p.kv_len[lo];
   }
-  for (int g0 = 0;; g0 += 32) {
-    // beyond the last group the costs only have to be positive
-    const int n = group_cost(s[6], s[7], g0 + lane, p);
-    int c = n;
+  if (s[6] <= 2 * p.tpt) {
+    // one query group (single tokens, short chunks)
+    const int wt = group_mt(s[6], 0, p) == 2 ? kTwoCost : kOneCost;
+    s[3] = (rem + wt - 1) / wt;
+    s[4] = t0 - rem;
+  } else {
+    for (int g0 = 0;; g0 += 32) {
+      // beyond the last group the costs only have to be positive
+      const int n = group_cost(s[6], s[7], g0 + lane, p);
+      int c = n;
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += a;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += a;
+      }
+      const unsigned int over = __ballot_sync(0xffffffffu, c > rem);
+      if (over != 0u) {
+        const int at = __ffs(over) - 1;
+        const int in = __shfl_sync(0xffffffffu, rem - (c - n), at);  // t0 within the segment
+        const int wt = group_mt(s[6], g0 + at, p) == 2 ? kTwoCost : kOneCost;
+        s[2] = g0 + at;
+        s[3] = (in + wt - 1) / wt;
+        s[4] = t0 - in;
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, c, 31);
     }
-    const unsigned int over = __ballot_sync(0xffffffffu, c > rem);
-    if (over != 0u) {
-      const int at = __ffs(over) - 1;
-      const int in = __shfl_sync(0xffffffffu, rem - (c - n), at);  // t0 within the segment
-      const int wt = group_mt(s[6], g0 + at, p) == 2 ? kTwoCost : kOneCost;
-      s[2] = g0 + at;
-      s[3] = (in + wt - 1) / wt;
-      s[4] = t0 - in;
-      break;
-    }
-    rem -= __shfl_sync(0xffffffffu, c, 31);
   }
   Cursor c;
   c.init(s, t1, p);
