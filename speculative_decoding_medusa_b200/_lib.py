@@ -1,11 +1,14 @@
 """ctypes binding of libmedusa_b200.so: one Python function per C entry point,
 same names, argument marshalling only (tensor -> pointer and sizes, stream
 handle).  Every step of the computation runs in the library's CUDA kernels;
-there is no fallback: a missing library or a non-OK status raises.
+there is no fallback: a missing library or a non-OK status raises.  The prompt
+side's calls, the shortest, are marshalled by an extension (csrc/marshal.cpp).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -498,9 +501,30 @@ def medusa_verify_from_records(records, cand_logit, cand_ids, tree: Tree, V: int
 # ---------------------------------------------------------------------------
 
 
-# These calls are short enough for the marshalling to show, so an argument is
-# checked with as few tensor queries as possible: one test of the common case,
-# and the reasons only when it fails.
+# These calls are short enough for the marshalling to show: on the current
+# stream an extension checks the tensors and makes the C call at once.  What it
+# does not take (-1), and calls on another stream, go through ctypes below; a
+# refusal is told its reason there.
+
+_fast = None
+
+
+def _marshal():
+    """The extension, bound to the library."""
+    global _fast
+    if _fast is None:
+        L = lib()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: run "
+                               "`python -m speculative_decoding_medusa_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.medusa_rope, L.medusa_rope_append, L.medusa_chunk_attention,
+            L.medusa_sample_tokens)))
+        _fast = m
+    return _fast
 
 
 def _dev() -> int:
@@ -619,6 +643,11 @@ def medusa_rope(rope: Rope, q, k, positions, q_out, k_out, inverse: bool = False
     """q [T,Hq,dh], k [T,Hkv,dh] (or None) rotated at positions [T] int32 into
     q_out, k_out (which may be q and k themselves).  inverse: by the negative
     angle (the gradient of the forward call)."""
+    if stream is None:
+        st = (_fast or _marshal()).rope(rope._ref, rope.turns, q, k, positions, q_out, k_out,
+                                        inverse)
+        if st >= 0:
+            return _check(st) if st else None
     dev = _dev()
     qsh, dtype = _3d(q, "q"), q.dtype
     T, Hq, dh = qsh
@@ -647,6 +676,12 @@ def medusa_rope_append(rope: Optional[Rope], q, k, v, cu_q, kv_len, q_out, cache
     """The new tokens q [T,Hq,dh] (or None), k, v [T,Hkv,dh] of cache.B
     sequences: q rotated into q_out, k rotated and v copied into the cache at
     slots kv_len[b] - (cu_q[b+1] - cu_q[b]) .. kv_len[b] - 1."""
+    if stream is None:
+        ref, turns = (rope._ref, rope.turns) if rope is not None else (None, None)
+        st = (_fast or _marshal()).append(ref, turns, q, k, v, cu_q, kv_len, q_out, cache._ref,
+                                          cache.K, cache.B, positions, dev_status)
+        if st >= 0:
+            return _check(st) if st else None
     dev = _dev()
     ksh, dtype = _3d(k, "k"), cache.K.dtype
     T, Hkv, dh = ksh
@@ -690,6 +725,12 @@ def medusa_chunk_attention(q, cache: PagedCache, cu_q, kv_len, out,
     """q [T,Hq,dh] of cache.B sequences' new tokens (their k and v already in
     the cache) -> out [T,Hq,dh], each token over its sequence's slots up to its
     own."""
+    if stream is None and ws is not None:
+        st = (_fast or _marshal()).attention(q, cache._ref, cache.K, cu_q, kv_len, out, cache.B,
+                                             cache.dh ** -0.5 if scale is None else scale, ws,
+                                             dev_status)
+        if st >= 0:
+            return _check(st) if st else None
     dev = _dev()
     qsh, dtype = _3d(q, "q"), cache.K.dtype
     T, Hq, dh = qsh
@@ -721,6 +762,11 @@ def medusa_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=
     """tokens [R] int32 drawn from logits [n_rows,V] (rows may be strided) with
     uniform numbers u [R]; temperature, top_p, min_p [R] fp32 and top_k [R]
     int32 are off when None; row_idx [R] picks each draw's row."""
+    if stream is None:
+        st = (_fast or _marshal()).sample(logits, u, tokens, temperature, top_k, top_p, min_p,
+                                          row_idx, kept, dev_status)
+        if st >= 0:
+            return _check(st) if st else None
     dev = _dev()
     sh = logits.shape
     if len(sh) != 2 or logits.get_device() != dev or (sh[1] > 1 and logits.stride(1) != 1):

@@ -1,4 +1,5 @@
-"""Build the CUDA library libmedusa_b200.so in-tree with nvcc (sm_100a).
+"""Build the CUDA library libmedusa_b200.so in-tree with nvcc (sm_100a), and
+the Python extension _marshal.so with g++.
 
 Usage: python -m speculative_decoding_medusa_b200.build [--force]
 """
@@ -9,11 +10,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmedusa_b200.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -43,7 +46,33 @@ def _stale() -> bool:
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def _build_marshal(force: bool, verbose: bool) -> None:
+    src = os.path.join(CSRC, "marshal.cpp")
+    deps = [src, os.path.join(INCLUDE, "medusa.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(MARSHAL) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in deps):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (INCLUDE, sysconfig.get_paths()["include"], f"{root}/include",
+              f"{root}/include/torch/csrc/api/include", f"{cuda}/include"):
+        cmd += ["-I", d]
+    cmd += [src, "-L", f"{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-o", tmp]
+    if verbose:
+        print(" ".join(cmd))
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on marshal.cpp:\n" + r.stdout.decode())
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_marshal(force, verbose)
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()

@@ -164,3 +164,48 @@ def test_captured_prompt_chunk_follows_its_lengths():
     for a, b in zip(res[0][0], res[1][0]):
         assert torch.equal(a, b)
     assert torch.equal(res[0][1], res[1][1]) and torch.equal(res[0][2], res[1][2])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_calls_on_a_given_stream_and_on_the_current_one(dtype):
+    """The two ways a call is marshalled (the extension on the current stream,
+    ctypes on a stream that is given): the same launches, packed slices and
+    missing operands included, and the same refusals."""
+    dev = "cuda"
+    g = torch.Generator(device=dev).manual_seed(5)
+    B, T, Hq, Hkv, dh, page = 2, 7, 4, 2, 64, 8
+    packed = torch.randn(T, Hq + 2 * Hkv, dh, generator=g, device=dev).to(dtype)
+    q, k, v = packed[:, :Hq], packed[:, Hq:Hq + Hkv], packed[:, Hq + Hkv:]
+    i32 = dict(dtype=torch.int32, device=dev)
+    cu, kv = torch.tensor([0, 3, 7], **i32), torch.tensor([10, 12], **i32)
+    rope = M.Rope(32, theta=1e4)
+    logits = torch.randn(B, 100, generator=g, device=dev).to(dtype)
+    u = torch.rand(B, generator=g, device=dev)
+    got = []
+    for stream in (None, torch.cuda.current_stream()):
+        K, V = torch.zeros(2, 4, Hkv, page, dh, dtype=dtype, device=dev)
+        cache = M.PagedCache(K, V, torch.arange(4, **i32).view(2, 2))
+        q_rot, out, k_rot = torch.zeros(2, T, Hq, dh, dtype=dtype, device=dev).unbind() + (
+            torch.zeros(T, Hkv, dh, dtype=dtype, device=dev),)
+        ws = M.workspace(M.medusa_chunk_attention_workspace_size(Hq, Hkv, dh, cache.dt), dev)
+        tok, kept = torch.zeros(2, B, **i32).unbind()
+        st = M.new_status()
+        M.medusa_rope(rope, q, k, torch.arange(T, **i32), q_rot, k_rot, inverse=True,
+                      stream=stream)
+        first = q_rot.clone()
+        M.medusa_rope_append(None, None, k, v, cu, kv, None, cache, dev_status=st, stream=stream)
+        M.medusa_rope_append(rope, q, k, v, cu, kv, q_rot, cache, dev_status=st, stream=stream)
+        M.medusa_chunk_attention(q_rot, cache, cu, kv, out, None, ws, st, stream)
+        M.medusa_sample_tokens(logits, u, tok, top_p=torch.full((B,), 0.9, device=dev), kept=kept,
+                               dev_status=st, stream=stream)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        got.append((first, k_rot, K, V, q_rot, out, tok, kept))
+        with pytest.raises(ValueError, match="dtype|CUDA"):
+            M.medusa_rope(rope, q, k.double(), torch.arange(T, **i32), q_rot, k_rot, stream=stream)
+        with pytest.raises(M.MedusaError, match="overlap"):
+            M.medusa_chunk_attention(out, cache, cu, kv, out, None, ws, st, stream)
+        with pytest.raises(ValueError, match="2 elements"):
+            M.medusa_sample_tokens(logits, u, tok[:1], stream=stream)
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and a.abs().sum() > 0

@@ -251,3 +251,22 @@ def test_oracle_sampling_pins():
     assert P.sample_row(z, 0.99, top_p=0.3)[:2] == (1, 1)
     assert P.sample_row(z, 0.5, min_p=0.3)[0] == 3
     assert P.sample_row(z, 0.5, temperature=0.0)[:2] == (1, 1)
+
+
+def test_marshalling_leaves_the_unusual_to_the_binding():
+    """The extension makes no call with what it cannot check: -1."""
+    m = _lib._marshal()
+    q, i = torch.zeros(4, 2, 64), torch.zeros(4, dtype=torch.int32)
+    r = M.Rope(64, device="cpu")
+    assert m.rope(r._ref, r.turns, q, None, i, q, None, False) == -1        # CPU tensors
+    assert m.rope(r._ref, r.turns, None, None, i, q, None, False) == -1
+    assert m.rope(r._ref, r.turns, [1.0], None, i, q, None, False) == -1
+    assert m.rope(r._ref) == -1
+    assert m.append(None, None, None, q, q, i, i, None, 0, q.view(4, 2, 1, 64), 3, None, None) == -1
+    assert m.append(None, None, None, q, q, i, i, None, 0, None, 3, None, None) == -1
+    assert m.attention(q, 0, q.view(4, 2, 1, 64), i, i, q, 3, 0.1, i, None) == -1
+    assert m.attention(q, 0, q, i, i, q, "three", 0.1, i, None) == -1
+    assert m.sample(q[0], i, i, None, None, None, None, None, None, None) == -1
+    assert m.sample(*[None] * 10) == -1
+    with pytest.raises(TypeError):
+        m.bind(1, 2)
