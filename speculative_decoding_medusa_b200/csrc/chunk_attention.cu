@@ -37,30 +37,49 @@ __global__ void __launch_bounds__(kWarps * 32) chunk_attn_f32_kernel(ChunkParams
   __shared__ float s_ml[kWarps][2];
   __shared__ float s_acc[kWarps][DH];
   const long long row = (long long)blockIdx.x * rows + warp / S;
-  int visible = 0, n = 0, t = 0, hq = 0;
+  int visible = 0, n = 0;
   bool live = row < (long long)p.T * p.Hq;
-  if (live) {
-    t = static_cast<int>(row / p.Hq);
-    hq = static_cast<int>(row - (long long)t * p.Hq);
-    for (int b = lane; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    live = n < p.B;  // not behind the last sequence
-  }
-  if (live) {
-    const int first = p.cu_q[n], len = p.cu_q[n + 1] - first, kv = p.kv_len[n];
-    if (first < 0 || t < first || first + len > p.T || kv < 0 ||
-        kv > (long long)p.max_pages * p.page_size) {
-      if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
-      live = false;
-    } else {
-      visible = max(0, kv - len + (t - first) + 1);
-    }
-  }
+  const int t = live ? static_cast<int>(row / p.Hq) : 0;
+  const int hq = live ? static_cast<int>(row - (long long)t * p.Hq) : 0;
+  // q needs no metadata: its load runs beside the chain lengths -> page -> keys
   float qv[PER], acc[PER], m = -INFINITY, l = 0.f;
   const float* qp = static_cast<const float*>(p.q) + t * p.q_stride + (size_t)hq * DH + lane * PER;
 #pragma unroll
+  for (int e = 0; e < PER; ++e) qv[e] = live ? qp[e] : 0.f;
+  if (live) {
+    int first = 0, end = 0, kv = 0;  // of sequence `lane`, then of the row's
+    if (lane < p.B) {
+      first = p.cu_q[lane];
+      end = p.cu_q[lane + 1];
+      kv = p.kv_len[lane];
+      n = end <= t ? 1 : 0;
+    }
+    for (int b = lane + 32; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    live = n < p.B;  // not behind the last sequence
+    if (live) {
+      if (n < 32) {
+        first = __shfl_sync(0xffffffffu, first, n);
+        end = __shfl_sync(0xffffffffu, end, n);
+        kv = __shfl_sync(0xffffffffu, kv, n);
+      } else {
+        first = p.cu_q[n];
+        end = p.cu_q[n + 1];
+        kv = p.kv_len[n];
+      }
+      const int len = end - first;
+      if (first < 0 || t < first || first + len > p.T || kv < 0 ||
+          kv > (long long)p.max_pages * p.page_size) {
+        if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+        live = false;
+      } else {
+        visible = max(0, kv - len + (t - first) + 1);
+      }
+    }
+  }
+#pragma unroll
   for (int e = 0; e < PER; ++e) {
-    qv[e] = live ? qp[e] * p.scale : 0.f;
+    qv[e] *= p.scale;
     acc[e] = 0.f;
   }
   const float* Kp = static_cast<const float*>(p.K) + lane * PER;
