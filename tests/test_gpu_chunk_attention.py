@@ -108,6 +108,21 @@ def test_fp32_head_sizes(dh):
     _check(_call(*c), *c)
 
 
+@pytest.mark.parametrize("G", [2, 3, 5, 8])
+@pytest.mark.parametrize("dh", [32, 128, 160, 256])
+def test_fp32_shared_heads(G, dh):
+    c = _case([(5, 40), (1, 9), (3, 3)], 2 * G, 2, dh, 16, f32, seed=dh + G, pad=2)
+    _check(_call(*c), *c)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+def test_many_sequences(dtype):
+    """More than a warp's lanes, some of them without new tokens."""
+    lens = [((b * 7) % 4, 4 + (b * 13) % 60) for b in range(75)]
+    c = _case(lens, 4, 2, 64, 8, dtype, seed=3, pad=1)
+    _check(_call(*c), *c)
+
+
 @pytest.mark.parametrize("dtype", [bf16, f32])
 @pytest.mark.parametrize("cap", [1, 3, 37, 100, 127, 129, 255, 400])
 def test_dense_caches(dtype, cap):
