@@ -351,11 +351,80 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
   }
 }
 
-// the widest vector every access allows: VEC elements must divide the pairs,
-// the head, every stride and (in bytes) every base address
-int vector_width(const RopeParams& p, int eb) {
+// A rotated part that whole vectors do not divide (an odd number of pairs, as
+// in rot = 34): a block per token holds the token's q, k and v in shared memory,
+// read and written by whole vectors whatever the rotation, and every element
+// finds its partner there.  8192 tokens of 32 + 8 heads of 128 with rot = 34
+// written into pages: 79 us, with vectors as narrow as the pairs allow 154.
+template <typename T, int VEC, bool kAppend>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_staged_kernel(RopeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  extern __shared__ __align__(16) uint8_t staged[];  // the token, cosines [rot / 2], sines
+  __shared__ Row s_row;
+  using V = Vec<T, VEC>;
+  V* token = reinterpret_cast<V*>(staged);
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int half = p.rot >> 1, per = p.dh / VEC;  // vectors of a head
+  const int nq = p.q != nullptr ? p.Hq * per : 0;
+  const int nk = p.k != nullptr ? p.Hkv * per : 0;
+  const int total = nq + nk + (kAppend ? p.Hkv * per : 0);
+  float* cs = reinterpret_cast<float*>(token + total);
+  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
+  const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
+  const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
+  for (int w = tid; w < total; w += blockDim.x)
+    token[w] = w < nq        ? reinterpret_cast<const V*>(q)[w]
+               : w < nq + nk ? reinterpret_cast<const V*>(k)[w - nq]
+                             : reinterpret_cast<const V*>(v)[w - nq - nk];
+  if (tid < 32) {
+    const Row r = row_of<kAppend>(t, p);
+    if (tid == 0) s_row = r;
+  }
+  __syncthreads();
+  const Row r = s_row;
+  for (int i = tid; i < half; i += blockDim.x) {
+    const float2 f = turn_cos_sin(p.turns[i], r.pos, p.scale, p.inverse ? -1.f : 1.f);
+    cs[i] = f.x;
+    cs[half + i] = f.y;
+  }
+  __syncthreads();
+  if (r.state == 0) return;
+  for (int w = tid; w < total; w += blockDim.x) {
+    const bool is_q = w < nq, is_v = w >= nq + nk;
+    const int x = is_q ? w : is_v ? w - nq - nk : w - nq;
+    const int h = x / per, j0 = (x - h * per) * VEC;
+    if (kAppend && !is_q && r.state != 3) continue;
+    V a = token[w];
+    if (!is_v && j0 < p.rot) {
+      const T* head = reinterpret_cast<const T*>(token + (w - j0 / VEC));
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int j = j0 + e;
+        if (j >= p.rot) break;
+        const bool second = p.interleaved ? (j & 1) != 0 : j >= half;
+        const int i = p.interleaved ? j >> 1 : second ? j - half : j;
+        const int partner = p.interleaved ? j ^ 1 : second ? j - half : j + half;
+        const float c = cs[i], s = cs[half + i], z = to_f(a.e[e]), y = to_f(head[partner]);
+        from_f(a.e[e], second ? fmaf(y, s, z * c) : fmaf(z, c, -(y * s)));
+      }
+    }
+    T* dst;
+    if (is_q)
+      dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + (size_t)h * p.dh;
+    else if (kAppend)
+      dst = static_cast<T*>(is_v ? p.V : p.K) + (r.dst + (long long)h * p.page_size) * p.dh;
+    else
+      dst = static_cast<T*>(p.k_out) + t * p.k_out_stride + (size_t)h * p.dh;
+    *reinterpret_cast<V*>(dst + j0) = a;
+  }
+}
+
+// the widest vector every access allows: VEC elements must divide `part`, the
+// head, every stride and (in bytes) every base address
+int vector_width(const RopeParams& p, int eb, long long part) {
   uintptr_t addr = 0;
-  long long step = p.rot / 2;
+  long long step = part;
   auto take = [&](const void* ptr, long long stride) {
     if (ptr == nullptr) return;
     addr |= reinterpret_cast<uintptr_t>(ptr);
@@ -398,17 +467,42 @@ medusa_status_t launch_vec(RopeParams& p, cudaStream_t stream) {
   return check_launch(kAppend ? "rope_append" : "rope");
 }
 
+template <typename T, int VEC, bool kAppend>
+medusa_status_t launch_staged(RopeParams& p, size_t smem, cudaStream_t stream) {
+  const int total = ((p.q ? p.Hq : 0) + (p.k ? p.Hkv : 0) + (kAppend ? p.Hkv : 0)) * (p.dh / VEC);
+  const int rounds = (total + kRopeThreads - 1) / kRopeThreads;
+  const int threads = ((total + rounds - 1) / rounds + 31) / 32 * 32;
+  launch(rope_staged_kernel<T, VEC, kAppend>, p.T, threads, smem, stream, p);
+  return check_launch(kAppend ? "rope_append" : "rope");
+}
+
 template <bool kAppend>
 medusa_status_t dispatch(RopeParams& p, medusa_dtype_t dt, cudaStream_t stream) {
+  const int eb = dt == MEDUSA_BF16 ? 2 : 4;
+  const int width = vector_width(p, eb, p.rot / 2), apart = vector_width(p, eb, 0);
+  const size_t smem = ((size_t)(p.q ? p.Hq : 0) + (p.k ? p.Hkv : 0) + (kAppend ? p.Hkv : 0)) *
+                          p.dh * eb +
+                      (size_t)p.rot * sizeof(float);
+  if (width < apart && smem <= 48 * 1024 - 64) {
+    if (dt == MEDUSA_BF16) {
+      switch (apart) {
+        case 8: return launch_staged<__nv_bfloat16, 8, kAppend>(p, smem, stream);
+        case 4: return launch_staged<__nv_bfloat16, 4, kAppend>(p, smem, stream);
+        default: return launch_staged<__nv_bfloat16, 2, kAppend>(p, smem, stream);
+      }
+    }
+    if (apart == 4) return launch_staged<float, 4, kAppend>(p, smem, stream);
+    return launch_staged<float, 2, kAppend>(p, smem, stream);
+  }
   if (dt == MEDUSA_BF16) {
-    switch (vector_width(p, 2)) {
+    switch (width) {
       case 8: return launch_vec<__nv_bfloat16, 8, kAppend>(p, stream);
       case 4: return launch_vec<__nv_bfloat16, 4, kAppend>(p, stream);
       case 2: return launch_vec<__nv_bfloat16, 2, kAppend>(p, stream);
       default: return launch_vec<__nv_bfloat16, 1, kAppend>(p, stream);
     }
   }
-  switch (vector_width(p, 4)) {
+  switch (width) {
     case 4: return launch_vec<float, 4, kAppend>(p, stream);
     case 2: return launch_vec<float, 2, kAppend>(p, stream);
     default: return launch_vec<float, 1, kAppend>(p, stream);

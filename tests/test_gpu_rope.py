@@ -36,7 +36,8 @@ def _check(got, x, ref, scale, rot, dtype):
     (1, 1, 1, 64, 64, False), (9, 4, 4, 64, 32, True), (33, 6, 2, 128, 128, False),
     (17, 5, 5, 80, 34, False), (17, 5, 1, 80, 34, True), (3, 2, 1, 7, 2, True),
     (5, 3, 3, 66, 66, False), (2500, 2, 1, 64, 64, True), (2371, 3, 1, 128, 64, False),
-    (4, 64, 8, 512, 512, False), (6, 71, 1, 64, 64, False)])
+    (4, 64, 8, 512, 512, False), (6, 71, 1, 64, 64, False), (300, 8, 2, 128, 34, False),
+    (300, 40, 8, 64, 18, True), (5, 200, 8, 128, 34, False)])
 def test_rotation(dtype, T, Hq, Hkv, dh, rot, inter):
     g = torch.Generator().manual_seed(T + dh + rot)
     q = torch.randn(T, Hq, dh, generator=g).to(dtype)
@@ -145,8 +146,9 @@ def test_refuses_wrong_layouts():
     (16, [(5, 40), (0, 7), (1, 16), (20, 20), (3, 17)], False),
     (1, [(3, 9), (2, 2)], False), (7, [(9, 30), (1, 1)], False),
     (50, [(6, 50), (1, 13), (0, 0)], True)])
-def test_append(dtype, page, lens, dense):
-    Hq, Hkv, dh, rot = 6, 2, 64, 32
+@pytest.mark.parametrize("rot", [32, 18])
+def test_append(dtype, page, lens, dense, rot):
+    Hq, Hkv, dh = 6, 2, 64
     g = torch.Generator().manual_seed(page)
     B, T = len(lens), sum(n for n, _ in lens)
     pad = 4  # rows behind the last sequence
