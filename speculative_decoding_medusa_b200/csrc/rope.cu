@@ -452,8 +452,9 @@ medusa_status_t launch_vec(RopeParams& p, cudaStream_t stream) {
   const int rounds = (work + kRopeThreads - 1) / kRopeThreads;
   const int threads = ((work + rounds - 1) / rounds + 31) / 32 * 32;
   const size_t table = (p.rot / 2) * sizeof(float);
-  // resident blocks once they have several tokens each
-  const int resident = 3 * device_sm_count();
+  // resident blocks once they have several tokens each (8192 tokens of 1 + 1
+  // heads appended: 24 us with three blocks an SM, 10 with as many as fit)
+  const int resident = min(3 * kRopeThreads / threads, 32) * device_sm_count();
   if (work <= kRopeThreads && p.T >= 2 * resident) {
     if (p.interleaved)
       launch(rope_pipe_kernel<T, VEC, true, kAppend>, resident, threads, 4 * table, stream, p);
