@@ -205,6 +205,18 @@ def workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def _own_workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """The workspace of a call that was given none.  It is dropped when the call
+    returns, so it comes from the pool of the call's stream: whatever gets the
+    memory next then follows the call's kernels."""
+    if stream is None:
+        return workspace(nbytes, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, device)
+
+
 class Tree:
     """A candidate tree on the device (parent/depth/rank int32 arrays)."""
 
@@ -246,7 +258,8 @@ def medusa_heads_topk(h, W1, b1, W2, kmax: int, topk_ids, topk_vals, logits=None
     K, V, _ = W2.shape
     dt = _dt(W2)
     if ws is None:
-        ws = workspace(medusa_heads_topk_workspace_size(B, d, V, K, kmax, dt), h.device)
+        ws = _own_workspace(medusa_heads_topk_workspace_size(B, d, V, K, kmax, dt), h.device,
+                            stream)
     _check(lib().medusa_heads_topk(_p(h), _p(W1), _p(b1), _p(W2), dt, B, d, V, K, kmax,
                                    _p(topk_ids), _p(topk_vals), _p(logits), _p(ws), ws.numel(),
                                    _p(dev_status), _stream(stream)))
@@ -264,7 +277,8 @@ def medusa_heads_topk_tree(h, W1, b1, W2, kmax: int, topk_ids, topk_vals, tree: 
     K, V, _ = W2.shape
     dt = _dt(W2)
     if ws is None:
-        ws = workspace(medusa_heads_topk_workspace_size(B, d, V, K, kmax, dt), h.device)
+        ws = _own_workspace(medusa_heads_topk_workspace_size(B, d, V, K, kmax, dt), h.device,
+                            stream)
     ct = tree.c()
     _check(lib().medusa_heads_topk_tree(_p(h), _p(W1), _p(b1), _p(W2), dt, B, d, V, K, kmax,
                                         _p(topk_ids), _p(topk_vals), _p(logits), _p(ws),
@@ -300,8 +314,8 @@ def medusa_tree_attention(q, k_new, v_new, Kc, Vc, prefix_len, anc_mask, max_pre
     if scale is None:
         scale = dh ** -0.5
     if ws is None:
-        ws = workspace(medusa_tree_attention_workspace_size(B, N, Hq, Hkv, dh, max_prefix, dt),
-                       q.device)
+        ws = _own_workspace(medusa_tree_attention_workspace_size(B, N, Hq, Hkv, dh, max_prefix,
+                                                                 dt), q.device, stream)
     _check(lib().medusa_tree_attention(_p(q), _p(k_new), _p(v_new), _p(Kc), _p(Vc),
                                        _p(prefix_len), _p(anc_mask), dt, B, N, Hq, Hkv, dh, cap,
                                        max_prefix, float(scale), _p(out), _dt(out), _p(ws),
@@ -320,7 +334,7 @@ def medusa_verify_accept(logits, cand_ids, tree: Tree, accept_len, accepted_node
     _req(logits, "logits")
     B, N, V = logits.shape
     if ws is None:
-        ws = workspace(medusa_verify_accept_workspace_size(B, N, V), logits.device)
+        ws = _own_workspace(medusa_verify_accept_workspace_size(B, N, V), logits.device, stream)
     ct = tree.c()
     _check(lib().medusa_verify_accept(_p(logits), _dt(logits), _p(cand_ids), ctypes.byref(ct), B, V,
                                       mode, float(temperature), float(eps), float(delta),
@@ -353,7 +367,7 @@ def medusa_verify_accept_compact(logits, cand_ids, tree: Tree, accept_len, accep
     B, N, V = logits.shape
     _, Hkv, cap, dh = Kc.shape
     if ws is None:
-        ws = workspace(medusa_verify_accept_workspace_size(B, N, V), logits.device)
+        ws = _own_workspace(medusa_verify_accept_workspace_size(B, N, V), logits.device, stream)
     ct = tree.c()
     _check(lib().medusa_verify_accept_compact(
         _p(logits), _dt(logits), _p(cand_ids), ctypes.byref(ct), B, V, mode, float(temperature),
@@ -396,7 +410,7 @@ def medusa_lmhead_verify(hidden, lm_head, cand_ids, tree: Tree, accept_len, acce
     B, N, d = hidden.shape
     V = lm_head.shape[0]
     if ws is None:
-        ws = workspace(medusa_lmhead_verify_workspace_size(B, N, d, V), hidden.device)
+        ws = _own_workspace(medusa_lmhead_verify_workspace_size(B, N, d, V), hidden.device, stream)
     ct = tree.c()
     _check(lib().medusa_lmhead_verify(_p(hidden), _p(lm_head), _dt(hidden), _p(cand_ids),
                                       ctypes.byref(ct), B, d, V, mode, float(temperature),
@@ -470,7 +484,7 @@ def medusa_verify_records(logits, cand_ids, tree: Tree, v_offset: int, records, 
     _req(logits, "logits")
     B, N, Vs = logits.shape
     if ws is None:
-        ws = workspace(medusa_verify_records_workspace_size(B, N, Vs), logits.device)
+        ws = _own_workspace(medusa_verify_records_workspace_size(B, N, Vs), logits.device, stream)
     ct = tree.c()
     _check(lib().medusa_verify_records(_p(logits), _dt(logits), _p(cand_ids), ctypes.byref(ct), B,
                                        Vs, v_offset, mode, float(temperature), _p(records),
@@ -745,8 +759,8 @@ def medusa_chunk_attention(q, cache: PagedCache, cu_q, kv_len, out,
     kvp = _vec(kv_len, "kv_len", i32, B, dev)
     cache._on(dev)
     if ws is None:
-        ws = workspace(medusa_chunk_attention_workspace_size(Hq, cache.Hkv, dh, cache.dt),
-                       cache.K.device)
+        ws = _own_workspace(medusa_chunk_attention_workspace_size(Hq, cache.Hkv, dh, cache.dt),
+                            cache.K.device, stream)
     nbytes = ws.numel()
     st = lib().medusa_chunk_attention(qp, qs, cache._ref, cache.dt, cup, kvp, B, T, Hq, cache.Hkv,
                                       dh, dh ** -0.5 if scale is None else scale, op,

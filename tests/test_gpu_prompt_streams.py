@@ -1,0 +1,44 @@
+"""GPU: the prompt side's calls on streams of their own."""
+import pytest
+import torch
+
+import speculative_decoding_medusa_b200 as M
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def test_a_missing_workspace_outlives_its_call_on_another_stream():
+    """Two chunk attentions without a workspace queue behind work on streams of
+    their own, their ranges split over blocks; what the current stream is given
+    and writes meanwhile is none of theirs."""
+    Hq, Hkv, dh, page, n = 8, 2, 128, 64, 80
+    g = torch.Generator(device=DEV).manual_seed(4)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    K, V = torch.randn(2, n, Hkv, page, dh, generator=g, **bf)
+    cache = M.PagedCache(K, V, torch.arange(n, dtype=torch.int32, device=DEV).view(1, n))
+    cu = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    kv = torch.tensor([n * page - 3], dtype=torch.int32, device=DEV)
+    qs = [torch.randn(40, Hq, dh, generator=g, **bf) for _ in range(2)]
+    nbytes = M.medusa_chunk_attention_workspace_size(Hq, Hkv, dh, M.MEDUSA_BF16)
+    ws = M.workspace(nbytes)
+    want = [torch.empty_like(q) for q in qs]
+    for q, o in zip(qs, want):
+        M.medusa_chunk_attention(q, cache, cu, kv, o, ws=ws)
+    outs = [torch.zeros_like(q) for q in qs]
+    del ws  # free for the next allocation of its size on this stream
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in qs]
+    for s, q, o in zip(sides, qs, outs):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)  # some 50 ms
+        M.medusa_chunk_attention(q, cache, cu, kv, o, stream=s)
+    taken = [torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.current_stream().synchronize()
+    assert not sides[0].query()  # its call was still to come
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    for t in taken:
+        assert bool((t == 255).all())
