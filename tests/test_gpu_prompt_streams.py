@@ -27,14 +27,22 @@ def test_a_missing_workspace_outlives_its_call_on_another_stream():
     for q, o in zip(qs, want):
         M.medusa_chunk_attention(q, cache, cu, kv, o, ws=ws)
     outs = [torch.zeros_like(q) for q in qs]
-    del ws  # free for the next allocation of its size on this stream
-    torch.cuda.synchronize()
     sides = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    # every pool filled and every kernel loaded first, which can wait for the GPU
+    for s, q, o in zip(sides, qs, outs):
+        M.medusa_chunk_attention(q, cache, cu, kv, o, stream=s)
+    taken = [M.workspace(nbytes).fill_(255) for _ in range(4)]
+    torch.cuda.synchronize()
+    del ws, taken  # free for this stream's next allocations of their size
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
     for s, q, o in zip(sides, qs, outs):
         with torch.cuda.stream(s):
-            torch.cuda._sleep(100_000_000)  # some 50 ms
+            torch.cuda._sleep(400_000_000)  # some 200 ms
         M.medusa_chunk_attention(q, cache, cu, kv, o, stream=s)
-    taken = [torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    taken = [M.workspace(nbytes).fill_(255) for _ in range(4)]
     torch.cuda.current_stream().synchronize()
     assert not sides[0].query()  # its call was still to come
     torch.cuda.synchronize()
