@@ -731,7 +731,7 @@ MEDUSA_API medusa_status_t medusa_rope_append(
  *   K and V must be finite.
  * Device checks: a page outside [0, n_pages), kv_len[b] outside
  *   [0, max_pages * page_size], cu_q decreasing, negative or above T, a
- *   non-finite output.
+ *   non-finite output.  Where kv_len or cu_q fails, no row is written.
  * Limits: B in [1, 1024], T >= 0, Hq % Hkv == 0, Hq / Hkv <= 128, Hkv <= 1024,
  *   scale > 0; pools 16-byte aligned; bf16: dh in {64, 128}, q_stride % 8 == 0,
  *   q and out 16-byte aligned; f32: dh % 32 == 0, dh <= 256.  Any page_size;

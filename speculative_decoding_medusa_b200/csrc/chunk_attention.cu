@@ -55,15 +55,32 @@ __global__ void __launch_bounds__(kWarps * 32) chunk_attn_f32_kernel(ChunkParams
     for (int e = 0; e < PER; ++e) qv[r][e] = live && r < nr ? qp[r * DH + e] : 0.f;
   if (live) {
     int first = 0, end = 0, kv = 0;  // of sequence `lane`, then of the row's
+    // The row's sequence is found by counting the ends at or before it, which
+    // says nothing unless they ascend: every warp checks all lengths, and none
+    // computes a row of a call that fails.
+    const long long slots = (long long)p.max_pages * p.page_size;
+    auto in_range = [&](int a, int e, int k) {
+      return a >= 0 && e >= a && e <= p.T && k >= 0 && k <= slots;
+    };
+    bool ok = true;
     if (lane < p.B) {
       first = p.cu_q[lane];
       end = p.cu_q[lane + 1];
       kv = p.kv_len[lane];
       n = end <= t ? 1 : 0;
+      ok = in_range(first, end, kv);
     }
-    for (int b = lane + 32; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
+    for (int b = lane + 32; b < p.B; b += 32) {
+      const int e = p.cu_q[b + 1];
+      n += e <= t ? 1 : 0;
+      ok = ok && in_range(p.cu_q[b], e, p.kv_len[b]);
+    }
     n = __reduce_add_sync(0xffffffffu, n);
     live = n < p.B;  // not behind the last sequence
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      live = false;
+    }
     if (live) {
       if (n < 32) {
         first = __shfl_sync(0xffffffffu, first, n);
@@ -74,13 +91,11 @@ __global__ void __launch_bounds__(kWarps * 32) chunk_attn_f32_kernel(ChunkParams
         end = p.cu_q[n + 1];
         kv = p.kv_len[n];
       }
-      const int len = end - first;
-      if (first < 0 || t < first || first + len > p.T || kv < 0 ||
-          kv > (long long)p.max_pages * p.page_size) {
+      if (t < first) {  // cu_q does not start at 0
         if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
         live = false;
       } else {
-        visible = max(0, kv - len + (t - first) + 1);
+        visible = max(0, kv - end + t + 1);
       }
     }
   }

@@ -1,0 +1,52 @@
+"""GPU: lengths that the prompt side's calls have to refuse on the device."""
+import pytest
+import torch
+
+import speculative_decoding_medusa_b200 as M
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+i32 = dict(dtype=torch.int32, device=DEV)
+
+
+def _attend(dtype, cu, kv, T=8, max_pages=3, page=16):
+    """A call over B = len(kv) sequences; the pools hold every page the tables
+    name.  Returns out (5.0 on entry) and the status."""
+    B = len(kv)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    K, V = torch.randn(2, 4, 1, page, 64, generator=g, device=DEV).to(dtype)
+    table = (torch.arange(B * max_pages, **i32) % 4).view(B, max_pages)
+    q = torch.randn(T, 2, 64, generator=g, device=DEV).to(dtype)
+    out, st = torch.full_like(q, 5.0), M.new_status()
+    M.medusa_chunk_attention(q, M.PagedCache(K, V, table), torch.tensor(cu, **i32),
+                             torch.tensor(kv, **i32), out, dev_status=st)
+    torch.cuda.synchronize()
+    return out, int(st.item())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cu,kv", [
+    ([0, 8, 1, 1], [48, 48, 48]),       # rows of the first land in the empty third
+    ([0, 8, 1, 1], [20, 20, 20]),
+    ([0, 4, 2, 8], [20, 20, 20]),
+    ([0, 8, 8, 7], [20, 20, 20]),       # behind every row
+    ([0, 8, 9, 8], [20, 20, 20]),
+    ([0, 8, 8], [20, 49]),              # a length of a sequence without new tokens
+    ([0, 8, 8], [20, -1]),
+    ([0] + [8] * 40 + [3], [9] * 41),   # beyond the first 32 sequences
+    ([0] * 40 + [8, 8], [9] * 40 + [49]),
+    ([0, 2 ** 31 - 1, 8], [9, 9]), ([0, -2 ** 31, 8], [9, 9])])
+def test_bad_lengths_leave_every_row(dtype, cu, kv):
+    out, status = _attend(dtype, cu, kv)
+    assert status == 6
+    assert bool((out == 5.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_good_lengths_around_them(dtype):
+    """The largest lengths that are in range; empty sequences on both sides."""
+    out, status = _attend(dtype, [0, 0, 6, 6, 6], [48, 48, 0, 48])
+    assert status == 0
+    assert bool((out[6:] == 5.0).all()) and bool(torch.isfinite(out[:6]).all())
+    assert not bool((out[:6] == 5.0).any())
