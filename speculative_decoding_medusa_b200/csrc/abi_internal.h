@@ -160,6 +160,8 @@ medusa_status_t chunk_attention(const void* q, long long q_stride, const medusa_
                                 int B, int T, int Hq, int Hkv, int dh, float scale, void* out,
                                 void* ws, int32_t* status, cudaStream_t stream);
 
+// the longest row that a cluster holds in shared memory
+constexpr int sample_max_vocab(size_t element_bytes) { return element_bytes == 2 ? 655360 : 327680; }
 medusa_status_t sample_tokens(const void* logits, medusa_dtype_t dt, long long row_stride,
                               int n_rows, const int32_t* row_idx, int R, int V, const float* u,
                               const float* temperature, const int32_t* top_k, const float* top_p,

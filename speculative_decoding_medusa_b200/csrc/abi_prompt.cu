@@ -223,7 +223,7 @@ medusa_status_t medusa_sample_tokens(const void* logits, medusa_dtype_t dt, long
                                      void* stream) {
   if (!valid_dtype(dt)) return fail(MEDUSA_ERR_INVALID_ARG, "sample_tokens: bad dtype");
   if (R < 0 || R > 65535 || n_rows < (R > 0 ? 1 : 0) || n_rows > 65535 || V < 1 ||
-      V > (dt == MEDUSA_BF16 ? 655360 : 327680))
+      V > medusa::sample_max_vocab(dt == MEDUSA_BF16 ? 2 : 4))
     return fail(MEDUSA_ERR_SHAPE, "sample_tokens: R, n_rows or V out of range");
   if (n_rows > 1 && row_stride < V)
     return fail(MEDUSA_ERR_SHAPE, "sample_tokens: row_stride is below V");

@@ -22,10 +22,6 @@ namespace medusa {
 
 constexpr int kCompactThreads = 512;
 
-// Shared memory that one round of staging may use; heads per round =
-// this / (2 * (max_depth + 1) * row bytes), at least one.
-constexpr size_t kCompactSmem = 96 * 1024;
-
 __global__ void __launch_bounds__(kCompactThreads)
     kv_compact_kernel(uint8_t* Kc, uint8_t* Vc, int row_bytes, int32_t* prefix_len,
                       const int32_t* __restrict__ accepted_nodes,

@@ -7,6 +7,10 @@
 
 namespace medusa {
 
+// Shared memory that one round of staging may use; heads per round =
+// this / (2 * (max_depth + 1) * row bytes), at least one.
+constexpr size_t kCompactSmem = 96 * 1024;
+
 // Where the kept branch moves: caches [B][Hkv][cap][row_bytes], the prefix
 // lengths (read, then advanced) and the source-slot list written back.
 // Kc == nullptr: no compaction.

@@ -1543,20 +1543,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleParams
   pick(target_of(all.mass), before);
 }
 
+// a block's share of the row and of its offset in a 16-byte word
+template <typename T>
+constexpr int sample_slice(int V, int C) {
+  constexpr int VE = 16 / sizeof(T);
+  return ((V + VE - 1 + C - 1) / C + 32 * VE - 1) / (32 * VE) * (32 * VE);
+}
+
 template <typename T>
 medusa_status_t launch_sample(SampleParams& p, cudaStream_t stream) {
-  constexpr int VE = 16 / sizeof(T);
   // A cluster holds the row in shared memory.  Few rows: more blocks for each
   // while a block still has 4096 tokens.  Many: as few as leave two blocks to
   // an SM (a step's barriers cost a block the same whatever its share).
   const bool few = p.R * kMaxCluster <= 2 * device_sm_count();
   int C = 1;
   while (C < kMaxCluster && (few ? p.V > 4096 * C : (size_t)p.V * sizeof(T) > kManyBytes * C)) C *= 2;
-  const int span = p.V + VE - 1;  // the row and its offset in a 16-byte word
-  p.slice = ((span + C - 1) / C + 32 * VE - 1) / (32 * VE) * (32 * VE);
+  p.slice = sample_slice<T>(p.V, C);
   const size_t smem = (size_t)p.slice * sizeof(T) + sample_extra_smem(C);
+  // What the kernel is allowed is the most that any row needs, not what this one
+  // does: the setting is shared by all host threads, and a shorter row's must not
+  // lower it between another's setting and its launch.
+  constexpr size_t kMaxSmem =
+      (size_t)sample_slice<T>(sample_max_vocab(sizeof(T)), kMaxCluster) * sizeof(T) +
+      sample_extra_smem(kMaxCluster);
+  static_assert(kManyBytes + 1024 + sample_extra_smem(kMaxCluster) <= kMaxSmem,
+                "smaller clusters need less");
+  static_assert(kMaxSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
   if (cudaFuncSetAttribute(sample_tokens_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+                           static_cast<int>(kMaxSmem)) != cudaSuccess)
     return fail(MEDUSA_ERR_CUDA, "cudaFuncSetAttribute(sample_tokens) failed");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.R) * C);

@@ -688,14 +688,15 @@ medusa_status_t verify_accept(const void* logits, medusa_dtype_t dt, const int32
                               void* ws, int32_t* status, cudaStream_t stream,
                               const CompactArgs& ca, size_t ca_smem) {
   const int N = tree.n_nodes;
-  // the compaction tail's staging memory
+  // the compaction tail's staging memory (the largest, whatever this call's: the
+  // setting is shared by all host threads)
   if (ca_smem > 48 * 1024) {
     const cudaError_t e =
         dt == MEDUSA_BF16
             ? cudaFuncSetAttribute(verify_path_kernel<__nv_bfloat16>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ca_smem)
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCompactSmem)
             : cudaFuncSetAttribute(verify_path_kernel<float>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ca_smem);
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCompactSmem);
     if (e != cudaSuccess) return fail(MEDUSA_ERR_CUDA, "cudaFuncSetAttribute(verify_path) failed");
   }
   const int n_chunks = (V + kVChunk - 1) / kVChunk;
