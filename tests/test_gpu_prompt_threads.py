@@ -55,3 +55,33 @@ def test_vocabularies_of_different_sizes(dtype):
     assert _together(works, 2000) == []
     for tok, first in checks:
         assert torch.equal(tok, first)
+
+
+def test_the_first_call_of_a_thread():
+    """A host thread that has made no CUDA call yet."""
+    g = torch.Generator(device=DEV).manual_seed(6)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    K, V = torch.randn(2, 3, 2, 64, 128, generator=g, **bf)
+    cache = M.PagedCache(K, V, torch.arange(3, dtype=torch.int32, device=DEV).view(1, 3))
+    cu = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    kv = torch.tensor([150], dtype=torch.int32, device=DEV)
+    q = torch.randn(5, 4, 128, generator=g, **bf)
+    out, first = torch.zeros(2, 5, 4, 128, **bf)
+    ws = M.workspace(M.medusa_chunk_attention_workspace_size(4, 2, 128, M.MEDUSA_BF16))
+    M.medusa_chunk_attention(q, cache, cu, kv, first, ws=ws)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    errors = []
+
+    def body():
+        try:
+            M.medusa_chunk_attention(q, cache, cu, kv, out, ws=ws, stream=s)
+        except Exception as e:  # noqa: BLE001
+            errors.append(repr(e))
+
+    t = threading.Thread(target=body)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert errors == []
+    assert torch.equal(out, first)
