@@ -185,8 +185,6 @@ medusa_status_t medusa_chunk_attention(const void* q, long long q_stride,
   if (B < 1 || B > 1024 || T < 0 || Hq < 1 || Hkv < 1 || Hkv > 1024 || Hq % Hkv != 0 ||
       Hq / Hkv > 128)
     return fail(MEDUSA_ERR_SHAPE, "chunk_attention: B, T, Hq or Hkv out of range");
-  if ((long long)pages->n_pages * Hkv * pages->page_size > (1LL << 40) / dh)
-    return fail(MEDUSA_ERR_SHAPE, "chunk_attention: cache too large");
   if (dt == MEDUSA_BF16) {
     if (dh != 64 && dh != 128)
       return fail(MEDUSA_ERR_SHAPE, "chunk_attention: bf16 dh must be 64 or 128");
@@ -195,6 +193,9 @@ medusa_status_t medusa_chunk_attention(const void* q, long long q_stride,
   } else if (dh < 32 || dh % 32 != 0 || dh > 256) {
     return fail(MEDUSA_ERR_SHAPE, "chunk_attention: f32 dh must be a multiple of 32, <= 256");
   }
+  // (dh is above zero here)
+  if ((long long)pages->n_pages * pages->page_size > (1LL << 40) / dh / Hkv)
+    return fail(MEDUSA_ERR_SHAPE, "chunk_attention: cache too large");
   if (!(scale > 0.f) || isinf(scale))
     return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention: scale must be > 0");
   if (T == 0) return MEDUSA_OK;
