@@ -259,10 +259,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_block_kernel(RopeParams 
 // What row_of finds, by one thread, with the sequences' lengths in cu and kv
 // (shared memory, or global where they do not fit).
 template <bool kAppend>
-__device__ __forceinline__ Row row_of_thread(int t, const int* cu, const int* kv,
+__device__ __forceinline__ Row row_of_thread(uint32_t token, const int* cu, const int* kv,
                                              const RopeParams& p) {
   Row r{0, 0, 0};
-  if (t >= p.T) return r;
+  if (token >= static_cast<uint32_t>(p.T)) return r;
+  const int t = static_cast<int>(token);
   if (!kAppend) return Row{1, p.positions[t], 0};
   int lo = 0, hi = p.B;  // the first sequence that ends after t
   while (lo < hi) {
@@ -302,7 +303,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
   extern __shared__ float cs[];  // two tokens' cosines and sines
   __shared__ Row s_row[kChunk];
   __shared__ int s_cu[kAppend ? kSmallB + 1 : 1], s_kv[kAppend ? kSmallB : 1];
-  const int tid = threadIdx.x, step = gridDim.x;
+  const int tid = threadIdx.x;
+  // (T may lie just below 2^31: tokens ahead of the current one pass it)
+  const uint32_t n_tok = static_cast<uint32_t>(p.T), step = gridDim.x;
   const int half = p.rot >> 1;
   const int nq = p.q != nullptr ? p.Hq * p.units : 0;
   const int nk = p.k != nullptr ? p.Hkv * p.units : 0;
@@ -318,8 +321,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
     }
   };
   Vec<T, VEC> a, b, a2, b2;
-  int t = blockIdx.x;
-  if (works && t < p.T) fetch<T, VEC>(u, t, p, a, b);
+  uint32_t t = blockIdx.x;
+  if (works && t < n_tok) fetch<T, VEC>(u, t, p, a, b);
   const bool small = kAppend && p.B <= kSmallB;
   if (small) {
     for (int i = tid; i <= p.B; i += blockDim.x) {
@@ -329,17 +332,17 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
     __syncthreads();
   }
   int parity = 0;
-  while (t < p.T) {
+  while (t < n_tok) {
     if (tid < kChunk)
       s_row[tid] = row_of_thread<kAppend>(t + tid * step, small ? s_cu : p.cu_q,
                                           small ? s_kv : p.kv_len, p);
     __syncthreads();
     angles(s_row[0].pos, cs + parity * 2 * half);
     __syncthreads();
-    for (int j = 0; j < kChunk && t < p.T; ++j, t += step) {
+    for (int j = 0; j < kChunk && t < n_tok; ++j, t += step) {
       const float* table = cs + parity * 2 * half;
       parity ^= 1;
-      if (t + step < p.T) {
+      if (t + step < n_tok) {
         if (works) fetch<T, VEC>(u, t + step, p, a2, b2);
         if (j + 1 < kChunk) angles(s_row[j + 1].pos, cs + parity * 2 * half);
       }
