@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The launch before this one is always chunk_zero_kernel, which waited for
   // every earlier grid: the inputs are final already.  Only the piece
   // counters it zeroes (and the writes that must follow it) need its
-  // completion, so griddepcontrol.wait comes right before those.
+  // completion, so griddepcontrol.wait comes right before those.  Every CTA
+  // also waits before it ends, with or without work: the grid after this one
+  // is ordered behind this one alone, and may zero or count again.
   grid_dep_launch();
   using L = Smem<DH>;
   extern __shared__ uint8_t smem_raw[];
@@ -636,7 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (start[8] == 0) {  // no tile is this CTA's
-    if (warp == 1) tmem_dealloc(*tmem_holder, kTmemCols);
+    if (warp == 1) {
+      grid_dep_wait();  // (at the other end, too: no grid ends before the counters are zero)
+      tmem_dealloc(*tmem_holder, kTmemCols);
+    }
     return;
   }
   const int t1 = start[8], per = start[9];
@@ -1159,6 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   mbar_arrive(exit_bar);
   if (warp == 1) {
+    grid_dep_wait();
     __syncwarp();
     int no_abort = 0;
     mbar_wait_bounded(exit_bar, 0, &no_abort, p.status);

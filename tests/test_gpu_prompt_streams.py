@@ -50,3 +50,40 @@ def test_a_missing_workspace_outlives_its_call_on_another_stream():
         assert torch.equal(o, w)
     for t in taken:
         assert bool((t == 255).all())
+
+
+def test_calls_without_work_between_calls_that_share_a_workspace():
+    """A call whose blocks have nothing to do (no new token, or lengths that are
+    refused) ends at once; its counters are zeroed before the next call counts."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    K, V = torch.randn(2, 40, 2, 64, 128, generator=g, **bf)
+    cache = M.PagedCache(K, V, torch.arange(40, **i32).view(1, 40))
+    q = torch.randn(9, 8, 128, generator=g, **bf)
+    cu, kv = torch.tensor([0, 9], **i32), torch.tensor([2500], **i32)
+    none, wrong = torch.tensor([0, 0], **i32), torch.tensor([0, 10], **i32)
+    ws = M.workspace(M.medusa_chunk_attention_workspace_size(8, 2, 128, M.MEDUSA_BF16))
+    first, st = torch.empty_like(q), M.new_status()
+    M.medusa_chunk_attention(q, cache, cu, kv, first, ws=ws)
+
+    def run(out):
+        M.medusa_chunk_attention(q, cache, none, kv, out, ws=ws)
+        M.medusa_chunk_attention(q, cache, cu, kv, out, ws=ws)
+        M.medusa_chunk_attention(q, cache, wrong, kv, out, ws=ws, dev_status=st)
+
+    outs = [torch.zeros_like(q) for _ in range(200)]
+    for o in outs:
+        run(o)
+    graph = torch.cuda.CUDAGraph()
+    late = torch.zeros_like(q)
+    with torch.cuda.graph(graph):
+        run(late)
+    for _ in range(50):
+        late.zero_()
+        graph.replay()
+        outs.append(late.clone())
+    torch.cuda.synchronize()
+    assert int(st.item()) == 6
+    for o in outs:
+        assert torch.equal(o, first)
