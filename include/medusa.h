@@ -731,12 +731,16 @@ MEDUSA_API medusa_status_t medusa_rope_append(
  *   K and V must be finite.
  * Device checks: a page outside [0, n_pages), kv_len[b] outside
  *   [0, max_pages * page_size], cu_q decreasing, negative or above T, a
- *   non-finite output.  Where kv_len or cu_q fails, no row is written.
+ *   non-finite output; bf16 also a call beyond its schedule: a sequence of
+ *   more than 2^28 key tiles, or more than about 2^27 tiles a multiprocessor,
+ *   counting a tile once for each group of up to 256 query rows and each kv
+ *   head (a prompt of some six million tokens of 32 + 8 heads).  Where kv_len,
+ *   cu_q or the schedule fails, no row is written.
  * Limits: B in [1, 1024], T >= 0, Hq % Hkv == 0, Hq / Hkv <= 128, Hkv <= 1024,
  *   scale > 0; pools 16-byte aligned; bf16: dh in {64, 128}, q_stride % 8 == 0,
  *   q and out 16-byte aligned; f32: dh % 32 == 0, dh <= 256.  Any page_size;
  *   in bf16, sizes of 128 or more and multiples of 8 fill the 128-key tiles
- *   best.
+ *   best (any other size below 128 takes a tile a page).
  * ---------------------------------------------------------------------- */
 MEDUSA_API size_t medusa_chunk_attention_workspace_size(int Hq, int Hkv, int dh,
                                                         medusa_dtype_t dt);

@@ -112,12 +112,14 @@ __global__ void __launch_bounds__(kWarps * 32) chunk_attn_f32_kernel(ChunkParams
   const float* Kp = static_cast<const float*>(p.K) + lane * PER;
   const float* Vp = static_cast<const float*>(p.V) + lane * PER;
   const int mine = (lane >> 2) & 7;  // the key whose score this lane ends with
-  for (int j0 = split * 8; j0 < visible; j0 += S * 8) {
-    const int nk = min(8, visible - j0);
+  // (unsigned: a sequence may fill an int with slots)
+  const uint32_t n_vis = visible, page_size = p.page_size;
+  for (uint32_t j0 = split * 8; j0 < n_vis; j0 += S * 8) {
+    const uint32_t nk = min(8u, n_vis - j0);
     size_t at[8];  // element offset of each key's row
     unsigned int have = (1u << nk) - 1u;
-    const int pg0 = j0 / p.page_size, r0 = j0 - pg0 * p.page_size;
-    if (r0 + nk <= p.page_size) {  // the eight lie in one page
+    const uint32_t pg0 = j0 / page_size, r0 = j0 - pg0 * page_size;
+    if (r0 + nk <= page_size) {  // the eight lie in one page
       const int id = p.table[(size_t)n * p.max_pages + pg0];
       if (id < 0 || id >= p.n_pages) have = 0u;
       const size_t first =
@@ -127,11 +129,11 @@ __global__ void __launch_bounds__(kWarps * 32) chunk_attn_f32_kernel(ChunkParams
     } else {
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const int j = min(j0 + x, visible - 1), pg = j / p.page_size;
+        const uint32_t j = min(j0 + x, n_vis - 1), pg = j / page_size;
         const int id = p.table[(size_t)n * p.max_pages + pg];
         at[x] = 0;
         if (id >= 0 && id < p.n_pages)
-          at[x] = (((size_t)id * p.Hkv + kvh) * p.page_size + (j - pg * p.page_size)) * DH;
+          at[x] = (((size_t)id * p.Hkv + kvh) * p.page_size + (j - pg * page_size)) * DH;
         else
           have &= ~(1u << x);
       }

@@ -92,6 +92,11 @@ constexpr int kSegCost = 8;
 // kv heads took 15.5, 19.5, 20.5 and 16.1 us, a chunk of 100 tokens 25.6, 27.2,
 // 30.4 and 34.3.
 constexpr int kMinCost = 8;
+// The most tiles of a sequence and the longest stretch of a CTA: with them
+// seg + (ntiles + 1) * kTwoCost + kSegCost stays below 2^31.
+constexpr int kMaxTiles = 1 << 28;
+constexpr int kMaxStretch = 1 << 29;
+static_assert((long long)kMaxStretch + (kMaxTiles + 1ll) * kTwoCost + kSegCost <= 0x7fffffffll, "");
 constexpr int kMaxB = 1024;
 constexpr int kFewRows = 8;    // rows of a warp whose pieces the whole warp merges
 
@@ -140,12 +145,12 @@ struct Smem {
   static constexpr int kBytes = kHalfOff + kMT * 8;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  static_assert((kMaxB + 1) * 4 <= kRing * kItem, "schedule fits in the ring");
+  static_assert((kMaxB + 1) * 8 <= kRing * kItem, "schedule fits in the ring");
 };
 
 // key tiles that cover `vis` slots (at least one, so an empty row is written)
 __device__ __forceinline__ int tiles_of(int vis, const TcParams& p) {
-  if (p.ppt > 0) return max(1, (vis + p.kt - 1) / p.kt);
+  if (p.ppt > 0) return max(1, vis / p.kt + (vis % p.kt != 0 ? 1 : 0));
   const int fp = vis / p.page;
   return max(1, fp * p.tpp + (vis - fp * p.page + kBN - 1) / kBN);
 }
@@ -158,7 +163,7 @@ __device__ __forceinline__ int group_vis(int qlen, int kv, int qg, const TcParam
 __device__ __forceinline__ int group_mt(int qlen, int qg, const TcParams& p) {
   return qlen - qg * 2 * p.tpt > p.tpt ? 2 : 1;
 }
-// length of a query group's segment on the axis below
+// length of a query group's segment on the axis below (an int: kMaxTiles)
 __device__ __forceinline__ int group_cost(int qlen, int kv, int qg, const TcParams& p) {
   return tiles_of(group_vis(qlen, kv, qg, p), p) *
              (group_mt(qlen, qg, p) == 2 ? kTwoCost : kOneCost) +
@@ -167,11 +172,13 @@ __device__ __forceinline__ int group_cost(int qlen, int kv, int qg, const TcPara
 
 // Walks the tiles of a CTA's range.  Segments lie end to end on one axis, each
 // tile wt long, kSegCost after its last; a tile belongs to the CTA in whose
-// stretch of the axis it starts.
+// stretch of the axis it starts.  The axis is as long as 64 bits; a cursor
+// counts from its CTA's start, where kMaxStretch and kMaxTiles keep everything
+// in 32.
 struct Cursor {
   int b, kvh, qg, n_qg, q0, qlen, kv;
   int lt, ntiles, vis, n_mt, wt;
-  int seg, end;  // start of the segment, end of the CTA's range
+  int seg, end;  // from the CTA's start: start of the segment, end of the range
   bool live, first, last;
 
   __device__ __forceinline__ void sequence(const TcParams& p) {
@@ -281,19 +288,20 @@ __global__ void chunk_zero_kernel(unsigned int* __restrict__ cnt, int n) {
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) cnt[i] = 0u;
 }
 
-// slot of the workspace that holds the piece of a segment (which starts at s0)
-// in CTA c
-__device__ __forceinline__ int piece_slot(int c, int per, int s0) {
-  return 2 * c + (c * per >= s0 ? 0 : 1);
+// The workspace has two slots a CTA: the first for a piece at the start of its
+// stretch, the second for a segment that starts within it and leaves it.  Slot
+// of the k-th piece of a segment whose first is in CTA c0, `within` its stretch.
+__device__ __forceinline__ int piece_slot(int c0, int k, bool within) {
+  return 2 * (c0 + k) + (k == 0 && within ? 1 : 0);
 }
 
-// The merge of the pieces (CTAs c0 .. c0 + n - 1) of a warp's rows by the last
-// to arrive: weights 2^(lse - max lse) over their sum.  `rows`: lanes with a
+// The merge of the pieces (CTAs c0 .. c0 + n - 1, the first `within` its stretch)
+// of a warp's rows by the last to arrive: weights 2^(lse - max lse) over their sum.  `rows`: lanes with a
 // row; row0: lane 0's row of the segment.  Partials of other CTAs are read past
 // L1 (they were released by a fence before their count).
 template <int DH>
 __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, unsigned int rows,
-                                        int c0, int n, int per, int s0, int row0) {
+                                        int c0, int n, bool within, int row0) {
   const int lane = threadIdx.x & 31;
   const bool valid = (rows >> lane) & 1u;
   bool finite = true;
@@ -322,7 +330,7 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
       }
 #pragma unroll 1
       for (int k0 = 0; k0 < n; k0 += 32) {
-        const float* lse = p.lse_part + (size_t)piece_slot(c0 + k0 + lane, per, s0) * kRows + row0;
+        const float* lse = p.lse_part + (size_t)piece_slot(c0, k0 + lane, within) * kRows + row0;
         float l[kR], mx[kR], w[kR];  // w: this lane's piece
 #pragma unroll
         for (int i = 0; i < kR; ++i)
@@ -347,7 +355,7 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
           V x[kK][kR];
 #pragma unroll
           for (int d = 0; d < kK; ++d) {
-            const size_t slot = piece_slot(c0 + k0 + min(k + d, cnt - 1), per, s0);
+            const size_t slot = piece_slot(c0, k0 + min(k + d, cnt - 1), within);
             const float* v = p.o_part + (slot * kRows + row0) * DH + lane * kCols;  // whole rows
 #pragma unroll
             for (int i = 0; i < kR; ++i)
@@ -390,11 +398,11 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
   float M = -INFINITY;
 #pragma unroll 4
   for (int k = 0; k < n; ++k)
-    M = fmaxf(M, __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row));
+    M = fmaxf(M, __ldcg(p.lse_part + (size_t)piece_slot(c0, k, within) * kRows + row));
   float sum = 0.f;
 #pragma unroll 4
   for (int k = 0; k < n; ++k) {
-    const float l = __ldcg(p.lse_part + (size_t)piece_slot(c0 + k, per, s0) * kRows + row);
+    const float l = __ldcg(p.lse_part + (size_t)piece_slot(c0, k, within) * kRows + row);
     sum += l == -INFINITY ? 0.f : exp2f(l - M);
   }
   const float inv = sum > 0.f ? 1.f / sum : sum;
@@ -407,7 +415,7 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
     // two, 25.3 four; three or fewer pieces are the same in all)
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const size_t slot = piece_slot(c0 + k, per, s0);
+      const size_t slot = piece_slot(c0, k, within);
       const float l = __ldcg(p.lse_part + slot * kRows + row);
       const float4* src = reinterpret_cast<const float4*>(p.o_part) +
                           (slot * kRows + row0) * (DH / 4) + ch * 8 * 32 + lane;
@@ -428,12 +436,20 @@ __device__ __noinline__ bool merge_rows(const TcParams& p, __nv_bfloat16* out, u
   return finite;
 }
 
+// a / b of numbers not below zero (64-bit divisions take several times as long)
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // One warp finds the CTA's stretch of the axis and the first tile that starts
 // in it: out = {b, kvh, qg, lt, seg, q0, qlen, kv, end, length of a stretch},
-// end 0 when no tile does or a length is out of range (reported).  cum (shared
-// memory, B + 1 words): length of the sequences before b.
+// seg and end from the stretch's start, end 0 when no tile does or a length is
+// out of range (reported).  cum (shared memory, B + 1 words): length of the
+// sequences before b.
 template <int DH>
-__device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, int cta, int grid) {
+__device__ __forceinline__ void schedule(const TcParams& p, long long* cum, int* out, int cta,
+                                         int grid) {
   const int lane = threadIdx.x & 31;
   bool ok = true;
   long long run = 0;
@@ -448,7 +464,7 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
       kv = p.kv_len[b];
       qlen = a1 - q0;
       ok = ok && q0 >= 0 && a1 >= q0 && a1 <= p.T && kv >= 0 &&
-           kv <= (long long)p.max_pages * p.page;
+           kv <= (long long)p.max_pages * p.page && tiles_of(kv, p) <= kMaxTiles;
     }
     if (!__all_sync(0xffffffffu, ok)) break;
     const int n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
@@ -473,11 +489,10 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
       if (lane >= o) n += a;
     }
     n += run;
-    if (n > 0x7fffffffLL) ok = false;
-    if (b < p.B) cum[b + 1] = static_cast<int>(n);
+    if (b < p.B) cum[b + 1] = n;
     run = __shfl_sync(0xffffffffu, n, 31);
-    if (!__all_sync(0xffffffffu, ok)) break;
   }
+  ok = ok && run <= (long long)grid * kMaxStretch;
   __syncwarp();
   if (!__all_sync(0xffffffffu, ok)) {
     if (lane == 0) {
@@ -486,23 +501,22 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
     }
     return;
   }
-  const int total = static_cast<int>(run);
-  const int per = max(kMinCost, (total + grid - 1) / grid);
-  const long long first = (long long)cta * per;
-  if (first >= total) {
+  const int per = max(kMinCost, static_cast<int>(divide(run + grid - 1, grid)));
+  const long long t0 = (long long)cta * per;
+  if (t0 >= run) {
     if (lane == 0) out[8] = 0;
     return;
   }
-  const int t0 = static_cast<int>(first), t1 = min(total, t0 + per);
+  const int end = static_cast<int>(min((long long)per, run - t0));
   int lo = 0, hi = p.B;  // cum[lo] <= t0 < cum[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (cum[mid] <= t0) lo = mid;
     else hi = mid;
   }
-  const int per_head = (cum[lo + 1] - cum[lo]) / p.Hkv;
-  int rem = t0 - cum[lo];
-  int s[8] = {lo, rem / per_head, 0, 0, 0, 0, 0, 0};
+  const long long per_head = divide(cum[lo + 1] - cum[lo], p.Hkv);
+  long long rem = t0 - cum[lo];
+  int s[8] = {lo, static_cast<int>(divide(rem, per_head)), 0, 0, 0, 0, 0, 0};
   rem -= s[1] * per_head;
   if (p.B <= 32) {
     s[5] = __shfl_sync(0xffffffffu, q0, lo);
@@ -516,37 +530,38 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
   if (s[6] <= 2 * p.tpt) {
     // one query group (single tokens, short chunks)
     const int wt = group_mt(s[6], 0, p) == 2 ? kTwoCost : kOneCost;
-    s[3] = (rem + wt - 1) / wt;
-    s[4] = t0 - rem;
+    const int in = static_cast<int>(rem);  // t0 within the segment
+    s[3] = (in + wt - 1) / wt;
+    s[4] = -in;
   } else {
     for (int g0 = 0;; g0 += 32) {
       // beyond the last group the costs only have to be positive
       const int n = group_cost(s[6], s[7], g0 + lane, p);
-      int c = n;
+      long long c = n;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, c, o);
+        const long long a = __shfl_up_sync(0xffffffffu, c, o);
         if (lane >= o) c += a;
       }
       const unsigned int over = __ballot_sync(0xffffffffu, c > rem);
       if (over != 0u) {
         const int at = __ffs(over) - 1;
-        const int in = __shfl_sync(0xffffffffu, rem - (c - n), at);  // t0 within the segment
+        const int in = static_cast<int>(__shfl_sync(0xffffffffu, rem - (c - n), at));
         const int wt = group_mt(s[6], g0 + at, p) == 2 ? kTwoCost : kOneCost;
         s[2] = g0 + at;
         s[3] = (in + wt - 1) / wt;
-        s[4] = t0 - in;
+        s[4] = -in;
         break;
       }
       rem -= __shfl_sync(0xffffffffu, c, 31);
     }
   }
   Cursor c;
-  c.init(s, t1, p);
+  c.init(s, end, p);
   if (c.lt >= c.ntiles) {
     c.skip(0, p);  // past the last tile: the next segment, if the stretch has one
   } else {
-    c.live = c.seg + c.lt * c.wt < t1;
+    c.live = c.seg + c.lt * c.wt < end;
   }
   if (lane == 0) {
     out[0] = c.b;
@@ -557,7 +572,7 @@ __device__ __forceinline__ void schedule(const TcParams& p, int* cum, int* out, 
     out[5] = c.q0;
     out[6] = c.qlen;
     out[7] = c.kv;
-    out[8] = c.live ? t1 : 0;
+    out[8] = c.live ? end : 0;
     out[9] = per;
   }
 }
@@ -601,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_holder, kTmemCols);
     tmem_relinquish();
   } else if (warp == 2) {
-    schedule<DH>(p, reinterpret_cast<int*>(smem + L::kRingOff), start, blockIdx.x, gridDim.x);
+    schedule<DH>(p, reinterpret_cast<long long*>(smem + L::kRingOff), start, blockIdx.x,
+                 gridDim.x);
     fence_proxy_async_smem();  // the ring is the copies' from here on
   } else if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
@@ -644,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  const int t1 = start[8], per = start[9];
+  const int end = start[8], per = start[9];
   if (p.ppt > 0 && p.kt < kBN) {
     // nor any past a full tile's slots (their weights are zero, but 0 * NaN
     // is not)
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K/V that several query groups read stays in L2, the rest passes by
       const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
       Cursor cur;
-      cur.init(start, t1, p);
+      cur.init(start, end, p);
       // A tile's page ids (one per lane) are fetched a tile ahead: the read
       // would otherwise hold up the copies of every tile.
       auto page_id = [&](const Cursor& x) {
@@ -992,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int even_lt = p.ppt > 0 ? (p.kt == kBN ? INT_MAX : 0)
                                   : (p.page % kBN == 0 ? INT_MAX : p.page / kBN);
     Cursor cur;
-    cur.init(start, t1, p);
+    cur.init(start, end, p);
     int j0 = 0;  // tiles before the piece
     bool ok = true;
     while (ok && cur.live) {
@@ -1115,10 +1131,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid) finite = store_row32<DH>(out + ch * 32, o) && finite;
         }
       } else {
-        const int s0 = done.seg;
-        const int c0 = s0 / per;
-        const int n_pieces = (s0 + (done.ntiles - 1) * done.wt) / per - c0 + 1;
-        const size_t slot = piece_slot(blockIdx.x, per, s0);
+        // CTAs before this one that hold earlier pieces, and after it
+        const int back = done.seg < 0 ? (per - 1 - done.seg) / per : 0;
+        const int ahead = (done.seg + (done.ntiles - 1) * done.wt) / per;
+        const bool within = done.seg + back * per != 0;
+        const int c0 = blockIdx.x - back, n_pieces = back + ahead + 1;
+        const size_t slot = piece_slot(c0, back, within);
         const int row = m * kMT + rl;
         // Many rows in a warp: groups of 4 columns of all rows, so that its
         // lanes write 512 bytes side by side.  Few: whole rows, which the
@@ -1150,8 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == static_cast<unsigned int>(n_pieces - 1)) {
           __threadfence();
-          finite = merge_rows<DH>(p, out, mask, c0, n_pieces, per, s0,
-                                  row - lane) && finite;
+          finite = merge_rows<DH>(p, out, mask, c0, n_pieces, within, row - lane) && finite;
         }
       }
       tc_fence_before();
