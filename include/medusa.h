@@ -695,7 +695,8 @@ MEDUSA_API medusa_status_t medusa_rope(const medusa_rope_t* rope, const void* q,
  *   batch) are left as they are, in q_out too.  A row whose slot is negative
  *   (kv_len shorter than the chunk) is rotated but not written.
  * Device checks: a slot past max_pages pages, a page outside [0, n_pages)
- *   (that row is not written).
+ *   (that row is not written); a row in front of cu_q[0] (left, in q_out too);
+ *   cu_q decreasing, negative or above T (no row is written).
  * Limits: B >= 1, T >= 0, page_size, n_pages, max_pages >= 1; the rest as
  *   medusa_rope.
  * ---------------------------------------------------------------------- */

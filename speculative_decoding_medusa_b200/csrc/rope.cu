@@ -107,6 +107,12 @@ struct Row {
   long long dst;  // row of kv head 0 in the pools
 };
 
+// The sequences' ends have to ascend up to T: otherwise a row may be counted to
+// a sequence whose slots it has no business in, and no row is taken.
+__device__ __forceinline__ bool ascends(int first, int end, const RopeParams& p) {
+  return first >= 0 && end >= first && end <= p.T;
+}
+
 template <bool kAppend>
 __device__ __forceinline__ Row row_of(int t, const RopeParams& p) {
   Row r{0, 0, 0};
@@ -117,12 +123,22 @@ __device__ __forceinline__ Row row_of(int t, const RopeParams& p) {
   // the sequence of row t: how many sequences end at or before it
   const int lane = threadIdx.x & 31;
   int n = 0;
-  for (int b = lane; b < p.B; b += 32) n += p.cu_q[b + 1] <= t ? 1 : 0;
+  bool ok = true;
+  for (int b = lane; b < p.B; b += 32) {
+    const int end = p.cu_q[b + 1];
+    n += end <= t ? 1 : 0;
+    ok = ok && ascends(p.cu_q[b], end, p);
+  }
   n = __reduce_add_sync(0xffffffffu, n);
-  if (t < p.T && n < p.B) {
+  ok = __all_sync(0xffffffffu, ok);
+  if (ok && n < p.B) ok = t >= p.cu_q[n];  // (cu_q starts at 0)
+  if (!ok) {
+    if (lane == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    return r;
+  }
+  if (n < p.B) {
     r.state = 1;
-    const int first = p.cu_q[n];
-    const int slot = p.kv_len[n] - (p.cu_q[n + 1] - first) + (t - first);
+    const int slot = p.kv_len[n] - p.cu_q[n + 1] + t;
     r.pos = p.positions != nullptr ? p.positions[t] : slot;
     if (slot >= 0) {
       const int pg = slot / p.page_size;
@@ -272,8 +288,12 @@ __device__ __forceinline__ Row row_of_thread(uint32_t token, const int* cu, cons
     else hi = mid;
   }
   if (lo >= p.B) return r;
+  if (t < cu[lo]) {  // cu_q does not start at 0
+    report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+    return r;
+  }
   r.state = 1;
-  const int first = cu[lo], slot = kv[lo] - (cu[lo + 1] - first) + (t - first);
+  const int slot = kv[lo] - cu[lo + 1] + t;
   r.pos = p.positions != nullptr ? p.positions[t] : slot;
   if (slot >= 0) {
     const int pg = slot / p.page_size;
@@ -324,12 +344,21 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
   uint32_t t = blockIdx.x;
   if (works && t < n_tok) fetch<T, VEC>(u, t, p, a, b);
   const bool small = kAppend && p.B <= kSmallB;
-  if (small) {
-    for (int i = tid; i <= p.B; i += blockDim.x) {
-      s_cu[i] = p.cu_q[i];
-      if (i < p.B) s_kv[i] = p.kv_len[i];
+  if (kAppend) {
+    bool ok = true;
+    for (int i = tid; i < p.B; i += blockDim.x) {
+      const int first = p.cu_q[i], end = p.cu_q[i + 1];
+      ok = ok && ascends(first, end, p);
+      if (small) {
+        if (i == 0) s_cu[0] = first;
+        s_cu[i + 1] = end;
+        s_kv[i] = p.kv_len[i];
+      }
     }
-    __syncthreads();
+    if (!__syncthreads_and(ok)) {
+      if (blockIdx.x == 0 && tid == 0) report(p.status, MEDUSA_ERR_DEVICE_CHECK);
+      return;
+    }
   }
   int parity = 0;
   while (t < n_tok) {

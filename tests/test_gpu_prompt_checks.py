@@ -50,3 +50,41 @@ def test_good_lengths_around_them(dtype):
     assert status == 0
     assert bool((out[6:] == 5.0).all()) and bool(torch.isfinite(out[:6]).all())
     assert not bool((out[:6] == 5.0).any())
+
+
+@pytest.mark.parametrize("T,rot", [(8, 128), (3000, 128), (8, 34)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_refuses_lengths_out_of_order(dtype, T, rot):
+    """Rows in front of their sequence or behind its end would reach slots of
+    older tokens.  A block per row (8), resident blocks (3000) and a rotation
+    that vectors do not divide."""
+    Hq, Hkv, dh, page = (16, 4, 128, 16) if dtype is torch.bfloat16 else (8, 2, 128, 16)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    normal = lambda H: torch.randn(T, H, dh, generator=g, device=DEV).to(dtype)
+    q, k, v = normal(Hq), normal(Hkv), normal(Hkv)
+    r = M.Rope(rot)
+    n = T // page + 40
+
+    def append(cu, kv):
+        B = len(kv)
+        K, V = torch.full((2, n, Hkv, page, dh), 2.5, dtype=dtype, device=DEV)
+        table = (torch.arange(B * n, **i32) % n).view(B, n)
+        qo, st = torch.full_like(q, 5.0), M.new_status()
+        M.medusa_rope_append(r, q, k, v, torch.tensor(cu, **i32), torch.tensor(kv, **i32), qo,
+                             M.PagedCache(K, V, table), dev_status=st)
+        torch.cuda.synchronize()
+        return K, V, qo, int(st.item())
+
+    for cu in ([0, 5, 3, T], [0, T - 2, 0], [0, T, T + 1], [0, -1, T], [0] + [T] * 40 + [T - 1],
+               [0] + [T] * 300 + [1]):
+        K, V, qo, status = append(cu, [T + 100] * (len(cu) - 1))
+        assert status == 6, cu
+        assert bool((K == 2.5).all()) and bool((V == 2.5).all()) and bool((qo == 5.0).all()), cu
+    # not from 0: the rows in front are reported and left, the others written
+    K, V, qo, status = append([2, T], [T + 100])
+    assert status == 6
+    assert bool((qo[:2] == 5.0).all()) and bool((qo[2:] != 5.0).any(-1).all())
+    flat = V.transpose(1, 2).reshape(-1, Hkv, dh)  # slots in order
+    first = T + 100 - (T - 2)
+    assert bool((flat[:first] == 2.5).all()) and torch.equal(flat[first:T + 100], v[2:])
+    assert bool((flat[T + 100:] == 2.5).all())
