@@ -25,12 +25,16 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t x) {
 // ----------------------------------------------------------------------------
 // Programmatic dependent launch.  Every kernel of the library is launched with
 // programmatic stream serialisation, so it can be made resident while its
-// predecessor in the stream drains.  Its first statement is grid_dep_wait():
-// nothing (no global access, no tensor-memory allocation) happens before the
-// predecessor grid has completed and its memory is visible, so the overlap
-// hides only the launch and the rasterisation of the grid.  grid_dep_launch()
-// lets this grid's own dependents be launched early.  Both are no-ops for a
-// kernel launched without the attribute.
+// predecessor in the stream drains.  grid_dep_wait() returns once the
+// predecessor grid has completed and its memory is visible.  Nearly every
+// kernel begins with it: nothing (no global access, no tensor-memory
+// allocation) happens before, and the overlap hides only the launch and the
+// rasterisation of the grid.  Three begin earlier and say so in their place:
+// sampling prepares tables in shared memory; tree and chunk attention follow a
+// kernel of their own that zeroes counters and has itself waited for every
+// earlier grid, so their inputs are final, and only what touches the counters
+// or the results waits.  grid_dep_launch() lets this grid's own dependents be
+// launched early.  Both are no-ops for a kernel launched without the attribute.
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -739,7 +739,9 @@ medusa_status_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const Ge
   auto kern = heads_gemm_kernel<NB, S, MODE>;
   const size_t smem =
       L::kAlloc + (p.run_lists ? (size_t)p.n_heads * p.B * kRunRowBytes : (size_t)0);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+  // (the limit, not this call's size: the setting is the process's, and another
+  // thread's smaller call must not lower it before this one's launch)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
       cudaSuccess)
     return fail(MEDUSA_ERR_CUDA, "cudaFuncSetAttribute(heads_gemm) failed");
   launch(kern, gemm_grid(p), kGemmThreads, smem, stream, a, b, p);

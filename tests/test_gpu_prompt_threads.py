@@ -57,6 +57,30 @@ def test_vocabularies_of_different_sizes(dtype):
         assert torch.equal(tok, first)
 
 
+def test_heads_of_different_batches():
+    """The same of the heads, whose running lists follow the batch."""
+    d, V, K, kmax = 64, 2000, 4, 4
+    works, checks = [], []
+    g = torch.Generator(device=DEV).manual_seed(3)
+    W1 = (torch.randn(K, d, d, generator=g, device=DEV) / 8).bfloat16()
+    b1 = torch.randn(K, d, generator=g, device=DEV).bfloat16()
+    W2 = torch.randn(K, V, d, generator=g, device=DEV).bfloat16()
+    for B in (8, 1, 8, 2):
+        h = torch.randn(B, d, generator=g, device=DEV).bfloat16()
+        ids, first = torch.zeros(2, B, K, kmax, dtype=torch.int32, device=DEV)
+        vals = torch.zeros(B, K, kmax, device=DEV)
+        ws = M.workspace(M.medusa_heads_topk_workspace_size(B, d, V, K, kmax, M.MEDUSA_BF16))
+        M.medusa_heads_topk(h, W1, b1, W2, kmax, first, vals, ws=ws)
+        s = torch.cuda.Stream()
+        works.append(lambda h=h, ids=ids, vals=vals, ws=ws, s=s: M.medusa_heads_topk(
+            h, W1, b1, W2, kmax, ids, vals, ws=ws, stream=s))
+        checks.append((ids, first))
+    torch.cuda.synchronize()
+    assert _together(works, 1000) == []
+    for ids, first in checks:
+        assert torch.equal(ids, first)
+
+
 def test_the_first_call_of_a_thread():
     """A host thread that has made no CUDA call yet."""
     g = torch.Generator(device=DEV).manual_seed(6)
