@@ -85,6 +85,16 @@ int count(int64_t n) {
   return static_cast<int>(n);
 }
 
+// The C call itself runs without the interpreter's lock, as through ctypes: a
+// launch waits where the stream's queue is full, and other threads go on.
+template <typename F>
+int unlocked(F&& call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int st = static_cast<int>(call());
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 
 template <typename F>
@@ -140,9 +150,13 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     on(tensor(a[1]), dev);
     const int inverse = PyObject_IsTrue(a[7]);
     need(inverse >= 0);
-    return (int)g_rope(static_cast<const medusa_rope_t*>(address(a[0])), qr.p, qr.stride, kr.p,
-                       kr.stride, dt, pos, count(T), count(Hq), count(Hkv), count(dh), inverse,
-                       qo.p, qo.stride, ko.p, ko.stride, stream_of(dev));
+    const auto* r = static_cast<const medusa_rope_t*>(address(a[0]));
+    const int t = count(T), hq = count(Hq), hkv = count(Hkv), d = count(dh);
+    void* const stream = stream_of(dev);
+    return unlocked([&] {
+      return g_rope(r, qr.p, qr.stride, kr.p, kr.stride, dt, pos, t, hq, hkv, d, inverse, qo.p,
+                    qo.stride, ko.p, ko.stride, stream);
+    });
   });
 }
 
@@ -168,13 +182,18 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       qo = rows(a[7], type, T, Hq, dh, dev);
     }
     if (a[0] != Py_None) on(tensor(a[1]), dev);
-    return (int)g_append(
-        static_cast<const medusa_rope_t*>(address(a[0])), qr.p, qr.stride, kr.p, kr.stride, vr.p,
-        vr.stride, dt, static_cast<const int32_t*>(vec(a[11], at::kInt, T, dev)),
-        static_cast<const int32_t*>(vec(a[5], at::kInt, B + 1, dev)),
-        static_cast<const int32_t*>(vec(a[6], at::kInt, B, dev)), count(B), count(T), count(Hq),
-        count(Hkv), count(dh), qo.p, qo.stride, static_cast<const medusa_pages_t*>(address(a[8])),
-        static_cast<int32_t*>(vec(a[12], at::kInt, 1, dev)), stream_of(dev));
+    const auto* r = static_cast<const medusa_rope_t*>(address(a[0]));
+    const auto* pages = static_cast<const medusa_pages_t*>(address(a[8]));
+    const auto* pos = static_cast<const int32_t*>(vec(a[11], at::kInt, T, dev));
+    const auto* cu = static_cast<const int32_t*>(vec(a[5], at::kInt, B + 1, dev));
+    const auto* kv = static_cast<const int32_t*>(vec(a[6], at::kInt, B, dev));
+    auto* status = static_cast<int32_t*>(vec(a[12], at::kInt, 1, dev));
+    const int nb = count(B), t = count(T), hq = count(Hq), hkv = count(Hkv), d = count(dh);
+    void* const stream = stream_of(dev);
+    return unlocked([&] {
+      return g_append(r, qr.p, qr.stride, kr.p, kr.stride, vr.p, vr.stride, dt, pos, cu, kv, nb, t,
+                      hq, hkv, d, qo.p, qo.stride, pages, status, stream);
+    });
   });
 }
 
@@ -195,12 +214,17 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(!PyErr_Occurred());
     const int64_t bytes = tensor(a[8]).numel();
     void* ws = vec(a[8], at::kByte, bytes, dev);
-    return (int)g_attention(qr.p, qr.stride, static_cast<const medusa_pages_t*>(address(a[1])), dt,
-                            static_cast<const int32_t*>(vec(a[3], at::kInt, B + 1, dev)),
-                            static_cast<const int32_t*>(vec(a[4], at::kInt, B, dev)), count(B),
-                            count(T), count(Hq), count(K.size(1)), count(dh),
-                            static_cast<float>(scale), out.p, ws, static_cast<size_t>(bytes),
-                            static_cast<int32_t*>(vec(a[9], at::kInt, 1, dev)), stream_of(dev));
+    const auto* pages = static_cast<const medusa_pages_t*>(address(a[1]));
+    const auto* cu = static_cast<const int32_t*>(vec(a[3], at::kInt, B + 1, dev));
+    const auto* kv = static_cast<const int32_t*>(vec(a[4], at::kInt, B, dev));
+    auto* status = static_cast<int32_t*>(vec(a[9], at::kInt, 1, dev));
+    const int nb = count(B), t = count(T), hq = count(Hq), hkv = count(K.size(1)), d = count(dh);
+    void* const stream = stream_of(dev);
+    return unlocked([&] {
+      return g_attention(qr.p, qr.stride, pages, dt, cu, kv, nb, t, hq, hkv, d,
+                         static_cast<float>(scale), out.p, ws, static_cast<size_t>(bytes), status,
+                         stream);
+    });
   });
 }
 
@@ -216,10 +240,18 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(a[2] != Py_None);
     auto f32 = [&](int i) { return static_cast<const float*>(vec(a[i], at::kFloat, R, dev)); };
     auto i32 = [&](int i) { return static_cast<int32_t*>(vec(a[i], at::kInt, R, dev)); };
-    return (int)g_sample(z.data_ptr(), dt, rows > 1 ? z.stride(0) : V, count(rows), i32(7),
-                         count(R), count(V), f32(1), f32(3), i32(4), f32(5), f32(6), i32(2),
-                         i32(8), static_cast<int32_t*>(vec(a[9], at::kInt, 1, dev)),
-                         stream_of(dev));
+    const float *u = f32(1), *temperature = f32(3), *top_p = f32(5), *min_p = f32(6);
+    const int32_t *row_idx = i32(7), *top_k = i32(4);
+    int32_t *tokens = i32(2), *kept = i32(8);
+    auto* status = static_cast<int32_t*>(vec(a[9], at::kInt, 1, dev));
+    const int n_rows = count(rows), r = count(R), v = count(V);
+    const void* logits = z.data_ptr();
+    const long long stride = rows > 1 ? z.stride(0) : V;
+    void* const stream = stream_of(dev);
+    return unlocked([&] {
+      return g_sample(logits, dt, stride, n_rows, row_idx, r, v, u, temperature, top_k, top_p,
+                      min_p, tokens, kept, status, stream);
+    });
   });
 }
 

@@ -1,10 +1,13 @@
 """GPU: calls of different sizes from several host threads at once."""
+import ctypes
 import threading
+import time
 
 import pytest
 import torch
 
 import speculative_decoding_medusa_b200 as M
+from speculative_decoding_medusa_b200 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +112,34 @@ def test_the_first_call_of_a_thread():
     torch.cuda.synchronize()
     assert errors == []
     assert torch.equal(out, first)
+
+
+def test_other_threads_run_during_a_call():
+    """The extension's C call with the library's functions replaced by one that
+    sleeps (its first argument, the address of the rotation, as microseconds):
+    another thread counts meanwhile."""
+    m, L = _lib._marshal(), M.lib()
+    q = torch.zeros(4, 2, 64, device=DEV)
+    pos = torch.zeros(4, dtype=torch.int32, device=DEV)
+    own = [ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.medusa_rope, L.medusa_rope_append, L.medusa_chunk_attention, L.medusa_sample_tokens)]
+    sleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    count, stop = [0], threading.Event()
+
+    def body():
+        while not stop.is_set():
+            count[0] += 1
+            time.sleep(0.001)
+
+    t = threading.Thread(target=body)
+    t.start()
+    try:
+        m.bind(sleep, *own[1:])
+        before = count[0]
+        assert m.rope(300000, q, q, None, pos, q, None, False) == 0
+        during = count[0] - before
+    finally:
+        m.bind(*own)
+        stop.set()
+        t.join()
+    assert during > 20
