@@ -586,7 +586,18 @@ def _3d(t: torch.Tensor, name: str):
     return sh
 
 
-class Rope:
+class _Fixed:
+    """Attributes are set once: the C struct holds their addresses and sizes, and
+    would not follow a new value."""
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new "
+                                 f"{type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
+class Rope(_Fixed):
     """A rotation of the first ``rot`` elements of each head: the frequencies
     theta^(-2i/rot) under a long-context scaling ("none", "linear", "llama3",
     "yarn"), in pairs (i, i + rot/2), or (2i, 2i + 1) when interleaved.
@@ -618,9 +629,10 @@ class Rope:
         self._ref = ctypes.addressof(self._c)
 
 
-class PagedCache:
+class PagedCache(_Fixed):
     """K and V pools [n_pages, Hkv, page_size, dh] and the page table
-    [B, max_pages] int32 of the sequences that use them."""
+    [B, max_pages] int32 of the sequences that use them.  Their contents change
+    in place; for other tensors make another PagedCache."""
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor):
         _req(K, "K")

@@ -5,6 +5,10 @@ import subprocess
 import sys
 
 import pytest
+import torch
+
+import speculative_decoding_medusa_b200 as M
+from speculative_decoding_medusa_b200 import _lib
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -32,3 +36,20 @@ def test_chunk_attention_shapes(dt, kw):
     code = CALL.format(**{**dict(n=4, page=16, dt=dt, dh=128, hkv=2), **kw})
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert (r.returncode, r.stdout.strip()) == (0, "2"), r.stderr
+
+
+def test_a_rotation_and_a_cache_keep_their_tensors(monkeypatch):
+    """The C structs hold the tensors' addresses: a new tensor would be taken
+    for the old one's memory, so it is refused."""
+    r = M.Rope(64, device="cpu")
+    for name, value in (("turns", r.turns.clone()), ("scale", 2.0), ("rot", 32),
+                        ("interleaved", True)):
+        with pytest.raises(AttributeError, match="fixed"):
+            setattr(r, name, value)
+    monkeypatch.setattr(_lib, "_req", lambda t, name: None)
+    cache = M.PagedCache.dense(torch.zeros(2, 1, 8, 64), torch.zeros(2, 1, 8, 64))
+    for name in ("K", "V", "table"):
+        with pytest.raises(AttributeError, match="make a new PagedCache"):
+            setattr(cache, name, getattr(cache, name).clone())
+    cache.table.fill_(1)  # contents are the caller's
+    assert cache._c.table == cache.table.data_ptr() and cache._c.K == cache.K.data_ptr()
