@@ -105,6 +105,7 @@ struct TcParams {
   int n_pages, page, max_pages;
   int ppt;  // pages per tile (0: pages of 128 or more, tpp tiles each)
   int tpp, kt;  // kt: slots of a full tile
+  int max_kv;   // slots of the table's pages, and of no more than kMaxTiles tiles
   int B, T, Hq, Hkv, G, tpt;  // tpt: tokens per M tile
   int q_box;                  // tokens per copy of Q
   float scale_log2;
@@ -464,7 +465,7 @@ __device__ __forceinline__ void schedule(const TcParams& p, long long* cum, int*
       kv = p.kv_len[b];
       qlen = a1 - q0;
       ok = ok && q0 >= 0 && a1 >= q0 && a1 <= p.T && kv >= 0 &&
-           kv <= (long long)p.max_pages * p.page && tiles_of(kv, p) <= kMaxTiles;
+           kv <= p.max_kv;
     }
     if (!__all_sync(0xffffffffu, ok)) break;
     const int n_qg = (qlen + 2 * p.tpt - 1) / (2 * p.tpt);
@@ -1211,6 +1212,12 @@ medusa_status_t launch_tc(const ChunkParams& c, void* ws, cudaStream_t stream) {
     p.tpp = 1;
     p.kt = p.ppt * c.page_size;
   }
+  // (tiles a page: tpp; or ppt pages a tile)
+  const long long slots = (long long)c.max_pages * c.page_size;
+  const long long most = p.ppt > 0 ? (long long)kMaxTiles * p.kt
+                                   : (long long)(kMaxTiles / p.tpp) * c.page_size;
+  const long long bound = slots < most ? slots : most;
+  p.max_kv = bound < INT_MAX ? static_cast<int>(bound) : INT_MAX;
   p.B = c.B;
   p.T = c.T;
   p.Hq = c.Hq;
