@@ -34,22 +34,26 @@
 //               independent chains instead of one; the first warpgroup adds
 //               the second's O to its own where the piece ends.
 //
-// Roundings to fewer bits than fp32: P to bf16, the product's operand type
-// (relative 2^-8 of each probability, while the sum l is of the fp32 values);
-// O to bf16 once, at the end.  Scores, maxima, sums, O and the pieces are fp32.
+// Roundings to fewer bits than fp32: P to bf16, for both operands of a product
+// have one type and V is bf16 (relative 2^-8 of each probability, while the sum
+// l is of the fp32 values); O to bf16 once, at the end.  Scores, maxima, sums, O
+// and the pieces are fp32.
 //
 // What bounds it, with what it measured (one B200; 6.55 TB/s copy and 1.66
 // PFLOP/s bf16 products in a burst, 1.36 sustained):
 //   prompts         the chain scores -> maximum -> exponentials -> P of a tile
 //                   and, in long runs, the power limit.  8192 tokens, 32 + 8
-//                   heads of 128: 480 us, 1.14 PFLOP/s.
+//                   heads of 128: 485 us a call in a run of 100 (1.13
+//                   PFLOP/s), 545 to 560 in runs of a thousand (0.98).
 //   short chunks    the same, with M tiles partly empty and segments of a few
 //                   tiles: 12 sequences of 1 to 600 tokens that end at 601 to
-//                   6000 slots, pages of 16: 163 to 177 us.
-//   single tokens   HBM: 32 sequences of 30001 to 32768 slots 600 us, 6.9
-//                   TB/s (676 in long runs, under the power limit); eight of
-//                   4096 to 8192 45 us, of which the prologue, the merge and
-//                   the launch are a third; one of 6000, all latency, 18.7 us.
+//                   6000 slots, pages of 16: 157 us in a run of 100, 170 to
+//                   183 in long ones.
+//   single tokens   HBM: 32 sequences of 30001 to 32768 slots 605 us, 6.8
+//                   TB/s (660 to 680 in long runs, under the power limit);
+//                   eight of 4096 to 8192 47 us, of which the prologue, the
+//                   merge and the launch are a third; one of 6000, all
+//                   latency, 19.3 us.
 // Tried and slower: tiles of 64 keys with two score buffers a warpgroup (848 us
 // where tiles of 128 took 565); some of the exponentials as a polynomial on the
 // FMA units (every fourth pair: prompt 498 us, every eighth: 490, none: 480);

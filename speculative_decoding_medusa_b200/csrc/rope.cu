@@ -311,11 +311,13 @@ __device__ __forceinline__ Row row_of_thread(uint32_t token, const int* cu, cons
 // Many tokens, a thread per unit: resident blocks walk the tokens in chunks of
 // kChunk, whose metadata they find at once, with the next token's data and
 // angles on their way while they finish the current one; one barrier a token.
-// 8192 tokens of 32 + 8 heads written into pages (214 MB): 46.5 us
+// 8192 tokens of 32 + 8 heads written into pages (214 MB): 46.3 us
 // (4.6 TB/s of the 6.55 that a copy reaches; 33 us at that), against
 // 60 us with a block per token, whose latencies only other blocks cover, and
 // 54 us with each token's metadata found two tokens ahead (its chain of three
-// reads was as long as a token's turn).
+// reads was as long as a token's turn).  A token of more units than a block has
+// threads (64 + 8 or 32 + 32 heads of 128 in bf16, 32 + 8 in fp32) takes a block
+// of its own: 80, 90 and 76 us for 8192 of them (4.5, 4.7 and 5.7 TB/s).
 template <typename T, int VEC, bool kInter, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p) {
   grid_dep_wait();
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_pipe_kernel(RopeParams p
 // in rot = 34): a block per token holds the token's q, k and v in shared memory,
 // read and written by whole vectors whatever the rotation, and every element
 // finds its partner there.  8192 tokens of 32 + 8 heads of 128 with rot = 34
-// written into pages: 79 us, with vectors as narrow as the pairs allow 154.
+// written into pages: 81 us, with vectors as narrow as the pairs allow 154.
 template <typename T, int VEC, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_staged_kernel(RopeParams p) {
   grid_dep_wait();
