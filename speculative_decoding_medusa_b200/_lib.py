@@ -587,11 +587,13 @@ def _3d(t: torch.Tensor, name: str):
 
 
 class _Fixed:
-    """Attributes are set once: the C struct holds their addresses and sizes, and
-    would not follow a new value."""
+    """The attributes named in _held are set once: the C struct has their
+    addresses and sizes, and would not follow a new value."""
+
+    _held = frozenset()
 
     def __setattr__(self, name, value):
-        if "_ref" in self.__dict__:
+        if name in self._held and name in self.__dict__:
             raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new "
                                  f"{type(self).__name__}")
         object.__setattr__(self, name, value)
@@ -604,6 +606,8 @@ class Rope(_Fixed):
 
     ``low_freq_factor`` and ``high_freq_factor`` are full turns over
     ``original_max_position`` (llama3: 1 and 4, yarn: 1 and 32 by default)."""
+
+    _held = frozenset(("rot", "interleaved", "scale", "turns", "_c", "_ref"))
 
     def __init__(self, rot: int, *, theta: float = 10000.0, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0,
@@ -633,6 +637,9 @@ class PagedCache(_Fixed):
     """K and V pools [n_pages, Hkv, page_size, dh] and the page table
     [B, max_pages] int32 of the sequences that use them.  Their contents change
     in place; for other tensors make another PagedCache."""
+
+    _held = frozenset(("K", "V", "table", "dt", "B", "n_pages", "Hkv", "page_size", "dh",
+                       "_device", "_c", "_ref"))
 
     def __init__(self, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor):
         _req(K, "K")

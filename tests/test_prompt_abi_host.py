@@ -51,5 +51,7 @@ def test_a_rotation_and_a_cache_keep_their_tensors(monkeypatch):
     for name in ("K", "V", "table"):
         with pytest.raises(AttributeError, match="make a new PagedCache"):
             setattr(cache, name, getattr(cache, name).clone())
+    cache.name = "mine"  # and what the caller adds
+    cache.name = "yours"
     cache.table.fill_(1)  # contents are the caller's
     assert cache._c.table == cache.table.data_ptr() and cache._c.K == cache.K.data_ptr()
