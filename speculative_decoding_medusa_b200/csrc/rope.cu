@@ -138,9 +138,10 @@ __device__ __forceinline__ Row row_of(int t, const RopeParams& p) {
   }
   if (n < p.B) {
     r.state = 1;
-    const int slot = p.kv_len[n] - p.cu_q[n + 1] + t;
+    const long long at = (long long)p.kv_len[n] - p.cu_q[n + 1] + t;
+    const int slot = static_cast<int>(at);
     r.pos = p.positions != nullptr ? p.positions[t] : slot;
-    if (slot >= 0) {
+    if (at >= 0) {
       const int pg = slot / p.page_size;
       const int id = pg < p.max_pages ? p.table[(size_t)n * p.max_pages + pg] : -1;
       if (id >= 0 && id < p.n_pages) {
@@ -293,9 +294,10 @@ __device__ __forceinline__ Row row_of_thread(uint32_t token, const int* cu, cons
     return r;
   }
   r.state = 1;
-  const int slot = kv[lo] - cu[lo + 1] + t;
+  const long long at = (long long)kv[lo] - cu[lo + 1] + t;
+  const int slot = static_cast<int>(at);
   r.pos = p.positions != nullptr ? p.positions[t] : slot;
-  if (slot >= 0) {
+  if (at >= 0) {
     const int pg = slot / p.page_size;
     const int id = pg < p.max_pages ? p.table[(size_t)lo * p.max_pages + pg] : -1;
     if (id >= 0 && id < p.n_pages) {

@@ -88,3 +88,19 @@ def test_append_refuses_lengths_out_of_order(dtype, T, rot):
     first = T + 100 - (T - 2)
     assert bool((flat[:first] == 2.5).all()) and torch.equal(flat[first:T + 100], v[2:])
     assert bool((flat[T + 100:] == 2.5).all())
+
+
+@pytest.mark.parametrize("T", [8, 3000])
+def test_append_with_the_lowest_length(T):
+    """Slots below -2^31: none of the rows has one, which is no error."""
+    Hkv, dh, page = 8, 128, 16
+    k = torch.randn(T, Hkv, dh, generator=torch.Generator(device=DEV).manual_seed(T),
+                    device=DEV).bfloat16()
+    K, V = torch.full((2, 4, Hkv, page, dh), 2.5, dtype=torch.bfloat16, device=DEV)
+    st = M.new_status()
+    M.medusa_rope_append(None, None, k, k, torch.tensor([0, T], **i32),
+                         torch.tensor([-2 ** 31 + 3], **i32), None,
+                         M.PagedCache(K, V, torch.arange(4, **i32).view(1, 4)), dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert bool((K == 2.5).all()) and bool((V == 2.5).all())
