@@ -40,10 +40,10 @@
 // with a pass between them, many rows by the same chain two blocks at a time
 // on an SM and by the shared-memory atomics of the count (about six cycles a
 // warp's; computing the bins with half the instructions changed nothing).  One
-// row of 32000 (fp32, top-k and top-p) 12 to 15 us; 8 rows of 128256 (bf16,
-// top-p) 16.7 us; 512 of them with settings of their own 156 us, 0.84 TB/s.  With the
-// weights of all tokens added into bins, as in fp32, the bf16 rows took 44 and
-// 269 us.
+// row of 32000 (fp32, top-k and top-p) 12 to 18 us, as its list serves at once
+// or not; 8 rows of 128256 (bf16, top-p) 16.7 us; 512 of them with settings of
+// their own 156 us, 0.84 TB/s.  With the weights of all tokens added into bins,
+// as in fp32, the bf16 rows took 44 and 269 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
